@@ -248,6 +248,151 @@ int sgp_router_topk_noalloc(const sgp_dims* dims, const void* h, const void* g_m
                             const void* w_router, const float* router_bias, int n_tokens,
                             void* u_out, int32_t* topk_idx, float* topk_w, sgp_stream_t stream);
 
+/* ---- serving operators beside the layer ----------------------------------------------
+ * Operators of a decode step that serves many requests: attention over prompts that requests
+ * share, caches held to a budget, adapters of many tenants.  The paper has no counterpart.
+ *
+ * Common to all of them:
+ *   - up to 512 sequences per call; asynchronous on `stream`; nothing is allocated and no state
+ *     is kept between calls, so a call can be captured into a CUDA graph (make one call of the
+ *     kind before the capture: the first one on a device sets kernel attributes).
+ *   - The workspace is the caller's, 256-byte aligned.  Its first 64 bytes are the status word,
+ *     which sgp_status_from_workspace reads and clears (op 16 prefix attention, 17 attention
+ *     weights, 18 eviction, 19 adapters); zero them once before the first use.  The rest needs
+ *     no initialisation.  Calls that may run at the same time (two streams, two graphs, a graph
+ *     and a stream) need a workspace each; calls ordered on the GPU may share one.
+ *   - Device arrays of lengths and indices are checked on the device: what is out of range is
+ *     recorded as SGP_ERR_DEVICE_BOUNDS and treated as each entry point says, never followed.
+ *   - Every pointer must be accessible from the current device.
+ *   - Of sgp_dims only n_q_heads, n_kv_heads and head_dim are read; of sgp_layer, here a cache,
+ *     only k_cache, v_cache, kv_cap and window.                                             */
+
+/* Prefixes that sequences share (device pointers, caller-owned).
+ *   k, v       bf16 [n_prefixes][n_kv][cap][d]; n_prefixes * n_kv * cap < 2^31
+ *   len        int32 [n_prefixes], 0 <= len <= cap
+ *   prefix_of  int32 [n_tokens]: the prefix of a sequence, negative: none.  Sequences of one
+ *              prefix may stand anywhere in the batch.
+ * n_prefixes is at most 512; with 0 the other fields are not read. */
+typedef struct sgp_prefix {
+    const void* k;
+    const void* v;
+    const int32_t* len;
+    const int32_t* prefix_of;
+    int n_prefixes;
+    int cap;
+} sgp_prefix;
+
+/* Bytes of workspace sgp_prefix_attention needs.  Returns 0 on invalid arguments. */
+size_t sgp_prefix_attention_workspace_bytes(const sgp_dims* dims, int n_tokens, int kv_cap,
+                                            int n_prefixes);
+
+/* Decode attention (as SGP_OP_ATTENTION) over a shared prefix and the sequence's own cache:
+ * sequence b attends to the len[prefix_of[b]] positions of its prefix, then to the kv_len[b]
+ * positions of its own cache, which the caller has filled (the current token's included).  A
+ * prefix is read once for all its sequences.  With cache->window = W > 0 a sequence sees the
+ * last W of its positions, own and prefix counted together.
+ *   cache   own caches, bf16 [n_tokens][n_kv][kv_cap][d]; read only
+ *   prefix  NULL: no sequence has a prefix
+ *   kv_len  device int32 [n_tokens], 0 <= kv_len[b] <= kv_cap (out of range: taken as 0)
+ *   q, o    device bf16 [n_tokens][n_q d]; o may equal q
+ *   lse     device fp32 [n_tokens][n_q] or NULL: log of the sum of exp(q.k / sqrt(d)) (natural)
+ * A sequence that sees no position gets o = 0 and lse = -inf.  A prefix index past n_prefixes
+ * counts as none, a prefix length out of range as 0.  What caches hold behind their lengths is
+ * not looked at (it may be NaN).
+ * Returns SGP_OK, SGP_ERR_INVALID_ARG, SGP_ERR_UNSUPPORTED or SGP_ERR_CUDA. */
+int sgp_prefix_attention(const sgp_dims* dims, const sgp_layer* cache, const sgp_prefix* prefix,
+                         const int32_t* kv_len, const void* q, void* o, float* lse, int n_tokens,
+                         void* workspace, size_t ws_bytes, sgp_stream_t stream);
+
+/* Adds one step's attention weights of the own cached positions:
+ *   acc[b][j][p] += sum over the query heads h of KV head j of exp(q_h.k_p / sqrt(d) - lse_h)
+ * for p < kv_len[b] (0 <= kv_len[b] <= kv_cap; out of range: nothing is added); acc behind kv_len
+ * is left as it is.
+ *   cache  only k_cache and kv_cap are read; window must be 0
+ *   lse    device fp32 [n_tokens][n_q], as sgp_prefix_attention writes it (the prefix's share of
+ *          the weight is then in it); a head with lse = -inf adds nothing
+ *   acc    device fp32 [n_tokens][n_kv][kv_cap]
+ *   workspace  64 bytes (the status word); any other operator's workspace serves
+ * Returns SGP_OK, SGP_ERR_INVALID_ARG or SGP_ERR_CUDA. */
+int sgp_attention_weights(const sgp_dims* dims, const sgp_layer* cache, const int32_t* kv_len,
+                          const void* q, const float* lse, float* acc, int n_tokens,
+                          void* workspace, size_t ws_bytes, sgp_stream_t stream);
+
+/* What an eviction keeps of a cache longer than `budget`: the first n_sink positions, the last
+ * n_recent ones, and of the others the budget - n_sink - n_recent with the largest accumulated
+ * weight (ties to the lower position; NaN ranks below every number).  0 <= n_sink, n_recent;
+ * n_sink + n_recent <= budget. */
+typedef struct sgp_evict {
+    int budget;
+    int n_sink;
+    int n_recent;
+} sgp_evict;
+
+/* Bytes of workspace sgp_kv_evict needs.  Returns 0 on invalid arguments. */
+size_t sgp_kv_evict_workspace_bytes(const sgp_dims* dims, int n_tokens, int budget);
+
+/* Evicts: moves the kept positions of every (sequence, KV head), K and V rows and acc, in their
+ * order to the front of the target cache, writes the new length min(kv_len, budget), and clears
+ * acc_out behind it (a new position starts at 0).  Every KV head keeps the same number, but its
+ * own positions.  K and V rows of the target behind the new length are left as they are.  Cached
+ * keys keep the rotation they were stored with.
+ *   from, to   caches of n_tokens sequences; `to` may be the same cache (k, v, acc and kv_cap all
+ *              the same: in place) or share no byte with `from`; its kv_cap >= budget
+ *   kv_len     device int32 [n_tokens], 0 <= kv_len[b] <= from->kv_cap (out of range: the
+ *              sequence is left as it is); kv_len_out device int32 [n_tokens], may equal kv_len
+ *   acc        device fp32 [n_tokens][n_kv][from->kv_cap]; acc_out [n_tokens][n_kv][to->kv_cap]
+ *   kept       device int32 [n_tokens][n_kv][budget] or NULL: the kept positions in order, -1
+ *              behind them
+ * Only n_kv_heads and head_dim of dims are read.  window is not read.
+ * Returns SGP_OK, SGP_ERR_INVALID_ARG or SGP_ERR_CUDA. */
+int sgp_kv_evict(const sgp_dims* dims, const sgp_layer* from, const sgp_layer* to,
+                 const sgp_evict* policy, const int32_t* kv_len, int32_t* kv_len_out,
+                 const float* acc, float* acc_out, int32_t* kept, int n_tokens, void* workspace,
+                 size_t ws_bytes, sgp_stream_t stream);
+
+/* Low-rank adapters of one projection (device pointers, caller-owned).
+ *   a      bf16 [n_adapters][max_rank][in]
+ *   b      bf16 [n_adapters][out][max_rank]
+ *   scale  fp32 [n_adapters] or NULL (1)
+ *   rank   int32 [n_adapters] or NULL (max_rank), 0 <= rank <= max_rank: only the first rank rows
+ *          of a and columns of b are the adapter's (the rest is not looked at)
+ * n_adapters <= 4096; in and out multiples of 32; max_rank a multiple of 8, 8 to 128. */
+typedef struct sgp_lora {
+    const void* a;
+    const void* b;
+    const float* scale;
+    const int32_t* rank;
+    int n_adapters;
+    int in;
+    int out;
+    int max_rank;
+} sgp_lora;
+
+/* Adds every sequence's adapter to the output of the projection they share:
+ *   y_out[t] = y_in[t] + scale_i B_i (A_i x[t]),  i = adapter_of[t].
+ *   adapter_of  device int32 [n_tokens], in any order; negative: none (y_out[t] = y_in[t]); an
+ *               index past n_adapters or a rank out of range is recorded and counts as none
+ *   x           device bf16 rows of `in`, ld_x elements apart
+ *   y_in,y_out  device bf16 rows of `out`, ld_y_in / ld_y_out elements apart; y_out may equal
+ *               y_in (same stride), else the buffers must not overlap; x and y_out must not either
+ *               Row strides are multiples of 8 elements.
+ *   workspace   64 bytes (the status word); any other operator's workspace serves
+ * Sums are fp32; the result is rounded once.
+ * Returns SGP_OK, SGP_ERR_INVALID_ARG or SGP_ERR_CUDA. */
+int sgp_lora_apply(const sgp_lora* lora, const int32_t* adapter_of, const void* x, int64_t ld_x,
+                   const void* y_in, int64_t ld_y_in, void* y_out, int64_t ld_y_out, int n_tokens,
+                   void* workspace, size_t ws_bytes, sgp_stream_t stream);
+
+/* Where sgp_layer_op keeps a layer's batch-wide activations in its workspace: fills
+ * view->a, q, o, h, u (bf16, as sgp_layer_dump documents them) and sets the other fields to
+ * NULL.  With it the operators above take part in a layer run op by op: adapters on q between
+ * SGP_OP_QKV and SGP_OP_ATTENTION (without RoPE: q is already rotated there) or on h after
+ * SGP_OP_OPROJ, and sgp_prefix_attention in the place of SGP_OP_ATTENTION (q to o).  The
+ * workspace's status word is the layer's.  Host only; arguments as sgp_workspace_bytes.
+ * Returns SGP_OK or SGP_ERR_INVALID_ARG. */
+int sgp_workspace_views(const sgp_dims* dims, int n_tokens, int max_kv_len, void* workspace,
+                        size_t ws_bytes, sgp_layer_dump* view);
+
 /* ---- spatial pipeline (Section 3: cut, binding, SM allocation, microbatches) -------- */
 typedef struct sgp_pipeline sgp_pipeline;
 

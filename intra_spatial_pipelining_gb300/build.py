@@ -20,7 +20,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libsgp.so")
 
-SOURCES = ["runtime.cu", "k_gemm.cu", "k_attention.cu", "k_small.cu"]
+SOURCES = ["runtime.cu", "serving.cu", "k_gemm.cu", "k_attention.cu", "k_prefix.cu", "k_cache.cu",
+           "k_lora.cu", "k_small.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

@@ -37,6 +37,7 @@
 // ("Starscream: Reimagining LLM Sharding on AMD Instinct GPUs with GPU Partitioning",
 // sequence-length-sharded attention).
 #include "kernels.h"
+#include "mma.cuh"
 
 namespace sgp {
 
@@ -50,36 +51,6 @@ namespace {
 //    6 x 128: larger TMA boxes -- faster on the full GPU when chunks per warp are few.
 constexpr int kAMaxRows = 512;               // sequences per launch (prefix table size)
 constexpr int kAPerLane = kAMaxRows / 32;    // sequences per lane of the prefix scan
-
-__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
-}
-__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
-}
-__device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
-    uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
-}
-// D(16x8, fp32) += A(16x16, bf16, row) * B(16x8, bf16, col)
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// byte offset of 16-byte chunk `ch` of row `r` in a 128-byte-swizzled tile
-__device__ __forceinline__ uint32_t sw128(int r, int ch) {
-    return (uint32_t)(r * 128 + ((ch ^ (r & 7)) << 4));
-}
 
 // Where a warp stands in its share of the chunk list.
 struct Cursor {
@@ -166,7 +137,11 @@ __device__ void merge_pair(const AttnProblem& P, int t, int kvh, int S_t, int la
     }
 }
 
-template <int NT, int NW, int POS, bool SPLIT>
+// PART: the own-cache part of an attention over a shared prefix and an own cache.  Lengths of
+// zero are legal and every chunk leaves its partial: the merge with the prefix's partials is
+// another kernel's (k_prefix.cu).  (A window reaches L - window back in the own cache whatever
+// lies before it.)
+template <int NT, int NW, int POS, bool SPLIT, bool PART>
 __global__ void __launch_bounds__(NW * 32, 1)
     attn_decode_kernel(const __grid_constant__ AttnProblem P, const KCtx ctx) {
     constexpr int kAWarps = NW;                    // streaming warps per CTA
@@ -197,7 +172,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
             if (t < P.nrows) {
                 const int L = P.kv_len[P.row0 + t];
                 kvl[t] = L;
-                if (L < 1 || L > P.cap) {
+                if (L < (PART ? 0 : 1) || L > P.cap) {
                     if (blockIdx.x == 0) report(ctx, ST_BOUNDS, (uint32_t)L);
                 } else {
                     const int first = P.window > 0 ? max(0, L - P.window) : 0;
@@ -455,7 +430,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
                     l_run[nt][1] += __shfl_xor_sync(0xffffffffu, l_run[nt][1], o);
                 }
             const size_t pair = (size_t)cs.t * P.nkv + cs.kvh;
-            if (cs.S_t == 1) {
+            if (!PART && cs.S_t == 1) {
                 bf16* o = P.o + (size_t)(P.row0 + cs.t) * (P.nq * 64) + (size_t)(cs.kvh * P.G) * 64;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -492,17 +467,19 @@ __global__ void __launch_bounds__(NW * 32, 1)
                         *reinterpret_cast<float4*>(pml + 2 * h) =
                             make_float4(m_run[nt][0], l_run[nt][0], m_run[nt][1], l_run[nt][1]);
                 }
-                __threadfence();
-                __syncwarp();
-                int last = 0;
-                if (lane == 0) {
-                    const uint32_t prev = atomicAdd(&P.cnt[pair], 1u);
-                    last = prev == (uint32_t)cs.S_t - 1;
-                    if (last) P.cnt[pair] = 0;
-                }
-                if (__shfl_sync(0xffffffffu, last, 0)) {
+                if constexpr (!PART) {
                     __threadfence();
-                    merge_pair<NT>(P, cs.t, cs.kvh, cs.S_t, lane);
+                    __syncwarp();
+                    int last = 0;
+                    if (lane == 0) {
+                        const uint32_t prev = atomicAdd(&P.cnt[pair], 1u);
+                        last = prev == (uint32_t)cs.S_t - 1;
+                        if (last) P.cnt[pair] = 0;
+                    }
+                    if (__shfl_sync(0xffffffffu, last, 0)) {
+                        __threadfence();
+                        merge_pair<NT>(P, cs.t, cs.kvh, cs.S_t, lane);
+                    }
                 }
             }
         }
@@ -532,12 +509,19 @@ int enqueue_attention(Launcher& L, const AttnProblem& p, const KCtx& c) {
     const size_t smem = (size_t)nw * 2 * p.pos * 128 + 1024 + nw * 2 * 8 +
                         (2 * kAMaxRows + 1) * 4;
     void* args[] = {(void*)&p, (void*)&c};
+    if (p.part) {  // [pos == 64][G > 8]; alone on the GPU: always the split schedule
+        static const void* const part[2][2] = {
+            {(const void*)attn_decode_kernel<1, 6, 128, true, true>, (const void*)attn_decode_kernel<2, 6, 128, true, true>},
+            {(const void*)attn_decode_kernel<1, 12, 64, true, true>, (const void*)attn_decode_kernel<2, 12, 64, true, true>}};
+        // kv_len may come from the kernel before this one (an eviction): no programmatic launch
+        return L.launch(part[p.pos == 64][p.G > 8], grid, block, smem, args, false);
+    }
     // [pos == 64][G > 8][kv_split]
     static const void* const kern[2][2][2] = {
-        {{(const void*)attn_decode_kernel<1, 6, 128, false>, (const void*)attn_decode_kernel<1, 6, 128, true>},
-         {(const void*)attn_decode_kernel<2, 6, 128, false>, (const void*)attn_decode_kernel<2, 6, 128, true>}},
-        {{(const void*)attn_decode_kernel<1, 12, 64, false>, (const void*)attn_decode_kernel<1, 12, 64, true>},
-         {(const void*)attn_decode_kernel<2, 12, 64, false>, (const void*)attn_decode_kernel<2, 12, 64, true>}}};
+        {{(const void*)attn_decode_kernel<1, 6, 128, false, false>, (const void*)attn_decode_kernel<1, 6, 128, true, false>},
+         {(const void*)attn_decode_kernel<2, 6, 128, false, false>, (const void*)attn_decode_kernel<2, 6, 128, true, false>}},
+        {{(const void*)attn_decode_kernel<1, 12, 64, false, false>, (const void*)attn_decode_kernel<1, 12, 64, true, false>},
+         {(const void*)attn_decode_kernel<2, 12, 64, false, false>, (const void*)attn_decode_kernel<2, 12, 64, true, false>}}};
     const void* f = kern[p.pos == 64][p.G > 8][p.kv_split != 0];
     return L.launch(f, grid, block, smem, args, true);
 }

@@ -148,6 +148,104 @@ struct AttnProblem {
     // scores, V after the V product); 0: together, after the V product.  Load schedule only:
     // the results are identical either way.
     int kv_split;
+    // 1: every chunk leaves its partial and nothing is merged (o and cnt unused)
+    int part;
+};
+
+// Prefixes that sequences of a batch share (lengths and membership as device arrays).
+struct PrefixRef {
+    const int* of;          // [T]: prefix of a sequence, -1: none
+    const int* len;         // [n]
+    int n, cap;
+};
+
+// Attention of the batch's query heads over the prefixes they share.  Sequences with the same
+// prefix form a group; a row is one (sequence, query head) of the group and KV head.  A tile is
+// `tile_seqs` sequences' rows (at most kPrefixRows), a step is one tile against kPrefixKeys
+// positions.  The steps of all (group, KV head, tile) in order are cut into kPrefixShares equal
+// shares, one per CTA; share s's part of tile i leaves its partial in slot s + i.
+constexpr int kPrefixRows = 256;
+constexpr int kPrefixKeys = 128;
+// Fixed, so that results never depend on the SM count: one share per SM of a 152-SM part.
+constexpr int kPrefixShares = 152;
+constexpr int kPrefixMax = 512;     // sequences, and prefixes, per call
+
+// What the merge needs of a sequence's group (written by the prefix kernel's first CTA).
+struct PrefixSeq {
+    int tile;               // first tile of the group
+    int tiles;              // tiles per KV head (0: nothing visible)
+    int step;               // first step of the group
+    int steps;              // steps per tile
+    int i;                  // the sequence's place in the group
+    int total;              // steps of the whole call
+    int pad[2];
+};
+
+struct PrefixProblem {
+    CUtensorMap tmK, tmV;   // prefixes as 2-D [n * nkv * cap][64], box {64, kPrefixKeys}, SW128
+    const bf16* q;          // [T][nq * 64]
+    const int* kv_len;      // [T] own lengths (window)
+    PrefixRef prefix;
+    float* part_ml;         // [slot][kPrefixRows][2]  (max, sum)
+    float* part_acc;        // [slot][kPrefixRows][64]
+    PrefixSeq* seq;         // [T]
+    int T, nq, nkv, G, kv_cap, window, tile_seqs;
+    float scale_log2;
+};
+
+// Joins a sequence's prefix partials and own-cache chunks.
+struct PrefixMergeProblem {
+    const float* pre_ml;
+    const float* pre_acc;
+    const PrefixSeq* seq;   // NULL: no prefixes
+    const float* own_ml;    // as AttnProblem::part_ml / part_acc
+    const float* own_acc;
+    const int* kv_len;
+    bf16* o;                // [T][nq * 64]
+    float* lse;             // [T][nq] or NULL
+    int T, nq, nkv, G, kv_cap, window, chunk, S_max, tile_seqs;
+};
+
+// acc[t][j][p] += sum over the group's heads of exp(scale q.k_p - lse)
+struct WeightsProblem {
+    const bf16* q;          // [T][nq * 64]
+    const bf16* k;          // [T][nkv][cap][64]
+    const float* lse;       // [T][nq]
+    const int* kv_len;      // [T]
+    float* acc;             // [T][nkv][cap]
+    int T, nq, nkv, G, cap;
+    float scale_log2;
+};
+
+// Which positions stay, then the move of their rows.
+struct EvictProblem {
+    const bf16* k;          // [T][nkv][cap][64]
+    const bf16* v;
+    const float* acc;       // [T][nkv][cap]
+    const int* kv_len;      // [T]
+    bf16* k_out;            // [T][nkv][cap_out][64]
+    bf16* v_out;
+    float* acc_out;         // [T][nkv][cap_out]
+    int* kv_len_out;        // [T]
+    int* kept;              // [T][nkv][budget] positions in order
+    int* user_kept;         // the same, filled up with -1, or NULL
+    int* count;             // [T] positions that stay, -1: a length out of range
+    int T, nkv, cap, cap_out, budget, n_sink, n_recent;
+    int in_place;
+};
+
+// y_out = y_in + scale_a B_a (A_a x), a = the sequence's adapter
+struct LoraProblem {
+    const bf16* x;          // [T] rows, ld_x apart
+    const bf16* y_in;       // [T] rows, ld_y_in apart
+    bf16* y_out;
+    const bf16* a;          // [n][max_rank][in]
+    const bf16* b;          // [n][out][max_rank]
+    const float* scale;     // [n] or NULL
+    const int* rank;        // [n] or NULL
+    const int* adapter_of;  // [T], -1: none
+    long long ld_x, ld_y_in, ld_y_out;
+    int T, n, in, out, max_rank;
 };
 
 struct NormProblem {
@@ -226,6 +324,11 @@ int enqueue_router(Launcher& L, const RouterProblem& p, const KCtx& c);
 int enqueue_dispatch(Launcher& L, const DispatchProblem& p, const KCtx& c);
 int enqueue_combine(Launcher& L, const CombineProblem& p, const KCtx& c);
 int enqueue_attention(Launcher& L, const AttnProblem& p, const KCtx& c);
+int enqueue_prefix(Launcher& L, const PrefixProblem& p, const KCtx& c);
+int enqueue_prefix_merge(Launcher& L, const PrefixMergeProblem& p, const KCtx& c);
+int enqueue_weights(Launcher& L, const WeightsProblem& p, const KCtx& c, int sms);
+int enqueue_evict(Launcher& L, const EvictProblem& p, const KCtx& c);
+int enqueue_lora(Launcher& L, const LoraProblem& p, const KCtx& c);
 int enqueue_gemm_tc(Launcher& L, const GemmProblem& p, const KCtx& c);
 int enqueue_gemm_finish(Launcher& L, const FinishProblem& p, const KCtx& c);
 int enqueue_gemv(Launcher& L, const GemvProblem& p, const KCtx& c);

@@ -21,6 +21,7 @@
 #include <unordered_set>
 #include <vector>
 
+#include "host.h"
 #include "kernels.h"
 #include "sgp.h"
 
@@ -232,7 +233,7 @@ struct GraphLauncher : Launcher {
 // =======================================================================================
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-constexpr int kMaxTokens = 512;  // sequences per call (attention prefix table, router groups)
+constexpr int kMaxTokens = kHostMaxTokens;  // sequences per call (attention prefix table, router groups)
 
 int check_dims(const sgp_dims* d) {
     if (!d) return fail_arg("dims is NULL");
@@ -949,6 +950,29 @@ int run_layer_stream(const sgp_dims& d, const sgp_layer* layer, int li, const in
 }  // namespace
 
 // =======================================================================================
+// shared with the other entry points (host.h)
+// =======================================================================================
+namespace sgp {
+
+int host_fail_arg(const char* what) { return fail_arg(what); }
+int host_fail_cuda(cudaError_t e, const char* what) { return fail_cuda(e, what); }
+int host_launch(cudaStream_t s, const void* func, dim3 grid, dim3 block, size_t smem, void** args,
+                bool overlap_ok) {
+    return StreamLauncher(s).launch(func, grid, block, smem, args, overlap_ok);
+}
+int host_tmap(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint32_t box_inner,
+              uint32_t box_rows) {
+    return make_tmap(map, base, inner, rows, box_inner, box_rows);
+}
+bool host_driver_ready() { return drv().core; }
+int host_sms() { return device_sms(); }
+KCtx host_ctx(void* status, uint32_t op) {
+    return plain_ctx(static_cast<uint32_t*>(status), kDefaultTimeout, op << 24);
+}
+
+}  // namespace sgp
+
+// =======================================================================================
 // C ABI: info
 // =======================================================================================
 extern "C" const char* sgp_status_string(int s) {
@@ -998,6 +1022,24 @@ extern "C" int sgp_device_info_get(sgp_device_info* info) {
 extern "C" size_t sgp_workspace_bytes(const sgp_dims* d, int n_tokens, int max_kv_len) {
     if (check_dims(d) != SGP_OK || n_tokens < 1 || max_kv_len < 1) return 0;
     return make_layout(*d, n_tokens, 1, max_kv_len, 0).total;
+}
+
+extern "C" int sgp_workspace_views(const sgp_dims* d, int n_tokens, int max_kv_len, void* ws,
+                                   size_t ws_bytes, sgp_layer_dump* view) {
+    int r;
+    if ((r = check_dims(d)) != SGP_OK) return r;
+    if (n_tokens < 1 || n_tokens > kMaxTokens || max_kv_len < 1) return fail_arg("n_tokens or max_kv_len");
+    if (!ws || !view) return fail_arg("NULL pointer");
+    const Layout Lay = make_layout(*d, n_tokens, 1, max_kv_len, 0);
+    if (ws_bytes < Lay.total) return fail_arg("workspace too small");
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    memset(view, 0, sizeof(*view));
+    view->a = base + Lay.a;
+    view->q = base + Lay.q;
+    view->o = base + Lay.o;
+    view->h = base + Lay.h;
+    view->u = base + Lay.u;
+    return SGP_OK;
 }
 
 static int temporal_common(const sgp_dims* d, const sgp_layer* layers, int n_layers,

@@ -65,6 +65,21 @@ class sgp_pipeline_opts(C.Structure):
                 ("stage_lanes", C.c_int), ("stage_times_shared", C.c_int)]
 
 
+class sgp_prefix(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("len", C.c_void_p),
+                ("prefix_of", C.c_void_p), ("n_prefixes", C.c_int), ("cap", C.c_int)]
+
+
+class sgp_evict(C.Structure):
+    _fields_ = [("budget", C.c_int), ("n_sink", C.c_int), ("n_recent", C.c_int)]
+
+
+class sgp_lora(C.Structure):
+    _fields_ = [("a", C.c_void_p), ("b", C.c_void_p), ("scale", C.c_void_p), ("rank", C.c_void_p),
+                ("n_adapters", C.c_int), ("in", C.c_int), ("out", C.c_int),
+                ("max_rank", C.c_int)]
+
+
 _lib = None
 
 _SIGS = {
@@ -128,6 +143,25 @@ ALLOC_OBJECTIVE = C.CFUNCTYPE(C.c_double, C.POINTER(C.c_int), C.c_int, C.c_void_
 _SIGS["sgp_refine_allocation"] = (C.c_int, [C.c_int, C.POINTER(C.c_int), C.c_int, C.c_int,
                                             C.c_int, ALLOC_OBJECTIVE, C.c_void_p,
                                             C.POINTER(C.c_double)])
+_SIGS["sgp_workspace_views"] = (C.c_int, [C.POINTER(sgp_dims), C.c_int, C.c_int, C.c_void_p,
+                                          C.c_size_t, C.POINTER(sgp_layer_dump)])
+_SIGS["sgp_prefix_attention_workspace_bytes"] = (C.c_size_t, [C.POINTER(sgp_dims), C.c_int,
+                                                              C.c_int, C.c_int])
+_SIGS["sgp_prefix_attention"] = (C.c_int, [C.POINTER(sgp_dims), C.POINTER(sgp_layer),
+                                           C.POINTER(sgp_prefix), C.c_void_p, C.c_void_p,
+                                           C.c_void_p, C.c_void_p, C.c_int, C.c_void_p,
+                                           C.c_size_t, C.c_void_p])
+_SIGS["sgp_attention_weights"] = (C.c_int, [C.POINTER(sgp_dims), C.POINTER(sgp_layer),
+                                            C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                                            C.c_int, C.c_void_p, C.c_size_t, C.c_void_p])
+_SIGS["sgp_kv_evict_workspace_bytes"] = (C.c_size_t, [C.POINTER(sgp_dims), C.c_int, C.c_int])
+_SIGS["sgp_kv_evict"] = (C.c_int, [C.POINTER(sgp_dims), C.POINTER(sgp_layer),
+                                   C.POINTER(sgp_layer), C.POINTER(sgp_evict), C.c_void_p,
+                                   C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int,
+                                   C.c_void_p, C.c_size_t, C.c_void_p])
+_SIGS["sgp_lora_apply"] = (C.c_int, [C.POINTER(sgp_lora), C.c_void_p, C.c_void_p, C.c_int64,
+                                     C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int,
+                                     C.c_void_p, C.c_size_t, C.c_void_p])
 
 ABI_FUNCTIONS = tuple(_SIGS)
 
@@ -173,6 +207,41 @@ def _stream(stream) -> Optional[int]:
     return getattr(stream, "cuda_stream", stream)
 
 
+# What the serving operators are given per call: a wrong type, size, layout or device would be
+# read as something else, so it raises here.
+_DTYPES = None
+
+
+def _arg(t, kind: str, count: int, what: str, rows: bool = False) -> int:
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+        _DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32, "i32": torch.int32,
+                   "u8": torch.uint8, "device": torch.cuda.current_device}
+    if t.dtype is not _DTYPES[kind]:
+        raise ValueError(f"{what}: expected {_DTYPES[kind]}, got {t.dtype}")
+    if t.get_device() != _DTYPES["device"]():
+        raise ValueError(f"{what}: not on the current CUDA device ({t.device})")
+    if t.numel() < count or not (rows or t.is_contiguous()):
+        raise ValueError(f"{what}: expected at least {count} contiguous elements, got "
+                         f"{tuple(t.shape)} with strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _rows(t, n: int, width: int, what: str):
+    """Pointer and row stride of a [>= n][width] bf16 matrix whose rows are contiguous."""
+    _arg(t, "bf16", n * width, what, rows=True)
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] < n or shape[1] != width or stride[1] != 1:
+        raise ValueError(f"{what}: expected [{n}][{width}] with contiguous rows, got "
+                         f"{tuple(shape)} with strides {stride}")
+    return t.data_ptr(), stride[0] if shape[0] > 1 else width
+
+
+def _ws(t):
+    return _arg(t, "u8", 64, "workspace"), t.numel()
+
+
 # --------------------------------------------------------------------------------------
 # structure builders
 # --------------------------------------------------------------------------------------
@@ -194,6 +263,54 @@ def make_layer(w: dict, k_cache, v_cache, window: int) -> sgp_layer:
                      _p(w["w_router"]), _p(w.get("router_bias")), _p(w["w_gate_up"]),
                      _p(w["w_down"]), _p(k_cache), _p(v_cache), int(k_cache.shape[2]),
                      int(window))
+
+
+def make_heads(n_q_heads: int, n_kv_heads: int, head_dim: int = 64) -> sgp_dims:
+    """Dimensions of the serving operators: only the head counts are set."""
+    return sgp_dims(n_q_heads=n_q_heads, n_kv_heads=n_kv_heads, head_dim=head_dim)
+
+
+def _cache4(t, what: str):
+    if t.dim() != 4:
+        raise ValueError(f"{what}: expected [n][n_kv][cap][d], got {tuple(t.shape)}")
+    return _arg(t, "bf16", t.numel(), what)
+
+
+def make_cache(k_cache, v_cache, window: int = 0) -> sgp_layer:
+    """A layer's cache alone, for the serving operators.  Keeps the tensors alive."""
+    if k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache differ in shape")
+    c = sgp_layer(k_cache=_cache4(k_cache, "k_cache"), v_cache=_cache4(v_cache, "v_cache"),
+                  kv_cap=int(k_cache.shape[2]), window=int(window))
+    c.tensors = (k_cache, v_cache)
+    return c
+
+
+def make_prefix(k, v, length, prefix_of) -> sgp_prefix:
+    """Shared prefixes.  Keeps the tensors alive."""
+    if k.shape != v.shape:
+        raise ValueError("the prefixes' k and v differ in shape")
+    p = sgp_prefix(_cache4(k, "prefix k"), _cache4(v, "prefix v"),
+                   _arg(length, "i32", k.shape[0], "prefix length"),
+                   _arg(prefix_of, "i32", 1, "prefix_of"), int(k.shape[0]), int(k.shape[2]))
+    p.tensors = (k, v, length, prefix_of)
+    return p
+
+
+def make_evict(budget: int, n_sink: int = 0, n_recent: int = 0) -> sgp_evict:
+    return sgp_evict(budget, n_sink, n_recent)
+
+
+def make_lora(a, b, scale=None, rank=None) -> sgp_lora:
+    """Adapters a [n][max_rank][in] and b [n][out][max_rank].  Keeps the tensors alive."""
+    if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
+        raise ValueError(f"adapters: a {tuple(a.shape)} and b {tuple(b.shape)} do not match")
+    n, r, n_in = a.shape
+    p = sgp_lora(_arg(a, "bf16", a.numel(), "a"), _arg(b, "bf16", b.numel(), "b"),
+                 None if scale is None else _arg(scale, "f32", n, "scale"),
+                 None if rank is None else _arg(rank, "i32", n, "rank"), n, n_in, b.shape[1], r)
+    p.tensors = (a, b, scale, rank)
+    return p
 
 
 def layer_array(layers: Sequence[sgp_layer]):
@@ -278,6 +395,85 @@ def sgp_router_topk_noalloc(dims, h, g_mlp, w_router, router_bias, n_tokens: int
                                                _p(router_bias), n_tokens, _p(u_out),
                                                _p(topk_idx), _p(topk_w), _stream(stream)),
                  "sgp_router_topk_noalloc")
+
+
+def sgp_workspace_views(dims, n_tokens: int, max_kv_len: int, workspace) -> sgp_layer_dump:
+    view = sgp_layer_dump()
+    check(lib().sgp_workspace_views(C.byref(dims), n_tokens, max_kv_len, _p(workspace),
+                                    workspace.numel() * workspace.element_size(),
+                                    C.byref(view)), "sgp_workspace_views")
+    return view
+
+
+def layer_views(dims, n_tokens: int, max_kv_len: int, workspace) -> dict:
+    """The activations of sgp_workspace_views as tensors that share the workspace (uint8)."""
+    import torch
+    view = sgp_workspace_views(dims, n_tokens, max_kv_len, workspace)
+    width = {"a": dims.hidden, "q": dims.n_q_heads * dims.head_dim,
+             "o": dims.n_q_heads * dims.head_dim, "h": dims.hidden, "u": dims.hidden}
+    out = {}
+    for name, w in width.items():
+        at = getattr(view, name) - workspace.data_ptr()
+        out[name] = workspace[at:at + n_tokens * w * 2].view(torch.bfloat16).view(n_tokens, w)
+    return out
+
+
+def sgp_prefix_attention_workspace_bytes(dims, n_tokens: int, kv_cap: int,
+                                         n_prefixes: int) -> int:
+    return int(lib().sgp_prefix_attention_workspace_bytes(C.byref(dims), n_tokens, kv_cap,
+                                                          n_prefixes))
+
+
+def sgp_prefix_attention(dims, cache: sgp_layer, prefix: Optional[sgp_prefix], kv_len, q, o, lse,
+                         n_tokens: int, workspace, stream=None) -> int:
+    rows = n_tokens * dims.n_q_heads
+    ws, nbytes = _ws(workspace)
+    return check(lib().sgp_prefix_attention(
+        C.byref(dims), C.byref(cache), None if prefix is None else C.byref(prefix),
+        _arg(kv_len, "i32", n_tokens, "kv_len"), _arg(q, "bf16", rows * dims.head_dim, "q"),
+        _arg(o, "bf16", rows * dims.head_dim, "o"),
+        None if lse is None else _arg(lse, "f32", rows, "lse"), n_tokens, ws, nbytes,
+        _stream(stream)), "sgp_prefix_attention")
+
+
+def sgp_attention_weights(dims, cache: sgp_layer, kv_len, q, lse, acc, n_tokens: int, workspace,
+                          stream=None) -> int:
+    rows = n_tokens * dims.n_q_heads
+    ws, nbytes = _ws(workspace)
+    return check(lib().sgp_attention_weights(
+        C.byref(dims), C.byref(cache), _arg(kv_len, "i32", n_tokens, "kv_len"),
+        _arg(q, "bf16", rows * dims.head_dim, "q"), _arg(lse, "f32", rows, "lse"),
+        _arg(acc, "f32", n_tokens * dims.n_kv_heads * cache.kv_cap, "acc"), n_tokens, ws, nbytes,
+        _stream(stream)), "sgp_attention_weights")
+
+
+def sgp_kv_evict_workspace_bytes(dims, n_tokens: int, budget: int) -> int:
+    return int(lib().sgp_kv_evict_workspace_bytes(C.byref(dims), n_tokens, budget))
+
+
+def sgp_kv_evict(dims, source: sgp_layer, target: sgp_layer, policy: sgp_evict, kv_len,
+                 kv_len_out, acc, acc_out, kept, n_tokens: int, workspace, stream=None) -> int:
+    pairs = n_tokens * dims.n_kv_heads
+    ws, nbytes = _ws(workspace)
+    return check(lib().sgp_kv_evict(
+        C.byref(dims), C.byref(source), C.byref(target), C.byref(policy),
+        _arg(kv_len, "i32", n_tokens, "kv_len"), _arg(kv_len_out, "i32", n_tokens, "kv_len_out"),
+        _arg(acc, "f32", pairs * source.kv_cap, "acc"),
+        _arg(acc_out, "f32", pairs * target.kv_cap, "acc_out"),
+        None if kept is None else _arg(kept, "i32", pairs * policy.budget, "kept"), n_tokens, ws,
+        nbytes, _stream(stream)), "sgp_kv_evict")
+
+
+def sgp_lora_apply(lora: sgp_lora, adapter_of, x, y_in, y_out, n_tokens: int, workspace,
+                   stream=None) -> int:
+    n_in = getattr(lora, "in")
+    px, ld_x = _rows(x, n_tokens, n_in, "x")
+    pi, ld_i = _rows(y_in, n_tokens, lora.out, "y_in")
+    po, ld_o = _rows(y_out, n_tokens, lora.out, "y_out")
+    ws, nbytes = _ws(workspace)
+    return check(lib().sgp_lora_apply(C.byref(lora), _arg(adapter_of, "i32", n_tokens, "adapter_of"),
+                                      px, ld_x, pi, ld_i, po, ld_o, n_tokens, ws, nbytes,
+                                      _stream(stream)), "sgp_lora_apply")
 
 
 def sgp_status_from_workspace(workspace, stream=None) -> int:
