@@ -178,7 +178,7 @@ def prepare(case, seed):
             st["cache"] = sgp.make_cache(st["k"], st["v"], case["window"])
             st["prefix"] = sgp.make_prefix(st["pk"], st["pv"], st["plen"], st["of"])
             nbytes = sgp.sgp_prefix_attention_workspace_bytes(
-                st["dims"], n, case["own"], case["prefixes"], case["prefix"])
+                st["dims"], n, case["own"], case["prefixes"])
             st["ws"] = torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
             st["o"] = torch.empty_like(st["q"])
             st["lse"] = torch.empty(n, nq, dtype=torch.float32, device="cuda")
