@@ -20,7 +20,7 @@ namespace sgp {
 
 namespace {
 
-constexpr int kPThreads = 512;
+constexpr int kPThreads = 320;
 constexpr int kPHalf = kPrefixKeys * 128;     // K (or V) bytes of a step
 
 // The groups of the batch, built by every CTA in shared memory.
@@ -155,188 +155,339 @@ __device__ __forceinline__ Step step_at(const Plan& pl, int n, int x) {
     return {lo, i / pl.tiles[lo], i % pl.tiles[lo], r % pl.steps[lo]};
 }
 
-// The simplest form: 16 warps of 16 rows, warp-level matrix products, two stages of keys.
+// Warp 0 loads keys and values (TMA, a ring of steps), warp 1 issues the matrix products, warps
+// 2-5 and 6-9 are two softmax groups of 128 rows each.  Per step and group
+//     S = Q K^T   (M = 128 rows, N = 128 positions, K = 64), accumulators in tensor memory;
+//     P = exp2(scale S - m) by the group's threads, one row each, back to tensor memory as bf16;
+//     O += P V    (M = 128, N = 64, K = 128), P read from tensor memory.
+// The next step's S is issued before this step's O product, so that one group's exponentials run
+// beside the other's products.  A row's maximum m is only raised when it grew by more than 2^8:
+// weights up to 256 lose nothing in bf16 or fp32, and O is rescaled (a round trip through tensor
+// memory) almost never.
+constexpr int kPStages = 5;
+constexpr int kPRaise = 8;
+constexpr uint32_t kTmemS = 0, kTmemO = 256, kTmemP = 384;  // columns; per group 128, 64, 64
+
+struct PrefixBars {
+    uint64_t kv_full[kPStages], kv_empty[kPStages];
+    uint64_t q_full[2];    // the group's query rows are in shared memory
+    uint64_t s_full[2];    // S is complete
+    uint64_t s_free[2];    // the group holds S in registers
+    uint64_t p_full[2];    // P is in tensor memory (and O is rescaled)
+    uint64_t pv_done[2];   // O holds this step, P may be overwritten
+    uint32_t tmem;
+    int err;
+};
+
 __global__ void __launch_bounds__(kPThreads, 1)
     prefix_attn_kernel(const __grid_constant__ PrefixProblem P, const KCtx ctx) {
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + 4 * kPHalf);
-    Plan& pl = *reinterpret_cast<Plan*>(full + 2);
-    __shared__ int sh_err;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, cq = lane & 3;
+    uint8_t* qs = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));  // [2][128 rows]
+    uint8_t* ring = qs + 2 * 128 * 128;
+    PrefixBars& bar = *reinterpret_cast<PrefixBars*>(ring + kPStages * 2 * kPHalf);
+    Plan& pl = *reinterpret_cast<Plan*>(&bar + 1);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     griddep_launch();
     if (tid == 0) {
-        mbar_init(&full[0], 1);
-        mbar_init(&full[1], 1);
+        for (int s = 0; s < kPStages; ++s) {
+            mbar_init(&bar.kv_full[s], 1);
+            mbar_init(&bar.kv_empty[s], 1);
+        }
+        for (int h = 0; h < 2; ++h) {
+            mbar_init(&bar.q_full[h], 4);
+            mbar_init(&bar.s_full[h], 1);
+            mbar_init(&bar.s_free[h], 4);
+            mbar_init(&bar.p_full[h], 4);
+            mbar_init(&bar.pv_done[h], 1);
+        }
+        bar.err = 0;
         fence_barrier_init();
-        sh_err = 0;
+        prefetch_tensormap(&P.tmK);
+        prefetch_tensormap(&P.tmV);
     }
+    if (warp == 1) {
+        tmem_alloc(&bar.tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
     task_begin(ctx);
-    build_plan(pl, P, ctx);
+    build_plan(pl, P, ctx);  // ends with a barrier
+    tc_fence_after();
+    const uint32_t tmem = bar.tmem;
     const int n = P.prefix.n, total = pl.step0[n];
     const int shares = min(kPrefixShares, total);  // none of them empty
     const int b = blockIdx.x;
     const int x0 = b < shares ? (int)((long long)b * total / shares) : 0;
     const int x1 = b < shares ? (int)((long long)(b + 1) * total / shares) : 0;
-    const uint64_t pol = policy_evict_last();
-    auto issue = [&](int x, int stage) {
-        const Step s = step_at(pl, n, x);
-        const int row = (s.g * P.nkv + s.kvh) * P.prefix.cap + (pl.first[s.g] + s.k) * kPrefixKeys;
-        uint8_t* dst = smem + stage * 2 * kPHalf;
-        mbar_arrive_expect_tx(&full[stage], 2 * kPHalf);
-        tma_load_2d(dst, &P.tmK, &full[stage], 0, row, pol);
-        tma_load_2d(dst + kPHalf, &P.tmV, &full[stage], 0, row, pol);
+    volatile int* err = &bar.err;
+    auto gave_up = [&](uint32_t where) {
+        report(ctx, ST_TIMEOUT, where);
+        *err = 1;
     };
-    if (tid == 0 && x0 < x1) issue(x0, 0);
-    uint32_t it = 0;
-    bool ok = true;
-    for (int x = x0; x < x1 && ok;) {
-        const Step s = step_at(pl, n, x);
-        const int end = min(x1, x + pl.steps[s.g] - s.k);
-        const int seq0 = pl.base[s.g] + s.tile * P.tile_seqs;
-        const int rows = min(P.tile_seqs, pl.base[s.g + 1] - seq0) * P.G;
-        const int len = pl.len[s.g];
-        const bool active = warp * 16 < rows;
-        // query rows of this lane (g and g + 8 of the warp's 16) and their least positions
-        uint32_t qf[4][4];
-        int low[2] = {0, 0};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = warp * 16 + g + 8 * h;
-            const bool has = r < rows;
-            const int t = has ? pl.mem[seq0 + r / P.G] : 0;
-            const bf16* q = P.q + (size_t)t * P.nq * 64 + (size_t)(s.kvh * P.G + (has ? r % P.G : 0)) * 64;
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                qf[kk][h] = has ? *reinterpret_cast<const uint32_t*>(q + kk * 16 + 2 * cq) : 0u;
-                qf[kk][2 + h] = has ? *reinterpret_cast<const uint32_t*>(q + kk * 16 + 2 * cq + 8) : 0u;
+
+    if (warp == 0) {
+        if (elect_one()) {
+            const uint64_t pol = policy_evict_last();  // the other row tiles read it too
+            uint32_t it = 0;
+            for (int x = x0; x < x1 && !*err; ++it, ++x) {
+                const uint32_t st = it % kPStages, use = it / kPStages;
+                if (use > 0 && !mbar_wait(&bar.kv_empty[st], (use - 1) & 1u, ctx.timeout_ns)) {
+                    gave_up(20);
+                    break;
+                }
+                const Step s = step_at(pl, n, x);
+                const int row = (s.g * P.nkv + s.kvh) * P.prefix.cap + (pl.first[s.g] + s.k) * kPrefixKeys;
+                uint8_t* dst = ring + st * 2 * kPHalf;
+                mbar_arrive_expect_tx(&bar.kv_full[st], 2 * kPHalf);
+                tma_load_2d(dst, &P.tmK, &bar.kv_full[st], 0, row, pol);
+                tma_load_2d(dst + kPHalf, &P.tmV, &bar.kv_full[st], 0, row, pol);
             }
-            if (has && P.window > 0) {
-                const int own = P.kv_len[t];
-                low[h] = max(0, len + (own >= 0 && own <= P.kv_cap ? own : 0) - P.window);
+            if (*err)  // loads in flight into this CTA's shared memory (bounded)
+                for (uint32_t i = it > kPStages ? it - kPStages : 0; i < it; ++i)
+                    (void)mbar_wait(&bar.kv_full[i % kPStages], (i / kPStages) & 1u, 10000000ull);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (elect_one()) {
+            uint32_t it = 0, n_q[2] = {0, 0}, n_s[2] = {0, 0}, n_p[2] = {0, 0};
+            constexpr uint32_t id_s = idesc_bf16_f32(128, kPrefixKeys), id_o = idesc_bf16_f32(128, 64) | kIdescBmn;
+            auto product = [&](uint32_t st, int groups, bool first) {  // O += P V of one step
+                const uint32_t va = smem_u32(ring + st * 2 * kPHalf + kPHalf);
+                for (int h = 0; h < groups; ++h) {
+                    if (!mbar_wait(&bar.p_full[h], n_p[h] & 1u, ctx.timeout_ns)) {
+                        gave_up(21);
+                        return false;
+                    }
+                    ++n_p[h];
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < kPrefixKeys / 16; ++k)
+                        tc_mma_bf16_ta(tmem + kTmemO + 64 * h, tmem + kTmemP + 64 * h + 8 * k,
+                                       smem_desc_sw128(va + k * 16 * 128), id_o, !(first && k == 0));
+                    tc_commit(&bar.pv_done[h]);
+                }
+                tc_commit(&bar.kv_empty[st]);
+                return true;
+            };
+            bool ok = true;
+            for (int x = x0; x < x1 && ok;) {
+                const Step s = step_at(pl, n, x);
+                const int end = min(x1, x + pl.steps[s.g] - s.k);
+                const int rows = min(P.tile_seqs, pl.base[s.g + 1] - pl.base[s.g] - s.tile * P.tile_seqs) * P.G;
+                const int groups = rows > 128 ? 2 : 1;
+                uint32_t prev = 0;
+                const int begin = x;
+                for (; x < end && ok; ++x, ++it) {
+                    const uint32_t st = it % kPStages;
+                    if (!mbar_wait(&bar.kv_full[st], (it / kPStages) & 1u, ctx.timeout_ns)) {
+                        gave_up(22);
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t ka = smem_u32(ring + st * 2 * kPHalf);
+                    for (int h = 0; h < groups && ok; ++h) {
+                        if (x == begin) ok = mbar_wait(&bar.q_full[h], n_q[h]++ & 1u, ctx.timeout_ns);
+                        if (ok && n_s[h] > 0) ok = mbar_wait(&bar.s_free[h], (n_s[h] - 1) & 1u, ctx.timeout_ns);
+                        if (!ok) {
+                            gave_up(23);
+                            break;
+                        }
+                        ++n_s[h];
+                        tc_fence_after();
+                        const uint32_t qa = smem_u32(qs + h * 128 * 128);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            tc_mma_bf16(tmem + kTmemS + 128 * h, smem_desc_sw128(qa + 32 * k),
+                                        smem_desc_sw128(ka + 32 * k), id_s, k > 0);
+                        tc_commit(&bar.s_full[h]);
+                    }
+                    if (ok && x > begin) ok = product(prev, groups, x == begin + 1);
+                    prev = st;
+                }
+                // the last step's product, before a wait for the next tile's queries
+                if (ok) ok = product(prev, groups, end == begin + 1);
             }
         }
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[8][4];
-#pragma unroll
-        for (int d = 0; d < 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
-        int k = s.k;
-        for (; x < end; ++x, ++k, ++it) {
-            const int stage = it & 1;
-            if (tid == 0 && x + 1 < x1) issue(x + 1, stage ^ 1);
-            if (!mbar_wait(&full[stage], (it >> 1) & 1u, ctx.timeout_ns)) {
-                if (lane == 0) report(ctx, ST_TIMEOUT, 20);
-                sh_err = 1;
+        __syncwarp();
+    } else {
+        const int h = (warp - 2) >> 2, quad = warp & 3;  // a warp reads its quadrant's TMEM lanes
+        const int r = h * 128 + quad * 32 + lane;        // this thread's row of the tile
+        const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
+        const uint32_t ts = tl + kTmemS + 128 * h, to = tl + kTmemO + 64 * h, tp = tl + kTmemP + 64 * h;
+        uint32_t it = 0;  // steps of this group
+        bool ok = true;
+        // every wait's outcome is the warp's: its tensor-memory accesses are warp-wide
+        auto wait = [&](uint64_t* bar_, uint32_t parity, uint32_t where) {
+            if (__all_sync(0xffffffffu, mbar_wait(bar_, parity, ctx.timeout_ns))) return true;
+            if (lane == 0) gave_up(where);
+            return false;
+        };
+        for (int x = x0; x < x1 && ok;) {
+            const Step s = step_at(pl, n, x);
+            const int end = min(x1, x + pl.steps[s.g] - s.k);
+            const int seq0 = pl.base[s.g] + s.tile * P.tile_seqs;
+            const int rows = min(P.tile_seqs, pl.base[s.g + 1] - seq0) * P.G;
+            if (rows <= 128 * h) {
+                x = end;
+                continue;
             }
-            uint8_t* ks = smem + stage * 2 * kPHalf;
-            const int pos0 = (pl.first[s.g] + k) * kPrefixKeys;
-            const int valid = min(kPrefixKeys, len - pos0);
-            if (valid < kPrefixKeys) {  // what lies behind the prefix is arbitrary: P is 0 there
-                uint4* v4 = reinterpret_cast<uint4*>(ks + kPHalf);
-                for (int e = valid * 8 + tid; e < kPrefixKeys * 8; e += kPThreads)
-                    v4[e] = make_uint4(0, 0, 0, 0);
-                fence_proxy_async();
-            }
-            __syncthreads();
-            if (sh_err) {
-                ok = false;
-                ++it;
-                break;
-            }
-            const uint32_t ka = smem_u32(ks), va = ka + kPHalf;
-            if (active) {
+            const int len = pl.len[s.g];
+            // this warp's 32 query rows, 8 lanes to a row, into the swizzled tile (zeros past the
+            // tile's rows: rows do not mix, and theirs are not stored)
+            {
+                uint8_t* dst = qs + h * 128 * 128;
+                uint4 v[8];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    float sc[8][4];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint32_t bf[4];
-                            const int mi = lane >> 3;
-                            ldsm_x4(ka + sw128(half * 64 + j * 16 + (mi >> 1) * 8 + (lane & 7),
-                                               kk * 2 + (mi & 1)), bf);
-                            mma16816(sc[2 * j], qf[kk], bf[0], bf[1]);
-                            mma16816(sc[2 * j + 1], qf[kk], bf[2], bf[3]);
-                        }
+                for (int i = 0; i < 8; ++i) {
+                    const int q = quad * 32 + i * 4 + (lane >> 3), row = h * 128 + q;
+                    v[i] = make_uint4(0, 0, 0, 0);
+                    if (row < rows) {
+                        const bf16* src = P.q + (size_t)pl.mem[seq0 + row / P.G] * P.nq * 64 +
+                                          (size_t)(s.kvh * P.G + row % P.G) * 64;
+                        v[i] = reinterpret_cast<const uint4*>(src)[lane & 7];
                     }
-                    float mx[2] = {-INFINITY, -INFINITY};
+                }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<uint4*>(dst + sw128(quad * 32 + i * 4 + (lane >> 3), lane & 7)) = v[i];
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.q_full[h]);
+            }
+            int low = 0;
+            if (P.window > 0 && r < rows) {
+                const int own = P.kv_len[pl.mem[seq0 + r / P.G]];
+                low = max(0, len + (own >= 0 && own <= P.kv_cap ? own : 0) - P.window);
+            }
+            const bool live = h * 128 + quad * 32 < rows;  // some row of this warp counts
+            float m = -INFINITY;  // the maximum the weights are taken against (scaled, base 2)
+            float2 l2 = make_float2(0.f, 0.f);
+            const int begin = x;
+            for (int k = s.k; x < end; ++x, ++k, ++it) {
+                if (!(ok = wait(&bar.s_full[h], it & 1u, 24))) break;
+                tc_fence_after();
+                const int pos0 = (pl.first[s.g] + k) * kPrefixKeys;
+                if (h == 0 && pos0 + kPrefixKeys > len) {
+                    // what lies behind the prefix is arbitrary and its weight is 0: clear V there
+                    // (both groups' products wait for this group's P)
+                    const uint32_t i = (uint32_t)(x - x0), st = i % kPStages;
+                    if (!(ok = wait(&bar.kv_full[st], (i / kPStages) & 1u, 27))) break;
+                    uint4* v4 = reinterpret_cast<uint4*>(ring + st * 2 * kPHalf + kPHalf);
+                    for (int e = (len - pos0) * 8 + quad * 32 + lane; e < kPrefixKeys * 8; e += 128)
+                        v4[e] = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async();
+                }
+                if (!live) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.s_free[h]);
+                    // one arrival for every step: not before the step before is through
+                    if (x > begin && !(ok = wait(&bar.pv_done[h], (it - 1) & 1u, 28))) break;
+                    if (lane == 0) mbar_arrive(&bar.p_full[h]);
+                    continue;
+                }
+                uint32_t sr[4][32];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int at = half * 64 + j * 8 + 2 * cq + (e & 1);
-                            float v = sc[j][e] * P.scale_log2;
-                            if (at >= valid || pos0 + at < low[e >> 1]) v = -INFINITY;
-                            sc[j][e] = v;
-                            mx[e >> 1] = fmaxf(mx[e >> 1], v);
+                for (int c = 0; c < 4; ++c) tmem_ld_x32(ts + 32 * c, sr[c]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld_wait32(sr[c]);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.s_free[h]);
+                if (pos0 + kPrefixKeys > len || __any_sync(0xffffffffu, pos0 < low)) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const int at = pos0 + c * 32 + j;
+                            if (at >= len || at < low) sr[c][j] = 0xff800000u;  // -inf
                         }
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-                        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-                        const float nm = fmaxf(m[h], mx[h]);
-                        const float c = m[h] == -INFINITY ? 0.f : exp2f(m[h] - nm);
-                        m[h] = nm;
-                        l[h] *= c;
+                for (int j = 0; j < 32; ++j)
 #pragma unroll
-                        for (int d = 0; d < 8; ++d) {
-                            o[d][2 * h] *= c;
-                            o[d][2 * h + 1] *= c;
-                        }
-                        // a row that has seen nothing yet: every score is -inf, every weight 0
-                        const float sub = nm == -INFINITY ? 0.f : nm;
+                    for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], __uint_as_float(sr[c][j]));
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * P.scale_log2;
+                // P and O are this thread's once the step before has been multiplied
+                if (x > begin) {
+                    if (!(ok = wait(&bar.pv_done[h], (it - 1) & 1u, 25))) break;
+                    tc_fence_after();
+                }
+                if (__any_sync(0xffffffffu, top > m + kPRaise)) {
+                    const float nm = fmaxf(m, top);
+                    const float c = m == -INFINITY ? 0.f : ex2(m - nm);
+                    m = nm;
+                    l2.x *= c;
+                    l2.y *= c;
+                    if (x > begin) {
+                        uint32_t o[32];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
+                        for (int q = 0; q < 2; ++q) {
+                            tmem_ld_x32(to + 32 * q, o);
+                            tmem_ld_wait32(o);
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                const float w = exp2f(sc[j][2 * h + e] - sub);
-                                sc[j][2 * h + e] = w;
-                                l[h] += w;
+                                uint32_t w[16];
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    w[j] = __float_as_uint(__uint_as_float(o[e * 16 + j]) * c);
+                                tmem_st_x16(to + 32 * q + 16 * e, w);
                             }
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t a[4] = {pack_bf16x2(sc[2 * j][0], sc[2 * j][1]),
-                                               pack_bf16x2(sc[2 * j][2], sc[2 * j][3]),
-                                               pack_bf16x2(sc[2 * j + 1][0], sc[2 * j + 1][1]),
-                                               pack_bf16x2(sc[2 * j + 1][2], sc[2 * j + 1][3])};
-#pragma unroll
-                        for (int d = 0; d < 4; ++d) {
-                            uint32_t bf[4];
-                            const int mi = lane >> 3;
-                            ldsm_x4_t(va + sw128(half * 64 + j * 16 + (mi & 1) * 8 + (lane & 7),
-                                                 2 * d + (mi >> 1)), bf);
-                            mma16816(o[2 * d], a, bf[0], bf[1]);
-                            mma16816(o[2 * d + 1], a, bf[2], bf[3]);
                         }
                     }
                 }
+                // a row that has seen nothing yet: every score is -inf, every weight 0
+                const float sub = m == -INFINITY ? 0.f : -m;
+                const float2 sc2 = make_float2(P.scale_log2, P.scale_log2), sub2 = make_float2(sub, sub);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        float2 v = make_float2(__uint_as_float(sr[c][2 * j]), __uint_as_float(sr[c][2 * j + 1]));
+                        v = fma2(v, sc2, sub2);
+                        v.x = ex2(v.x);
+                        v.y = ex2(v.y);
+                        l2 = add2(l2, v);
+                        // the weight's rounding to bf16, the second product's operand type
+                        w[j] = pack_bf16x2(v.x, v.y);
+                    }
+                    tmem_st_x16(tp + 16 * c, w);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.p_full[h]);
             }
-            __syncthreads();
-        }
-        if (!ok) break;
+            if (!ok) break;
+            // the last product, then this row's partial
+            if (!wait(&bar.pv_done[h], (it - 1) & 1u, 26)) break;
+            tc_fence_after();
+            if (live) {
+                const size_t slot = b + (size_t)(pl.tile0[s.g] + s.kvh * pl.tiles[s.g] + s.tile);
+                const size_t at = slot * kPrefixRows + r;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-            const int r = warp * 16 + g + 8 * h;
-            if (r >= rows) continue;
-            const size_t slot = b + (size_t)(pl.tile0[s.g] + s.kvh * pl.tiles[s.g] + s.tile);
-            const size_t at = slot * kPrefixRows + r;
-            if (cq == 0) *reinterpret_cast<float2*>(P.part_ml + at * 2) = make_float2(m[h], l[h]);
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t o[32];
+                    tmem_ld_x32(to + 32 * q, o);
+                    tmem_ld_wait32(o);
+                    if (r < rows) {
+                        uint4* dst = reinterpret_cast<uint4*>(P.part_acc + at * 64 + 32 * q);
 #pragma unroll
-            for (int d = 0; d < 8; ++d)
-                *reinterpret_cast<float2*>(P.part_acc + at * 64 + d * 8 + 2 * cq) =
-                    make_float2(o[d][2 * h], o[d][2 * h + 1]);
+                        for (int j = 0; j < 8; ++j) dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                    }
+                }
+                if (r < rows) *reinterpret_cast<float2*>(P.part_ml + at * 2) = make_float2(m, l2.x + l2.y);
+            }
+            tc_fence_before();
         }
     }
-    // the load after the last one waited for, if the loop gave up
-    if (!ok && tid == 0 && it > 0) (void)mbar_wait(&full[it & 1], (it >> 1) & 1u, 10000000ull);
     // the merge waits for this kernel: the own caches' kernel before it must be complete too
     griddep_wait();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 512);
     task_end(ctx);
 }
 
@@ -441,7 +592,7 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixMergeProb
 }  // namespace
 
 int enqueue_prefix(Launcher& L, const PrefixProblem& p, const KCtx& c) {
-    const size_t smem = 1024 + 4 * kPHalf + 2 * 8 + sizeof(Plan);
+    const size_t smem = 1024 + 2 * 128 * 128 + kPStages * 2 * kPHalf + sizeof(PrefixBars) + sizeof(Plan);
     void* args[] = {(void*)&p, (void*)&c};
     return L.launch((const void*)prefix_attn_kernel, dim3(kPrefixShares), dim3(kPThreads), smem, args,
                     true);
