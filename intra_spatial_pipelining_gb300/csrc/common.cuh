@@ -153,6 +153,21 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
     }
 }
 
+// The same for waits that end within a few hundred cycles and stand in a chain of them: the
+// timer is read only every 128 tries (its read takes longer than such a wait).
+__device__ __forceinline__ bool mbar_wait_near(uint64_t* bar, uint32_t parity, uint64_t timeout_ns) {
+    const uint32_t a = smem_u32(bar);
+    uint64_t t0 = 0;
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 128; ++i)
+            if (mbar_try_wait(a, parity)) return true;
+        const uint64_t t = globaltimer();
+        if (t0 == 0) t0 = t;
+        else if (t - t0 > timeout_ns) return false;
+    }
+}
+
 // ---------------------------------------------------------------------------------------
 // TMA (cp.async.bulk.tensor) and L2 cache policies
 // ---------------------------------------------------------------------------------------
@@ -437,6 +452,12 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// maximum of three (a NaN gives way to a number)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 // two fp32 operations in one instruction
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {

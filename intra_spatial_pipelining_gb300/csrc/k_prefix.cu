@@ -20,7 +20,7 @@ namespace sgp {
 
 namespace {
 
-constexpr int kPThreads = 320;
+constexpr int kPThreads = 384;
 constexpr int kPHalf = kPrefixKeys * 128;     // K (or V) bytes of a step
 
 // The groups of the batch, built by every CTA in shared memory.
@@ -155,8 +155,9 @@ __device__ __forceinline__ Step step_at(const Plan& pl, int n, int x) {
     return {lo, i / pl.tiles[lo], i % pl.tiles[lo], r % pl.steps[lo]};
 }
 
-// Warp 0 loads keys and values (TMA, a ring of steps), warp 1 issues the matrix products, warps
-// 2-5 and 6-9 are two softmax groups of 128 rows each.  Per step and group
+// Warp 0 loads keys and values (TMA, a ring of steps), warps 4-7 and 8-11 are two softmax groups
+// of 128 rows each, and warps 1 and 2 issue one group's matrix products each (one warp for both
+// took 2,800 cycles a step to issue them).  Per step and group
 //     S = Q K^T   (M = 128 rows, N = 128 positions, K = 64), accumulators in tensor memory;
 //     P = exp2(scale S - m) by the group's threads, one row each, back to tensor memory as bf16;
 //     O += P V    (M = 128, N = 64, K = 128), P read from tensor memory.
@@ -164,6 +165,9 @@ __device__ __forceinline__ Step step_at(const Plan& pl, int n, int x) {
 // beside the other's products.  A row's maximum m is only raised when it grew by more than 2^8:
 // weights up to 256 lose nothing in bf16 or fp32, and O is rescaled (a round trip through tensor
 // memory) almost never.
+// A thread holds a row's 128 scores in registers: the softmax warps take 208 registers of those
+// that the others give back (384 threads x 168 at launch; 128 x 64 + 256 x 208 is less).  At 168
+// the scores spilled, and a step took 3,600 cycles.
 constexpr int kPStages = 5;
 constexpr int kPRaise = 8;
 constexpr uint32_t kTmemS = 0, kTmemO = 256, kTmemP = 384;  // columns; per group 128, 64, 64
@@ -192,7 +196,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     if (tid == 0) {
         for (int s = 0; s < kPStages; ++s) {
             mbar_init(&bar.kv_full[s], 1);
-            mbar_init(&bar.kv_empty[s], 1);
+            mbar_init(&bar.kv_empty[s], 2);
         }
         for (int h = 0; h < 2; ++h) {
             mbar_init(&bar.q_full[h], 4);
@@ -226,13 +230,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
         *err = 1;
     };
 
+    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 0) {
         if (elect_one()) {
             const uint64_t pol = policy_evict_last();  // the other row tiles read it too
             uint32_t it = 0;
             for (int x = x0; x < x1 && !*err; ++it, ++x) {
                 const uint32_t st = it % kPStages, use = it / kPStages;
-                if (use > 0 && !mbar_wait(&bar.kv_empty[st], (use - 1) & 1u, ctx.timeout_ns)) {
+                if (use > 0 && !mbar_wait_near(&bar.kv_empty[st], (use - 1) & 1u, ctx.timeout_ns)) {
                     gave_up(20);
                     break;
                 }
@@ -245,73 +250,73 @@ __global__ void __launch_bounds__(kPThreads, 1)
             }
             if (*err)  // loads in flight into this CTA's shared memory (bounded)
                 for (uint32_t i = it > kPStages ? it - kPStages : 0; i < it; ++i)
-                    (void)mbar_wait(&bar.kv_full[i % kPStages], (i / kPStages) & 1u, 10000000ull);
+                    (void)mbar_wait_near(&bar.kv_full[i % kPStages], (i / kPStages) & 1u, 10000000ull);
         }
         __syncwarp();
-    } else if (warp == 1) {
+    } else if (warp <= 2) {
         if (elect_one()) {
-            uint32_t it = 0, n_q[2] = {0, 0}, n_s[2] = {0, 0}, n_p[2] = {0, 0};
+            const int h = warp - 1;
             constexpr uint32_t id_s = idesc_bf16_f32(128, kPrefixKeys), id_o = idesc_bf16_f32(128, 64) | kIdescBmn;
-            auto product = [&](uint32_t st, int groups, bool first) {  // O += P V of one step
-                const uint32_t va = smem_u32(ring + st * 2 * kPHalf + kPHalf);
-                for (int h = 0; h < groups; ++h) {
-                    if (!mbar_wait(&bar.p_full[h], n_p[h] & 1u, ctx.timeout_ns)) {
-                        gave_up(21);
-                        return false;
-                    }
-                    ++n_p[h];
-                    tc_fence_after();
-#pragma unroll
-                    for (int k = 0; k < kPrefixKeys / 16; ++k)
-                        tc_mma_bf16_ta(tmem + kTmemO + 64 * h, tmem + kTmemP + 64 * h + 8 * k,
-                                       smem_desc_sw128(va + k * 16 * 128), id_o, !(first && k == 0));
-                    tc_commit(&bar.pv_done[h]);
+            // descriptors advance by address / 16: 32 bytes to the next 16 dims, 16 rows of V
+            const uint64_t dq = smem_desc_sw128(smem_u32(qs + h * 128 * 128));
+            const uint64_t dk0 = smem_desc_sw128(smem_u32(ring)), dv0 = dk0 + kPHalf / 16;
+            const uint32_t ts = tmem + kTmemS + 128 * h, to = tmem + kTmemO + 64 * h, tp = tmem + kTmemP + 64 * h;
+            uint32_t n_q = 0, n = 0;  // tiles and steps of this group
+            uint32_t st = 0, ph = 0, prev = 0;
+            bool ok = true;
+            auto product = [&](bool first) {  // O += P V of step n - 1, in stage prev
+                if (!mbar_wait_near(&bar.p_full[h], (n - 1) & 1u, ctx.timeout_ns)) {
+                    gave_up(21);
+                    return false;
                 }
-                tc_commit(&bar.kv_empty[st]);
+                tc_fence_after();
+                const uint64_t dv = dv0 + prev * (2 * kPHalf / 16);
+#pragma unroll
+                for (int k = 0; k < kPrefixKeys / 16; ++k)
+                    tc_mma_bf16_ta(to, tp + 8 * k, dv + k * (16 * 128 / 16), id_o, !(first && k == 0));
+                tc_commit(&bar.pv_done[h]);
+                tc_commit(&bar.kv_empty[prev]);
                 return true;
             };
-            bool ok = true;
             for (int x = x0; x < x1 && ok;) {
-                const Step s = step_at(pl, n, x);
-                const int end = min(x1, x + pl.steps[s.g] - s.k);
+                const Step s = step_at(pl, P.prefix.n, x);
+                const int steps = min(x1 - x, pl.steps[s.g] - s.k);
                 const int rows = min(P.tile_seqs, pl.base[s.g + 1] - pl.base[s.g] - s.tile * P.tile_seqs) * P.G;
-                const int groups = rows > 128 ? 2 : 1;
-                uint32_t prev = 0;
-                const int begin = x;
-                for (; x < end && ok; ++x, ++it) {
-                    const uint32_t st = it % kPStages;
-                    if (!mbar_wait(&bar.kv_full[st], (it / kPStages) & 1u, ctx.timeout_ns)) {
+                x += steps;
+                if (rows <= 128 * h) {  // no rows here: the stages are free for this group's part
+                    for (int i = 0; i < steps && ok; ++i) {
+                        if (!(ok = mbar_wait_near(&bar.kv_full[st], ph, ctx.timeout_ns))) gave_up(31);
+                        mbar_arrive(&bar.kv_empty[st]);
+                        if (++st == kPStages) st = 0, ph ^= 1;
+                    }
+                    continue;
+                }
+                for (int i = 0; i < steps && ok; ++i) {
+                    ok = mbar_wait_near(&bar.kv_full[st], ph, ctx.timeout_ns);
+                    if (ok && i == 0) ok = mbar_wait_near(&bar.q_full[h], n_q++ & 1u, ctx.timeout_ns);
+                    if (ok && n > 0) ok = mbar_wait_near(&bar.s_free[h], (n - 1) & 1u, ctx.timeout_ns);
+                    if (!ok) {
                         gave_up(22);
-                        ok = false;
                         break;
                     }
-                    const uint32_t ka = smem_u32(ring + st * 2 * kPHalf);
-                    for (int h = 0; h < groups && ok; ++h) {
-                        if (x == begin) ok = mbar_wait(&bar.q_full[h], n_q[h]++ & 1u, ctx.timeout_ns);
-                        if (ok && n_s[h] > 0) ok = mbar_wait(&bar.s_free[h], (n_s[h] - 1) & 1u, ctx.timeout_ns);
-                        if (!ok) {
-                            gave_up(23);
-                            break;
-                        }
-                        ++n_s[h];
-                        tc_fence_after();
-                        const uint32_t qa = smem_u32(qs + h * 128 * 128);
+                    tc_fence_after();
+                    const uint64_t dk = dk0 + st * (2 * kPHalf / 16);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            tc_mma_bf16(tmem + kTmemS + 128 * h, smem_desc_sw128(qa + 32 * k),
-                                        smem_desc_sw128(ka + 32 * k), id_s, k > 0);
-                        tc_commit(&bar.s_full[h]);
-                    }
-                    if (ok && x > begin) ok = product(prev, groups, x == begin + 1);
+                    for (int k = 0; k < 4; ++k) tc_mma_bf16(ts, dq + 2 * k, dk + 2 * k, id_s, k > 0);
+                    tc_commit(&bar.s_full[h]);
+                    if (i > 0) ok = product(i == 1);
+                    ++n;
                     prev = st;
+                    if (++st == kPStages) st = 0, ph ^= 1;
                 }
                 // the last step's product, before a wait for the next tile's queries
-                if (ok) ok = product(prev, groups, end == begin + 1);
+                if (ok) ok = product(steps == 1);
             }
         }
         __syncwarp();
-    } else {
-        const int h = (warp - 2) >> 2, quad = warp & 3;  // a warp reads its quadrant's TMEM lanes
+    } else if (warp >= 4) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        const int h = (warp - 4) >> 2, quad = warp & 3;  // a warp reads its quadrant's TMEM lanes
         const int r = h * 128 + quad * 32 + lane;        // this thread's row of the tile
         const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
         const uint32_t ts = tl + kTmemS + 128 * h, to = tl + kTmemO + 64 * h, tp = tl + kTmemP + 64 * h;
@@ -319,7 +324,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         bool ok = true;
         // every wait's outcome is the warp's: its tensor-memory accesses are warp-wide
         auto wait = [&](uint64_t* bar_, uint32_t parity, uint32_t where) {
-            if (__all_sync(0xffffffffu, mbar_wait(bar_, parity, ctx.timeout_ns))) return true;
+            if (__all_sync(0xffffffffu, mbar_wait_near(bar_, parity, ctx.timeout_ns))) return true;
             if (lane == 0) gave_up(where);
             return false;
         };
@@ -368,9 +373,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 if (!(ok = wait(&bar.s_full[h], it & 1u, 24))) break;
                 tc_fence_after();
                 const int pos0 = (pl.first[s.g] + k) * kPrefixKeys;
-                if (h == 0 && pos0 + kPrefixKeys > len) {
+                if (pos0 + kPrefixKeys > len) {
                     // what lies behind the prefix is arbitrary and its weight is 0: clear V there
-                    // (both groups' products wait for this group's P)
+                    // (each group for its own product; the other's writes are the same zeros)
                     const uint32_t i = (uint32_t)(x - x0), st = i % kPStages;
                     if (!(ok = wait(&bar.kv_full[st], (i / kPStages) & 1u, 27))) break;
                     uint4* v4 = reinterpret_cast<uint4*>(ring + st * 2 * kPHalf + kPHalf);
@@ -405,9 +410,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
+                for (int j = 0; j < 32; j += 2)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], __uint_as_float(sr[c][j]));
+                    for (int c = 0; c < 4; ++c)
+                        mx[c] = max3(mx[c], __uint_as_float(sr[c][j]), __uint_as_float(sr[c][j + 1]));
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * P.scale_log2;
                 // P and O are this thread's once the step before has been multiplied
                 if (x > begin) {
