@@ -164,10 +164,8 @@ __device__ __forceinline__ Step step_at(const Plan& pl, int n, int x) {
 // The next step's S is issued before this step's O product, so that one group's exponentials run
 // beside the other's products.  A row's maximum m is only raised when it grew by more than 2^8:
 // weights up to 256 lose nothing in bf16 or fp32, and O is rescaled (a round trip through tensor
-// memory) almost never.
-// A thread holds a row's 128 scores in registers: the softmax warps take 208 registers of those
-// that the others give back (384 threads x 168 at launch; 128 x 64 + 256 x 208 is less).  At 168
-// the scores spilled, and a step took 3,600 cycles.
+// memory) almost never.  S is read from tensor memory twice, 64 columns at a time, for the maximum
+// and for the weights: held in registers, 128 scores to a thread spilled.
 constexpr int kPStages = 5;
 constexpr int kPRaise = 8;
 constexpr uint32_t kTmemS = 0, kTmemO = 256, kTmemP = 384;  // columns; per group 128, 64, 64
@@ -230,7 +228,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
         *err = 1;
     };
 
-    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 0) {
         if (elect_one()) {
             const uint64_t pol = policy_evict_last();  // the other row tiles read it too
@@ -315,7 +312,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
         __syncwarp();
     } else if (warp >= 4) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int h = (warp - 4) >> 2, quad = warp & 3;  // a warp reads its quadrant's TMEM lanes
         const int r = h * 128 + quad * 32 + lane;        // this thread's row of the tile
         const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
@@ -391,29 +387,30 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     if (lane == 0) mbar_arrive(&bar.p_full[h]);
                     continue;
                 }
-                uint32_t sr[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld_x32(ts + 32 * c, sr[c]);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld_wait32(sr[c]);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.s_free[h]);
                 if (pos0 + kPrefixKeys > len || __any_sync(0xffffffffu, pos0 < low)) {
+                    // hide positions in tensor memory (rare: a loop keeps the code of a step small)
+#pragma unroll 1
+                    for (int c = 0; c < kPrefixKeys; c += 16) {
+                        float v[16];
+                        uint32_t w[16];
+                        tmem_ld_wait_x16(ts + c, v);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const int at = pos0 + c * 32 + j;
-                            if (at >= len || at < low) sr[c][j] = 0xff800000u;  // -inf
+                        for (int j = 0; j < 16; ++j) {
+                            const int at = pos0 + c + j;
+                            w[j] = __float_as_uint(at >= len || at < low ? -INFINITY : v[j]);
                         }
+                        tmem_st_x16(ts + c, w);
+                    }
+                    tmem_st_wait();
                 }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                for (int c = 0; c < kPrefixKeys; c += 64) {
+                    float sr[64];
+                    tmem_ld_wait_x64(ts + c, sr);
 #pragma unroll
-                for (int j = 0; j < 32; j += 2)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        mx[c] = max3(mx[c], __uint_as_float(sr[c][j]), __uint_as_float(sr[c][j + 1]));
+                    for (int j = 0; j < 64; ++j) mx[j & 3] = fmaxf(mx[j & 3], sr[j]);
+                }
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * P.scale_log2;
                 // P and O are this thread's once the step before has been multiplied
                 if (x > begin) {
@@ -427,39 +424,44 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     l2.x *= c;
                     l2.y *= c;
                     if (x > begin) {
-                        uint32_t o[32];
+#pragma unroll 1
+                        for (int q = 0; q < 4; ++q) {
+                            float o[16];
+                            uint32_t w[16];
+                            tmem_ld_wait_x16(to + 16 * q, o);
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            tmem_ld_x32(to + 32 * q, o);
-                            tmem_ld_wait32(o);
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                uint32_t w[16];
-#pragma unroll
-                                for (int j = 0; j < 16; ++j)
-                                    w[j] = __float_as_uint(__uint_as_float(o[e * 16 + j]) * c);
-                                tmem_st_x16(to + 32 * q + 16 * e, w);
-                            }
+                            for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(o[j] * c);
+                            tmem_st_x16(to + 16 * q, w);
                         }
                     }
                 }
                 // a row that has seen nothing yet: every score is -inf, every weight 0
                 const float sub = m == -INFINITY ? 0.f : -m;
                 const float2 sc2 = make_float2(P.scale_log2, P.scale_log2), sub2 = make_float2(sub, sub);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        float2 v = make_float2(__uint_as_float(sr[c][2 * j]), __uint_as_float(sr[c][2 * j + 1]));
-                        v = fma2(v, sc2, sub2);
-                        v.x = ex2(v.x);
-                        v.y = ex2(v.y);
-                        l2 = add2(l2, v);
-                        // the weight's rounding to bf16, the second product's operand type
-                        w[j] = pack_bf16x2(v.x, v.y);
+#pragma unroll 1
+                for (int c = 0; c < kPrefixKeys; c += 64) {
+                    float sr[64];
+                    tmem_ld_wait_x64(ts + c, sr);
+                    if (c + 64 == kPrefixKeys) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar.s_free[h]);
                     }
-                    tmem_st_x16(tp + 16 * c, w);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            float2 v = make_float2(sr[32 * e + 2 * j], sr[32 * e + 2 * j + 1]);
+                            v = fma2(v, sc2, sub2);
+                            v.x = ex2(v.x);
+                            v.y = ex2(v.y);
+                            l2 = add2(l2, v);
+                            // the weight's rounding to bf16, the second product's operand type
+                            w[j] = pack_bf16x2(v.x, v.y);
+                        }
+                        tmem_st_x16(tp + c / 2 + 16 * e, w);
+                    }
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -473,16 +475,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
             if (live) {
                 const size_t slot = b + (size_t)(pl.tile0[s.g] + s.kvh * pl.tiles[s.g] + s.tile);
                 const size_t at = slot * kPrefixRows + r;
+                float o[64];
+                tmem_ld_wait_x64(to, o);
+                if (r < rows) {
+                    float4* dst = reinterpret_cast<float4*>(P.part_acc + at * 64);
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t o[32];
-                    tmem_ld_x32(to + 32 * q, o);
-                    tmem_ld_wait32(o);
-                    if (r < rows) {
-                        uint4* dst = reinterpret_cast<uint4*>(P.part_acc + at * 64 + 32 * q);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-                    }
+                    for (int j = 0; j < 16; ++j) dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
                 }
                 if (r < rows) *reinterpret_cast<float2*>(P.part_ml + at * 2) = make_float2(m, l2.x + l2.y);
             }
