@@ -35,7 +35,7 @@ struct Plan {
     int steps[kPrefixMax];       // steps per tile
     int first[kPrefixMax];       // first step's place in the prefix (in steps)
     int len[kPrefixMax];
-    int low[kPrefixMax];         // least visible position
+    int low[kPrefixMax];         // least position that some sequence of the group sees
 };
 
 // exclusive prefix sums over n <= kPrefixMax values of three arrays by one warp; x[n] = total
@@ -119,6 +119,7 @@ __device__ void build_plan(Plan& pl, const PrefixProblem& P, const KCtx& ctx) {
         const int members = pl.base[g], len = pl.len[g];
         const int first = low / kPrefixKeys;
         const bool some = members > 0 && low < len;
+        pl.low[g] = low;
         pl.first[g] = first;
         pl.tiles[g] = some ? (members + P.tile_seqs - 1) / P.tile_seqs : 0;
         pl.steps[g] = some ? (len + kPrefixKeys - 1) / kPrefixKeys - first : 0;
@@ -156,30 +157,40 @@ __device__ __forceinline__ Step step_at(const Plan& pl, int n, int x) {
 }
 
 // Warp 0 loads keys and values (TMA, a ring of steps), warps 4-7 and 8-11 are two softmax groups
-// of 128 rows each, and warps 1 and 2 issue one group's matrix products each (one warp for both
-// took 2,800 cycles a step to issue them).  Per step and group
-//     S = Q K^T   (M = 128 rows, N = 128 positions, K = 64), accumulators in tensor memory;
+// of 128 rows each, and warps 1 and 2 issue one group's matrix products each.  A step's positions
+// are taken in halves of 64.  Per half and group
+//     S = Q K^T   (M = 128 rows, N = 64 positions, K = 64), accumulators in tensor memory;
 //     P = exp2(scale S - m) by the group's threads, one row each, back to tensor memory as bf16;
-//     O += P V    (M = 128, N = 64, K = 128), P read from tensor memory.
-// The next step's S is issued before this step's O product, so that one group's exponentials run
-// beside the other's products.  A row's maximum m is only raised when it grew by more than 2^8:
-// weights up to 256 lose nothing in bf16 or fp32, and O is rescaled (a round trip through tensor
-// memory) almost never.  S is read from tensor memory twice, 64 columns at a time, for the maximum
-// and for the weights: held in registers, 128 scores to a thread spilled.
+//     O += P V    (M = 128, N = 64 dims, K = 64), P read from tensor memory.
+// S and P have two buffers each, and a half takes one signal either way: the softmax's "P(i) is
+// written" also frees S(i), and the products' "S(i + 2) is complete" also says that O holds P(i)
+// (it was issued behind it).  What a wait costs, 100 to 250 cycles although it passes at once, is
+// what a half has to be long against.
+// The weights are taken against a maximum m that is only raised when a row's scores pass it by
+// more than 2^8 (weights up to 256 lose nothing in bf16 or fp32); the half's own maximum is found
+// beside the exponentials, and in the rare case that it does, O and the sum are rescaled and the
+// half is done again.  m begins at 0, when the first scores are near it.
 constexpr int kPStages = 5;
-constexpr int kPRaise = 8;
-constexpr uint32_t kTmemS = 0, kTmemO = 256, kTmemP = 384;  // columns; per group 128, 64, 64
+constexpr int kPSub = 64;           // positions of a half
+constexpr float kPRaise = 8.f;
+constexpr uint32_t kTmemS = 0, kTmemP = 256, kTmemO = 384;  // columns; per group 2 x 64, 2 x 32, 64
 
 struct PrefixBars {
     uint64_t kv_full[kPStages], kv_empty[kPStages];
-    uint64_t q_full[2];    // the group's query rows are in shared memory
-    uint64_t s_full[2];    // S is complete
-    uint64_t s_free[2];    // the group holds S in registers
-    uint64_t p_full[2];    // P is in tensor memory (and O is rescaled)
-    uint64_t pv_done[2];   // O holds this step, P may be overwritten
+    uint64_t q_full[2];        // the group's query rows are in shared memory
+    uint64_t s_full[2][2];     // [group][buffer]; the group's half i uses buffer i & 1
+    uint64_t p_full[2][2];
+    uint64_t pv_done[2];       // phase i: O holds half i (a rescale and a tile's end wait for it)
     uint32_t tmem;
     int err;
 };
+
+// The part of a tile that a share holds: steps [s.k, s.k + steps), halves of them that hold
+// positions of the prefix.
+__device__ __forceinline__ int halves_of(const Plan& pl, const Step& s, int steps) {
+    const int p0 = (pl.first[s.g] + s.k) * kPrefixKeys;
+    return (min(pl.len[s.g] - p0, steps * kPrefixKeys) + kPSub - 1) / kPSub;
+}
 
 __global__ void __launch_bounds__(kPThreads, 1)
     prefix_attn_kernel(const __grid_constant__ PrefixProblem P, const KCtx ctx) {
@@ -198,10 +209,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
         for (int h = 0; h < 2; ++h) {
             mbar_init(&bar.q_full[h], 4);
-            mbar_init(&bar.s_full[h], 1);
-            mbar_init(&bar.s_free[h], 4);
-            mbar_init(&bar.p_full[h], 4);
             mbar_init(&bar.pv_done[h], 1);
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&bar.s_full[h][i], 1);
+                mbar_init(&bar.p_full[h][i], 4);
+            }
         }
         bar.err = 0;
         fence_barrier_init();
@@ -253,61 +265,70 @@ __global__ void __launch_bounds__(kPThreads, 1)
     } else if (warp <= 2) {
         if (elect_one()) {
             const int h = warp - 1;
-            constexpr uint32_t id_s = idesc_bf16_f32(128, kPrefixKeys), id_o = idesc_bf16_f32(128, 64) | kIdescBmn;
+            constexpr uint32_t id_s = idesc_bf16_f32(128, kPSub), id_o = idesc_bf16_f32(128, 64) | kIdescBmn;
             // descriptors advance by address / 16: 32 bytes to the next 16 dims, 16 rows of V
             const uint64_t dq = smem_desc_sw128(smem_u32(qs + h * 128 * 128));
             const uint64_t dk0 = smem_desc_sw128(smem_u32(ring)), dv0 = dk0 + kPHalf / 16;
+            constexpr int kStageD = 2 * kPHalf / 16, kHalfD = kPSub * 128 / 16;
             const uint32_t ts = tmem + kTmemS + 128 * h, to = tmem + kTmemO + 64 * h, tp = tmem + kTmemP + 64 * h;
-            uint32_t n_q = 0, n = 0;  // tiles and steps of this group
-            uint32_t st = 0, ph = 0, prev = 0;
+            uint32_t n_q = 0, n = 0;               // tiles of this group, halves whose S is issued
+            uint32_t st_s = 0, ph_s = 0, st_p = 0;  // stages of the next S and the next product
             bool ok = true;
-            auto product = [&](bool first) {  // O += P V of step n - 1, in stage prev
-                if (!mbar_wait_near(&bar.p_full[h], (n - 1) & 1u, ctx.timeout_ns)) {
-                    gave_up(21);
-                    return false;
+            auto scores = [&](int j) {  // S = Q K^T of the tile's half j
+                if ((j & 1) == 0 && !(ok = mbar_wait_near(&bar.kv_full[st_s], ph_s, ctx.timeout_ns))) {
+                    gave_up(22);
+                    return;
                 }
-                tc_fence_after();
-                const uint64_t dv = dv0 + prev * (2 * kPHalf / 16);
+                const uint64_t dk = dk0 + st_s * kStageD + (j & 1) * kHalfD;
 #pragma unroll
-                for (int k = 0; k < kPrefixKeys / 16; ++k)
-                    tc_mma_bf16_ta(to, tp + 8 * k, dv + k * (16 * 128 / 16), id_o, !(first && k == 0));
-                tc_commit(&bar.pv_done[h]);
-                tc_commit(&bar.kv_empty[prev]);
-                return true;
+                for (int k = 0; k < 4; ++k) tc_mma_bf16(ts + 64 * (n & 1u), dq + 2 * k, dk + 2 * k, id_s, k > 0);
+                tc_commit(&bar.s_full[h][n & 1u]);
+                ++n;
+                if ((j & 1) && ++st_s == kPStages) st_s = 0, ph_s ^= 1;
             };
             for (int x = x0; x < x1 && ok;) {
                 const Step s = step_at(pl, P.prefix.n, x);
-                const int steps = min(x1 - x, pl.steps[s.g] - s.k);
+                const int steps = min(x1 - x, pl.steps[s.g] - s.k), halves = halves_of(pl, s, steps);
                 const int rows = min(P.tile_seqs, pl.base[s.g + 1] - pl.base[s.g] - s.tile * P.tile_seqs) * P.G;
                 x += steps;
                 if (rows <= 128 * h) {  // no rows here: the stages are free for this group's part
                     for (int i = 0; i < steps && ok; ++i) {
-                        if (!(ok = mbar_wait_near(&bar.kv_full[st], ph, ctx.timeout_ns))) gave_up(31);
-                        mbar_arrive(&bar.kv_empty[st]);
-                        if (++st == kPStages) st = 0, ph ^= 1;
+                        if (!(ok = mbar_wait_near(&bar.kv_full[st_s], ph_s, ctx.timeout_ns))) gave_up(31);
+                        mbar_arrive(&bar.kv_empty[st_s]);
+                        if (++st_s == kPStages) st_s = 0, ph_s ^= 1;
                     }
+                    st_p = st_s;
                     continue;
                 }
-                for (int i = 0; i < steps && ok; ++i) {
-                    ok = mbar_wait_near(&bar.kv_full[st], ph, ctx.timeout_ns);
-                    if (ok && i == 0) ok = mbar_wait_near(&bar.q_full[h], n_q++ & 1u, ctx.timeout_ns);
-                    if (ok && n > 0) ok = mbar_wait_near(&bar.s_free[h], (n - 1) & 1u, ctx.timeout_ns);
-                    if (!ok) {
-                        gave_up(22);
+                if (!(ok = mbar_wait_near(&bar.q_full[h], n_q++ & 1u, ctx.timeout_ns))) {
+                    gave_up(23);
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t n0 = n;  // number of the tile's first half
+                scores(0);
+                if (ok && halves > 1) scores(1);
+                for (int j = 0; j < halves && ok; ++j) {
+                    const uint32_t i = n0 + j, buf = i & 1u;
+                    if (!(ok = mbar_wait_near(&bar.p_full[h][buf], (i >> 1) & 1u, ctx.timeout_ns))) {
+                        gave_up(21);
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t dk = dk0 + st * (2 * kPHalf / 16);
+                    const uint64_t dv = dv0 + st_p * kStageD + (j & 1) * kHalfD;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) tc_mma_bf16(ts, dq + 2 * k, dk + 2 * k, id_s, k > 0);
-                    tc_commit(&bar.s_full[h]);
-                    if (i > 0) ok = product(i == 1);
-                    ++n;
-                    prev = st;
-                    if (++st == kPStages) st = 0, ph ^= 1;
+                    for (int k = 0; k < kPSub / 16; ++k)  // O += P V
+                        tc_mma_bf16_ta(to, tp + 32 * buf + 8 * k, dv + k * (16 * 128 / 16), id_o, !(j == 0 && k == 0));
+                    tc_commit(&bar.pv_done[h]);
+                    if ((j & 1) || j + 1 == halves) {
+                        tc_commit(&bar.kv_empty[st_p]);
+                        if (++st_p == kPStages) st_p = 0;
+                    }
+                    if (j + 2 < halves) scores(j + 2);
                 }
-                // the last step's product, before a wait for the next tile's queries
-                if (ok) ok = product(steps == 1);
+                if (halves & 1) {  // the last stage's second half holds no positions
+                    if (++st_s == kPStages) st_s = 0, ph_s ^= 1;
+                }
             }
         }
         __syncwarp();
@@ -316,7 +337,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const int r = h * 128 + quad * 32 + lane;        // this thread's row of the tile
         const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
         const uint32_t ts = tl + kTmemS + 128 * h, to = tl + kTmemO + 64 * h, tp = tl + kTmemP + 64 * h;
-        uint32_t it = 0;  // steps of this group
+        const int row_of = (65536 + P.G - 1) / P.G;      // r / G = r * row_of >> 16 for r < 256
+        const float2 sc2 = make_float2(P.scale_log2, P.scale_log2);
+        uint32_t it = 0;  // halves of this group
         bool ok = true;
         // every wait's outcome is the warp's: its tensor-memory accesses are warp-wide
         auto wait = [&](uint64_t* bar_, uint32_t parity, uint32_t where) {
@@ -326,14 +349,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
         };
         for (int x = x0; x < x1 && ok;) {
             const Step s = step_at(pl, n, x);
-            const int end = min(x1, x + pl.steps[s.g] - s.k);
+            const int steps = min(x1 - x, pl.steps[s.g] - s.k), halves = halves_of(pl, s, steps);
             const int seq0 = pl.base[s.g] + s.tile * P.tile_seqs;
             const int rows = min(P.tile_seqs, pl.base[s.g + 1] - seq0) * P.G;
-            if (rows <= 128 * h) {
-                x = end;
-                continue;
-            }
-            const int len = pl.len[s.g];
+            const int i0 = x - x0;  // first step's place in the share
+            x += steps;
+            if (rows <= 128 * h) continue;
+            const int len = pl.len[s.g], seen = pl.low[s.g];
             // this warp's 32 query rows, 8 lanes to a row, into the swizzled tile (zeros past the
             // tile's rows: rows do not mix, and theirs are not stored)
             {
@@ -341,11 +363,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 uint4 v[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int q = quad * 32 + i * 4 + (lane >> 3), row = h * 128 + q;
+                    const int row = h * 128 + quad * 32 + i * 4 + (lane >> 3), q = row * row_of >> 16;
                     v[i] = make_uint4(0, 0, 0, 0);
                     if (row < rows) {
-                        const bf16* src = P.q + (size_t)pl.mem[seq0 + row / P.G] * P.nq * 64 +
-                                          (size_t)(s.kvh * P.G + row % P.G) * 64;
+                        const bf16* src = P.q + (size_t)pl.mem[seq0 + q] * P.nq * 64 +
+                                          (size_t)(s.kvh * P.G + row - q * P.G) * 64;
                         v[i] = reinterpret_cast<const uint4*>(src)[lane & 7];
                     }
                 }
@@ -358,115 +380,96 @@ __global__ void __launch_bounds__(kPThreads, 1)
             }
             int low = 0;
             if (P.window > 0 && r < rows) {
-                const int own = P.kv_len[pl.mem[seq0 + r / P.G]];
+                const int own = P.kv_len[pl.mem[seq0 + (r * row_of >> 16)]];
                 low = max(0, len + (own >= 0 && own <= P.kv_cap ? own : 0) - P.window);
             }
             const bool live = h * 128 + quad * 32 < rows;  // some row of this warp counts
-            float m = -INFINITY;  // the maximum the weights are taken against (scaled, base 2)
+            float m = 0.f;  // what the weights are taken against (scaled scores, base 2)
             float2 l2 = make_float2(0.f, 0.f);
-            const int begin = x;
-            for (int k = s.k; x < end; ++x, ++k, ++it) {
-                if (!(ok = wait(&bar.s_full[h], it & 1u, 24))) break;
+            int pos0 = (pl.first[s.g] + s.k) * kPrefixKeys;
+            for (int j = 0; j < halves; ++j, ++it, pos0 += kPSub) {
+                const uint32_t buf = it & 1u;
+                if (!(ok = wait(&bar.s_full[h][buf], (it >> 1) & 1u, 24))) break;
                 tc_fence_after();
-                const int pos0 = (pl.first[s.g] + k) * kPrefixKeys;
-                if (pos0 + kPrefixKeys > len) {
-                    // what lies behind the prefix is arbitrary and its weight is 0: clear V there
-                    // (each group for its own product; the other's writes are the same zeros)
-                    const uint32_t i = (uint32_t)(x - x0), st = i % kPStages;
+                if (pos0 + kPSub > len || pos0 < seen) {
+                    // what lies behind the prefix, or before what any sequence of the group sees,
+                    // is arbitrary and its weight is 0: clear V there (each group of warps for its
+                    // own product; the other's writes are the same zeros)
+                    const uint32_t i = i0 + (j >> 1), st = i % kPStages;
                     if (!(ok = wait(&bar.kv_full[st], (i / kPStages) & 1u, 27))) break;
-                    uint4* v4 = reinterpret_cast<uint4*>(ring + st * 2 * kPHalf + kPHalf);
-                    for (int e = (len - pos0) * 8 + quad * 32 + lane; e < kPrefixKeys * 8; e += 128)
-                        v4[e] = make_uint4(0, 0, 0, 0);
+                    uint4* v4 = reinterpret_cast<uint4*>(ring + st * 2 * kPHalf + kPHalf + (j & 1) * kPSub * 128);
+                    for (int e = quad * 32 + lane; e < kPSub * 8; e += 128)
+                        if (pos0 + (e >> 3) >= len || pos0 + (e >> 3) < seen) v4[e] = make_uint4(0, 0, 0, 0);
                     fence_proxy_async();
                 }
-                if (!live) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.s_free[h]);
-                    // one arrival for every step: not before the step before is through
-                    if (x > begin && !(ok = wait(&bar.pv_done[h], (it - 1) & 1u, 28))) break;
-                    if (lane == 0) mbar_arrive(&bar.p_full[h]);
-                    continue;
-                }
-                if (pos0 + kPrefixKeys > len || __any_sync(0xffffffffu, pos0 < low)) {
-                    // hide positions in tensor memory (rare: a loop keeps the code of a step small)
+                if (live) {
+                    if (pos0 + kPSub > len || __any_sync(0xffffffffu, pos0 < low)) {
+                        // hide positions in tensor memory (rare: a loop keeps the code small)
 #pragma unroll 1
-                    for (int c = 0; c < kPrefixKeys; c += 16) {
-                        float v[16];
-                        uint32_t w[16];
-                        tmem_ld_wait_x16(ts + c, v);
+                        for (int c = 0; c < kPSub; c += 16) {
+                            float v[16];
+                            uint32_t w[16];
+                            tmem_ld_wait_x16(ts + 64 * buf + c, v);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const int at = pos0 + c + j;
-                            w[j] = __float_as_uint(at >= len || at < low ? -INFINITY : v[j]);
+                            for (int e = 0; e < 16; ++e) {
+                                const int at = pos0 + c + e;
+                                w[e] = __float_as_uint(at >= len || at < low ? -INFINITY : v[e]);
+                            }
+                            tmem_st_x16(ts + 64 * buf + c, w);
                         }
-                        tmem_st_x16(ts + c, w);
+                        tmem_st_wait();
                     }
-                    tmem_st_wait();
-                }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-                for (int c = 0; c < kPrefixKeys; c += 64) {
-                    float sr[64];
-                    tmem_ld_wait_x64(ts + c, sr);
+                    const float2 l_old = l2;
+                    while (true) {
+                        // a row that has seen nothing yet: every score is -inf, every weight 0
+                        const float sub = m == -INFINITY ? 0.f : -m;
+                        const float2 sub2 = make_float2(sub, sub);
+                        float sr[64], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        tmem_ld_wait_x64(ts + 64 * buf, sr);
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) mx[j & 3] = fmaxf(mx[j & 3], sr[j]);
-                }
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * P.scale_log2;
-                // P and O are this thread's once the step before has been multiplied
-                if (x > begin) {
-                    if (!(ok = wait(&bar.pv_done[h], (it - 1) & 1u, 25))) break;
-                    tc_fence_after();
-                }
-                if (__any_sync(0xffffffffu, top > m + kPRaise)) {
-                    const float nm = fmaxf(m, top);
-                    const float c = m == -INFINITY ? 0.f : ex2(m - nm);
-                    m = nm;
-                    l2.x *= c;
-                    l2.y *= c;
-                    if (x > begin) {
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t w[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                float2 v = make_float2(sr[32 * c + 2 * e], sr[32 * c + 2 * e + 1]);
+                                mx[e & 1] = fmaxf(mx[e & 1], v.x);
+                                mx[2 + (e & 1)] = fmaxf(mx[2 + (e & 1)], v.y);
+                                v = fma2(v, sc2, sub2);
+                                v.x = ex2(v.x);
+                                v.y = ex2(v.y);
+                                l2 = add2(l2, v);
+                                // the weight's rounding to bf16, the second product's operand type
+                                w[e] = pack_bf16x2(v.x, v.y);
+                            }
+                            tmem_st_x16(tp + 32 * buf + 16 * c, w);
+                        }
+                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * P.scale_log2;
+                        // the first half also raises from below: its scores may be far under 0
+                        const bool far = top > m + kPRaise || (j == 0 && m == 0.f && top < -kPRaise);
+                        if (!__any_sync(0xffffffffu, far)) break;
+                        const float nm = j == 0 ? top : fmaxf(m, top);
+                        const float c = j == 0 || m == -INFINITY ? 0.f : ex2(m - nm);
+                        m = nm;
+                        l2 = make_float2(l_old.x * c, l_old.y * c);
+                        if (j == 0) continue;
+                        if (!(ok = wait(&bar.pv_done[h], (it - 1) & 1u, 25))) break;
+                        tc_fence_after();
 #pragma unroll 1
-                        for (int q = 0; q < 4; ++q) {
+                        for (int q = 0; q < 64; q += 16) {
                             float o[16];
                             uint32_t w[16];
-                            tmem_ld_wait_x16(to + 16 * q, o);
+                            tmem_ld_wait_x16(to + q, o);
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(o[j] * c);
-                            tmem_st_x16(to + 16 * q, w);
+                            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * c);
+                            tmem_st_x16(to + q, w);
                         }
                     }
+                    if (!ok) break;
+                    tmem_st_wait();
                 }
-                // a row that has seen nothing yet: every score is -inf, every weight 0
-                const float sub = m == -INFINITY ? 0.f : -m;
-                const float2 sc2 = make_float2(P.scale_log2, P.scale_log2), sub2 = make_float2(sub, sub);
-#pragma unroll 1
-                for (int c = 0; c < kPrefixKeys; c += 64) {
-                    float sr[64];
-                    tmem_ld_wait_x64(ts + c, sr);
-                    if (c + 64 == kPrefixKeys) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar.s_free[h]);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float2 v = make_float2(sr[32 * e + 2 * j], sr[32 * e + 2 * j + 1]);
-                            v = fma2(v, sc2, sub2);
-                            v.x = ex2(v.x);
-                            v.y = ex2(v.y);
-                            l2 = add2(l2, v);
-                            // the weight's rounding to bf16, the second product's operand type
-                            w[j] = pack_bf16x2(v.x, v.y);
-                        }
-                        tmem_st_x16(tp + c / 2 + 16 * e, w);
-                    }
-                }
-                tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.p_full[h]);
+                if (lane == 0) mbar_arrive(&bar.p_full[h][buf]);
             }
             if (!ok) break;
             // the last product, then this row's partial
@@ -481,8 +484,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     float4* dst = reinterpret_cast<float4*>(P.part_acc + at * 64);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                    *reinterpret_cast<float2*>(P.part_ml + at * 2) = make_float2(m, l2.x + l2.y);
                 }
-                if (r < rows) *reinterpret_cast<float2*>(P.part_ml + at * 2) = make_float2(m, l2.x + l2.y);
             }
             tc_fence_before();
         }
