@@ -137,11 +137,7 @@ __device__ void merge_pair(const AttnProblem& P, int t, int kvh, int S_t, int la
     }
 }
 
-// PART: the own-cache part of an attention over a shared prefix and an own cache.  Lengths of
-// zero are legal and every chunk leaves its partial: the merge with the prefix's partials is
-// another kernel's (k_prefix.cu).  (A window reaches L - window back in the own cache whatever
-// lies before it.)
-template <int NT, int NW, int POS, bool SPLIT, bool PART>
+template <int NT, int NW, int POS, bool SPLIT>
 __global__ void __launch_bounds__(NW * 32, 1)
     attn_decode_kernel(const __grid_constant__ AttnProblem P, const KCtx ctx) {
     constexpr int kAWarps = NW;                    // streaming warps per CTA
@@ -172,7 +168,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
             if (t < P.nrows) {
                 const int L = P.kv_len[P.row0 + t];
                 kvl[t] = L;
-                if (L < (PART ? 0 : 1) || L > P.cap) {
+                if (L < 1 || L > P.cap) {
                     if (blockIdx.x == 0) report(ctx, ST_BOUNDS, (uint32_t)L);
                 } else {
                     const int first = P.window > 0 ? max(0, L - P.window) : 0;
@@ -430,7 +426,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
                     l_run[nt][1] += __shfl_xor_sync(0xffffffffu, l_run[nt][1], o);
                 }
             const size_t pair = (size_t)cs.t * P.nkv + cs.kvh;
-            if (!PART && cs.S_t == 1) {
+            if (cs.S_t == 1) {
                 bf16* o = P.o + (size_t)(P.row0 + cs.t) * (P.nq * 64) + (size_t)(cs.kvh * P.G) * 64;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -467,19 +463,17 @@ __global__ void __launch_bounds__(NW * 32, 1)
                         *reinterpret_cast<float4*>(pml + 2 * h) =
                             make_float4(m_run[nt][0], l_run[nt][0], m_run[nt][1], l_run[nt][1]);
                 }
-                if constexpr (!PART) {
+                __threadfence();
+                __syncwarp();
+                int last = 0;
+                if (lane == 0) {
+                    const uint32_t prev = atomicAdd(&P.cnt[pair], 1u);
+                    last = prev == (uint32_t)cs.S_t - 1;
+                    if (last) P.cnt[pair] = 0;
+                }
+                if (__shfl_sync(0xffffffffu, last, 0)) {
                     __threadfence();
-                    __syncwarp();
-                    int last = 0;
-                    if (lane == 0) {
-                        const uint32_t prev = atomicAdd(&P.cnt[pair], 1u);
-                        last = prev == (uint32_t)cs.S_t - 1;
-                        if (last) P.cnt[pair] = 0;
-                    }
-                    if (__shfl_sync(0xffffffffu, last, 0)) {
-                        __threadfence();
-                        merge_pair<NT>(P, cs.t, cs.kvh, cs.S_t, lane);
-                    }
+                    merge_pair<NT>(P, cs.t, cs.kvh, cs.S_t, lane);
                 }
             }
         }
@@ -509,19 +503,12 @@ int enqueue_attention(Launcher& L, const AttnProblem& p, const KCtx& c) {
     const size_t smem = (size_t)nw * 2 * p.pos * 128 + 1024 + nw * 2 * 8 +
                         (2 * kAMaxRows + 1) * 4;
     void* args[] = {(void*)&p, (void*)&c};
-    if (p.part) {  // [pos == 64][G > 8]; alone on the GPU: always the split schedule
-        static const void* const part[2][2] = {
-            {(const void*)attn_decode_kernel<1, 6, 128, true, true>, (const void*)attn_decode_kernel<2, 6, 128, true, true>},
-            {(const void*)attn_decode_kernel<1, 12, 64, true, true>, (const void*)attn_decode_kernel<2, 12, 64, true, true>}};
-        // kv_len may come from the kernel before this one (an eviction): no programmatic launch
-        return L.launch(part[p.pos == 64][p.G > 8], grid, block, smem, args, false);
-    }
     // [pos == 64][G > 8][kv_split]
     static const void* const kern[2][2][2] = {
-        {{(const void*)attn_decode_kernel<1, 6, 128, false, false>, (const void*)attn_decode_kernel<1, 6, 128, true, false>},
-         {(const void*)attn_decode_kernel<2, 6, 128, false, false>, (const void*)attn_decode_kernel<2, 6, 128, true, false>}},
-        {{(const void*)attn_decode_kernel<1, 12, 64, false, false>, (const void*)attn_decode_kernel<1, 12, 64, true, false>},
-         {(const void*)attn_decode_kernel<2, 12, 64, false, false>, (const void*)attn_decode_kernel<2, 12, 64, true, false>}}};
+        {{(const void*)attn_decode_kernel<1, 6, 128, false>, (const void*)attn_decode_kernel<1, 6, 128, true>},
+         {(const void*)attn_decode_kernel<2, 6, 128, false>, (const void*)attn_decode_kernel<2, 6, 128, true>}},
+        {{(const void*)attn_decode_kernel<1, 12, 64, false>, (const void*)attn_decode_kernel<1, 12, 64, true>},
+         {(const void*)attn_decode_kernel<2, 12, 64, false>, (const void*)attn_decode_kernel<2, 12, 64, true>}}};
     const void* f = kern[p.pos == 64][p.G > 8][p.kv_split != 0];
     return L.launch(f, grid, block, smem, args, true);
 }

@@ -5,12 +5,14 @@
 //   o   = sum_p softmax(s)_p v_p,   lse = log sum_p exp(s_p).
 // Softmax splits over any cut of the positions: with m = max s, l = sum exp(s - m) and
 // a = sum exp(s - m) v of each part, the whole has M = max m, L = sum l exp(m - M) and
-// o = sum a exp(m - M) / L.  Three kernels: the own caches (attn_decode_kernel, partials only),
-// the prefixes (here), the merge (here).
+// o = sum a exp(m - M) / L.
 //
-// A prefix is read once for all query rows of its group (sequences x heads of one KV head),
-// so the prefix part is a matrix product, not a stream: 4 d flops for every (row, position)
-// against 256 bytes for every position.
+// Two kernels.  In the first, some CTAs take the prefixes and the others the own caches, and every
+// part leaves its (m, l, a); the second merges them.  A prefix is read once for all query rows of
+// its group (sequences x heads of one KV head), so the prefix part is a matrix product on tcgen05,
+// 4 d flops for every (row, position) against 256 bytes for every position; the own part is a
+// stream of the caches through warp-level products, bound by HBM.  Side by side, each has what
+// the other leaves idle.
 #include <climits>
 
 #include "kernels.h"
@@ -21,6 +23,9 @@ namespace sgp {
 namespace {
 
 constexpr int kPThreads = 384;
+constexpr int kOwnWarps = kPThreads / 32;
+constexpr int kOwnPos = 64;                  // positions of an own warp's stage
+constexpr int kOwnHalf = kOwnPos * 128;      // K (or V) bytes of it
 constexpr int kPHalf = kPrefixKeys * 128;     // K (or V) bytes of a step
 
 // The groups of the batch, built by every CTA in shared memory.
@@ -36,6 +41,11 @@ struct Plan {
     int first[kPrefixMax];       // first step's place in the prefix (in steps)
     int len[kPrefixMax];
     int low[kPrefixMax];         // least position that some sequence of the group sees
+    int chunk0[kPrefixMax + 1];  // own chunks (all KV heads) before a sequence
+    int own_first[kPrefixMax];   // first own position seen
+    int own_len[kPrefixMax];
+    long long own_pos;           // own positions seen, of all sequences
+    int n_own;                   // CTAs that take the own caches; the others take the prefixes
 };
 
 // exclusive prefix sums over n <= kPrefixMax values of three arrays by one warp; x[n] = total
@@ -71,9 +81,31 @@ __device__ __forceinline__ void scan3(int* a, int* b, int* c, int n, int lane) {
     }
 }
 
+// CTAs that take the own caches: what makes the slower part fastest, of the multiples of 8.  An own
+// CTA streams 100 GB/s (measured on partial pools) up to 6.6 TB/s together, a prefix CTA takes
+// 1.5 us for a step; beginning and end cost 4 and 6 us.
+__device__ __forceinline__ int own_ctas(long long own_pos, int nkv, int steps, int lane) {
+    const int x = lane < 19 ? 8 * lane : kPrefixCtas, y = kPrefixCtas - x;
+    const float own = x > 0 ? 4000.f + (float)own_pos * (float)(nkv * 256) / fminf(100.f * x, 6600.f) : 0.f;
+    const float pre = y > 0 ? 6000.f + 1500.f * (float)((steps + y - 1) / y) : 0.f;
+    float cost = fmaxf(own, pre);
+    if (lane > 19 || (x == 0 && own_pos > 0) || (y == 0 && steps > 0)) cost = INFINITY;
+    int best = x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float c = __shfl_xor_sync(0xffffffffu, cost, o);
+        const int z = __shfl_xor_sync(0xffffffffu, best, o);
+        if (c < cost || (c == cost && z < best)) {
+            cost = c;
+            best = z;
+        }
+    }
+    return best;
+}
+
 __device__ void build_plan(Plan& pl, const PrefixProblem& P, const KCtx& ctx) {
     const int tid = threadIdx.x, lane = tid & 31, n = P.prefix.n;
-    for (int g = tid; g < n; g += blockDim.x) {
+    for (int g = tid; g < n; g += kPThreads) {
         int len = P.prefix.len[g];
         if (len < 0 || len > P.prefix.cap) {
             if (blockIdx.x == 0) report(ctx, ST_BOUNDS, (uint32_t)len);
@@ -83,38 +115,71 @@ __device__ void build_plan(Plan& pl, const PrefixProblem& P, const KCtx& ctx) {
         pl.low[g] = INT_MAX;
         pl.base[g] = 0;  // members, until the scan
     }
-    for (int t = tid; t < P.T; t += blockDim.x) {
-        const int g = P.prefix.of[t];
-        if (g >= n && blockIdx.x == 0) report(ctx, ST_BOUNDS, (uint32_t)g);
-        pl.of[t] = g >= 0 && g < n ? g : -1;
+    for (int t = tid; t < P.T; t += kPThreads) {
+        int g = -1;
+        if (n > 0) {
+            g = P.prefix.of[t];
+            if (g >= n && blockIdx.x == 0) report(ctx, ST_BOUNDS, (uint32_t)g);
+            if (g >= n || g < 0) g = -1;
+        }
+        int own = P.kv_len[t];
+        if (own < 0 || own > P.kv_cap) {
+            if (blockIdx.x == 0) report(ctx, ST_BOUNDS, (uint32_t)own);
+            own = 0;
+        }
+        pl.of[t] = g;
+        pl.own_len[t] = own;
+        // a window reaches as far back in the own cache whatever lies before it
+        pl.own_first[t] = P.window > 0 ? max(0, own - P.window) : 0;
     }
     __syncthreads();
-    // place of every sequence in its group: 32 sequences a round, counts kept per group
     if (tid < 32) {
+        // place of every sequence in its group: 32 sequences a round, counts kept per group
+        if (n > 0)
+            for (int t0 = 0; t0 < P.T; t0 += 32) {
+                const int t = t0 + lane;
+                const int g = t < P.T ? pl.of[t] : -1;
+                const unsigned same = __match_any_sync(0xffffffffu, g);
+                const int before = __popc(same & ((1u << lane) - 1u));
+                const int had = g >= 0 ? pl.base[g] : 0;
+                __syncwarp();
+                if (g >= 0) {
+                    pl.rank[t] = had + before;
+                    if (before == 0) pl.base[g] = had + __popc(same);
+                }
+                __syncwarp();
+            }
+    } else if (tid < 64) {
+        int run = 0;
+        long long pos = 0;
         for (int t0 = 0; t0 < P.T; t0 += 32) {
             const int t = t0 + lane;
-            const int g = t < P.T ? pl.of[t] : -1;
-            const unsigned same = __match_any_sync(0xffffffffu, g);
-            const int before = __popc(same & ((1u << lane) - 1u));
-            const int had = g >= 0 ? pl.base[g] : 0;
-            __syncwarp();
-            if (g >= 0) {
-                pl.rank[t] = had + before;
-                if (before == 0) pl.base[g] = had + __popc(same);
+            const int seen = t < P.T ? pl.own_len[t] - pl.own_first[t] : 0;
+            const int cnt = (seen + P.chunk - 1) / P.chunk * P.nkv;
+            int incl = cnt;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
             }
-            __syncwarp();
+            if (t < P.T) pl.chunk0[t] = run + incl - cnt;
+            run += __shfl_sync(0xffffffffu, incl, 31);
+            pos += seen;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) pos += __shfl_xor_sync(0xffffffffu, pos, o);
+        if (lane == 0) {
+            pl.chunk0[P.T] = run;
+            pl.own_pos = pos;
+        }
+    } else if (P.window > 0) {
+        for (int t = tid - 64; t < P.T; t += kPThreads - 64) {
+            const int g = pl.of[t];
+            if (g >= 0) atomicMin(&pl.low[g], max(0, pl.len[g] + pl.own_len[t] - P.window));
         }
     }
-    if (P.window > 0)
-        for (int t = tid; t < P.T; t += blockDim.x) {
-            const int g = pl.of[t];
-            if (g < 0) continue;
-            const int own = P.kv_len[t];
-            const int at = pl.len[g] + (own >= 0 && own <= P.kv_cap ? own : 0) - P.window;
-            atomicMin(&pl.low[g], max(0, at));
-        }
     __syncthreads();
-    for (int g = tid; g < n; g += blockDim.x) {
+    for (int g = tid; g < n; g += kPThreads) {
         const int low = P.window > 0 ? pl.low[g] : 0;
         const int members = pl.base[g], len = pl.len[g];
         const int first = low / kPrefixKeys;
@@ -127,16 +192,19 @@ __device__ void build_plan(Plan& pl, const PrefixProblem& P, const KCtx& ctx) {
         pl.step0[g] = pl.tile0[g] * pl.steps[g];
     }
     __syncthreads();
-    if (tid < 32) scan3(pl.base, pl.tile0, pl.step0, n, lane);
+    if (tid < 32) {
+        scan3(pl.base, pl.tile0, pl.step0, n, lane);
+        __syncwarp();
+        const int x = own_ctas(pl.own_pos, P.nkv, pl.step0[n], lane);
+        if (lane == 0) pl.n_own = x;
+    }
     __syncthreads();
-    for (int t = tid; t < P.T; t += blockDim.x) {
-        const int g = pl.of[t];
+    for (int t = tid; t < P.T; t += kPThreads) {
+        const int g = pl.of[t], total = pl.step0[n], shares = min(kPrefixCtas - pl.n_own, total);
         if (g >= 0) pl.mem[pl.base[g] + pl.rank[t]] = t;
-        if (blockIdx.x == 0) {
-            PrefixSeq s = {0, 0, 0, 0, 0, pl.step0[n], {0, 0}};
-            if (g >= 0) s = {pl.tile0[g], pl.tiles[g], pl.step0[g], pl.steps[g], pl.rank[t], pl.step0[n], {0, 0}};
-            P.seq[t] = s;
-        }
+        if (blockIdx.x == 0)
+            P.seq[t] = g >= 0 ? PrefixSeq{pl.tile0[g], pl.tiles[g], pl.step0[g], pl.steps[g], pl.rank[t], total, shares, 0}
+                              : PrefixSeq{0, 0, 0, 0, 0, total, shares, 0};
     }
     __syncthreads();
 }
@@ -156,7 +224,210 @@ __device__ __forceinline__ Step step_at(const Plan& pl, int n, int x) {
     return {lo, i / pl.tiles[lo], i % pl.tiles[lo], r % pl.steps[lo]};
 }
 
-// Warp 0 loads keys and values (TMA, a ring of steps), warps 4-7 and 8-11 are two softmax groups
+// The own caches: independent warps, each with a private stage of 64 positions, K and V halves
+// refilled by themselves (K as soon as the scores are computed, V after its product), as the decode
+// layer's attention streams its caches.  S^T = K q^T and O^T += V^T P^T on warp-level products, the
+// heads of a group their N; a chunk's (m, l, a) go to its partial.
+struct OwnChunk {
+    int i, t, kvh, c, p0, p1;
+};
+__device__ __forceinline__ OwnChunk own_chunk(const Plan& pl, const PrefixProblem& P, int i) {
+    int lo = 0, hi = P.T;  // the last sequence whose chunks begin at or before i
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pl.chunk0[mid] <= i) lo = mid;
+        else hi = mid;
+    }
+    const int per = (pl.chunk0[lo + 1] - pl.chunk0[lo]) / P.nkv, r = i - pl.chunk0[lo];
+    const int kvh = r / per, c = r - kvh * per, p0 = pl.own_first[lo] + c * P.chunk;
+    return {i, lo, kvh, c, p0, min(pl.own_len[lo], p0 + P.chunk)};
+}
+
+template <int NT>
+__device__ void own_part(const PrefixProblem& P, const Plan& pl, uint8_t* ring_all, uint64_t* bars,
+                         const KCtx& ctx) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, cq = lane & 3;
+    const long long total = pl.chunk0[P.T], W = (long long)pl.n_own * kOwnWarps;
+    const long long gw = (long long)warp * pl.n_own + blockIdx.x;
+    const int i1 = (int)((gw + 1) * total / W);
+    int i = (int)(gw * total / W);
+    if (i >= i1) return;
+    uint8_t* ring = ring_all + (size_t)warp * 2 * kOwnHalf;
+    uint64_t *bar_k = bars + 2 * warp, *bar_v = bar_k + 1;
+    const uint32_t ka = smem_u32(ring), va = ka + kOwnHalf;
+    const uint64_t pol = policy_evict_first();
+    OwnChunk cs = own_chunk(pl, P, i), ld = cs;
+    int ld_p = ld.p0, v_row = 0;
+    uint32_t n_k = 0, n_v = 0, c_k = 0, c_v = 0;  // halves issued and consumed
+    auto issue_k = [&] {
+        v_row = (ld.t * P.nkv + ld.kvh) * P.kv_cap + ld_p;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(bar_k, kOwnHalf);
+            tma_load_2d(ring, &P.tmK, bar_k, 0, v_row, pol);
+        }
+        ++n_k;
+        ld_p += kOwnPos;
+        if (ld_p >= ld.p1) {
+            if (ld.i + 1 < i1) ld = own_chunk(pl, P, ld.i + 1);
+            else ld.i = i1;
+            ld_p = ld.p0;
+        }
+    };
+    auto issue_v = [&] {
+        if (lane == 0) {
+            mbar_arrive_expect_tx(bar_v, kOwnHalf);
+            tma_load_2d(ring + kOwnHalf, &P.tmV, bar_v, 0, v_row, pol);
+        }
+        ++n_v;
+    };
+    issue_k();
+    issue_v();
+    uint32_t qf[NT][4][2];
+    float m[NT][2], l[NT][2], o[4][NT][4];
+    int pair = -1;
+    bool ok = true;
+    for (; i < i1 && ok; ++i) {
+        if (i > cs.i) cs = own_chunk(pl, P, i);
+        if (cs.t * P.nkv + cs.kvh != pair) {  // query fragments of the new (sequence, KV head)
+            pair = cs.t * P.nkv + cs.kvh;
+            const bf16* q = P.q + (size_t)cs.t * P.nq * 64 + (size_t)cs.kvh * P.G * 64;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    const int h = nt * 8 + g;
+                    const uint32_t* src = reinterpret_cast<const uint32_t*>(q + h * 64 + kk * 16 + 2 * cq);
+                    qf[nt][kk][0] = h < P.G ? src[0] : 0u;
+                    qf[nt][kk][1] = h < P.G ? src[4] : 0u;
+                }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            m[nt][0] = m[nt][1] = -INFINITY;
+            l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+            for (int md = 0; md < 4; ++md) o[md][nt][0] = o[md][nt][1] = o[md][nt][2] = o[md][nt][3] = 0.f;
+        }
+        for (int p = cs.p0; p < cs.p1; p += kOwnPos) {
+            if (__any_sync(0xffffffffu, !mbar_wait(bar_k, c_k & 1u, ctx.timeout_ns))) {
+                if (lane == 0) report(ctx, ST_TIMEOUT, 40);
+                ok = false;
+                break;
+            }
+            ++c_k;
+            const int valid = min(kOwnPos, cs.p1 - p);
+            float s[4][NT][4];
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.f;
+                const int r = mt * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    uint32_t a[4];
+                    ldsm_x4(ka + sw128(r, kk * 2 + (lane >> 4)), a);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma16816(s[mt][nt], a, qf[nt][kk][0], qf[nt][kk][1]);
+                }
+            }
+            // K is consumed: the next keys load beside the softmax and the V product
+            fence_proxy_async();
+            __syncwarp();
+            if (ld.i < i1) issue_k();
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float v = s[mt][nt][e] * P.scale_log2;
+                        if (mt * 16 + (e >> 1) * 8 + g >= valid) v = -INFINITY;
+                        s[mt][nt][e] = v;
+                        mx[e & 1] = fmaxf(mx[e & 1], v);
+                    }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], d));
+                    const float nm = fmaxf(m[nt][e], mx[e]);
+                    const float c = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - nm);
+                    const float sub = nm == -INFINITY ? 0.f : nm;
+                    m[nt][e] = nm;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                        for (int f = 0; f < 2; ++f) {
+                            const float w = ex2(s[mt][nt][2 * f + e] - sub);
+                            s[mt][nt][2 * f + e] = w;
+                            sum += w;
+                        }
+                    l[nt][e] = l[nt][e] * c + sum;
+#pragma unroll
+                    for (int md = 0; md < 4; ++md) {
+                        o[md][nt][e] *= c;
+                        o[md][nt][2 + e] *= c;
+                    }
+                }
+            }
+            if (__any_sync(0xffffffffu, !mbar_wait(bar_v, c_v & 1u, ctx.timeout_ns))) {
+                if (lane == 0) report(ctx, ST_TIMEOUT, 41);
+                ok = false;
+                break;
+            }
+            ++c_v;
+            if (valid < kOwnPos) {  // what lies behind the chunk is arbitrary: its weight is 0
+                uint4* v4 = reinterpret_cast<uint4*>(ring + kOwnHalf);
+                for (int e = valid * 8 + lane; e < kOwnPos * 8; e += 32) v4[e] = make_uint4(0, 0, 0, 0);
+                __syncwarp();
+            }
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+                uint32_t b0[NT], b1[NT];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    b0[nt] = movmatrix_t(pack_bf16x2(s[ks][nt][0], s[ks][nt][1]));
+                    b1[nt] = movmatrix_t(pack_bf16x2(s[ks][nt][2], s[ks][nt][3]));
+                }
+                const int r = ks * 16 + ((lane >> 4) << 3) + (lane & 7);
+#pragma unroll
+                for (int md = 0; md < 4; ++md) {
+                    uint32_t a[4];
+                    ldsm_x4_t(va + sw128(r, md * 2 + ((lane >> 3) & 1)), a);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma16816(o[md][nt], a, b0[nt], b1[nt]);
+                }
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (n_v < n_k) issue_v();
+        }
+        if (!ok) break;
+        const size_t at = ((size_t)pair * P.S_max + cs.c) * 16;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], d);
+                const int h = nt * 8 + 2 * cq + e;
+                if (h >= P.G) continue;
+                if (g == 0) *reinterpret_cast<float2*>(P.own_ml + (at + h) * 2) = make_float2(m[nt][e], l[nt][e]);
+                float* acc = P.own_acc + (at + h) * 64 + g;
+#pragma unroll
+                for (int md = 0; md < 4; ++md) {
+                    acc[md * 16] = o[md][nt][e];
+                    acc[md * 16 + 8] = o[md][nt][2 + e];
+                }
+            }
+    }
+    // loads in flight into this warp's stage, if it gave up (bounded)
+    for (; c_k < n_k; ++c_k) (void)mbar_wait(bar_k, c_k & 1u, 10000000ull);
+    for (; c_v < n_v; ++c_v) (void)mbar_wait(bar_v, c_v & 1u, 10000000ull);
+}
+
+// The prefixes.  Warp 0 loads keys and values (TMA, a ring of steps), warps 4-7 and 8-11 are two softmax groups
 // of 128 rows each, and warps 1 and 2 issue one group's matrix products each.  A step's positions
 // are taken in halves of 64.  Per half and group
 //     S = Q K^T   (M = 128 rows, N = 64 positions, K = 64), accumulators in tensor memory;
@@ -181,6 +452,7 @@ struct PrefixBars {
     uint64_t s_full[2][2];     // [group][buffer]; the group's half i uses buffer i & 1
     uint64_t p_full[2][2];
     uint64_t pv_done[2];       // phase i: O holds half i (a rescale and a tile's end wait for it)
+    uint64_t own[kOwnWarps][2];  // an own warp's K and V halves
     uint32_t tmem;
     int err;
 };
@@ -192,16 +464,19 @@ __device__ __forceinline__ int halves_of(const Plan& pl, const Step& s, int step
     return (min(pl.len[s.g] - p0, steps * kPrefixKeys) + kPSub - 1) / kPSub;
 }
 
+template <int NT>
 __global__ void __launch_bounds__(kPThreads, 1)
     prefix_attn_kernel(const __grid_constant__ PrefixProblem P, const KCtx ctx) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* qs = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));  // [2][128 rows]
-    uint8_t* ring = qs + 2 * 128 * 128;
+    uint8_t* ring = qs + 2 * 128 * 128;  // (the own warps' stages take the place of both)
+    static_assert(2 * 128 * 128 + kPStages * 2 * kPHalf >= kOwnWarps * 2 * kOwnHalf, "own stages fit");
     PrefixBars& bar = *reinterpret_cast<PrefixBars*>(ring + kPStages * 2 * kPHalf);
     Plan& pl = *reinterpret_cast<Plan*>(&bar + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     griddep_launch();
+    griddep_wait();
     if (tid == 0) {
         for (int s = 0; s < kPStages; ++s) {
             mbar_init(&bar.kv_full[s], 1);
@@ -215,10 +490,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 mbar_init(&bar.p_full[h][i], 4);
             }
         }
+        for (int i = 0; i < kOwnWarps; ++i) {
+            mbar_init(&bar.own[i][0], 1);
+            mbar_init(&bar.own[i][1], 1);
+        }
         bar.err = 0;
         fence_barrier_init();
-        prefetch_tensormap(&P.tmK);
-        prefetch_tensormap(&P.tmV);
     }
     if (warp == 1) {
         tmem_alloc(&bar.tmem, 512);
@@ -230,17 +507,19 @@ __global__ void __launch_bounds__(kPThreads, 1)
     tc_fence_after();
     const uint32_t tmem = bar.tmem;
     const int n = P.prefix.n, total = pl.step0[n];
-    const int shares = min(kPrefixShares, total);  // none of them empty
-    const int b = blockIdx.x;
-    const int x0 = b < shares ? (int)((long long)b * total / shares) : 0;
-    const int x1 = b < shares ? (int)((long long)(b + 1) * total / shares) : 0;
+    const int shares = min(kPrefixCtas - pl.n_own, total);  // none of them empty
+    const int b = (int)blockIdx.x - pl.n_own;               // this CTA's share
+    const int x0 = b >= 0 && b < shares ? (int)((long long)b * total / shares) : 0;
+    const int x1 = b >= 0 && b < shares ? (int)((long long)(b + 1) * total / shares) : 0;
     volatile int* err = &bar.err;
     auto gave_up = [&](uint32_t where) {
         report(ctx, ST_TIMEOUT, where);
         *err = 1;
     };
 
-    if (warp == 0) {
+    if (b < 0) {
+        own_part<NT>(P, pl, qs, &bar.own[0][0], ctx);
+    } else if (warp == 0) {
         if (elect_one()) {
             const uint64_t pol = policy_evict_last();  // the other row tiles read it too
             uint32_t it = 0;
@@ -254,8 +533,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 const int row = (s.g * P.nkv + s.kvh) * P.prefix.cap + (pl.first[s.g] + s.k) * kPrefixKeys;
                 uint8_t* dst = ring + st * 2 * kPHalf;
                 mbar_arrive_expect_tx(&bar.kv_full[st], 2 * kPHalf);
-                tma_load_2d(dst, &P.tmK, &bar.kv_full[st], 0, row, pol);
-                tma_load_2d(dst + kPHalf, &P.tmV, &bar.kv_full[st], 0, row, pol);
+                tma_load_2d(dst, &P.tmPK, &bar.kv_full[st], 0, row, pol);
+                tma_load_2d(dst + kPHalf, &P.tmPV, &bar.kv_full[st], 0, row, pol);
             }
             if (*err)  // loads in flight into this CTA's shared memory (bounded)
                 for (uint32_t i = it > kPStages ? it - kPStages : 0; i < it; ++i)
@@ -380,8 +659,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             }
             int low = 0;
             if (P.window > 0 && r < rows) {
-                const int own = P.kv_len[pl.mem[seq0 + (r * row_of >> 16)]];
-                low = max(0, len + (own >= 0 && own <= P.kv_cap ? own : 0) - P.window);
+                low = max(0, len + pl.own_len[pl.mem[seq0 + (r * row_of >> 16)]] - P.window);
             }
             const bool live = h * 128 + quad * 32 < rows;  // some row of this warp counts
             float m = 0.f;  // what the weights are taken against (scaled scores, base 2)
@@ -481,118 +759,81 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 float o[64];
                 tmem_ld_wait_x64(to, o);
                 if (r < rows) {
-                    float4* dst = reinterpret_cast<float4*>(P.part_acc + at * 64);
+                    float4* dst = reinterpret_cast<float4*>(P.pre_acc + at * 64);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-                    *reinterpret_cast<float2*>(P.part_ml + at * 2) = make_float2(m, l2.x + l2.y);
+                    *reinterpret_cast<float2*>(P.pre_ml + at * 2) = make_float2(m, l2.x + l2.y);
                 }
             }
             tc_fence_before();
         }
     }
-    // the merge waits for this kernel: the own caches' kernel before it must be complete too
-    griddep_wait();
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, 512);
     task_end(ctx);
 }
 
-// One warp per (sequence, KV head): lane l holds dims 2l, 2l + 1 of every query head.  The
-// partials join in a fixed order: the prefix's shares, then the own chunks.
-template <int GP>
-__global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixMergeProblem P, const KCtx ctx) {
+// The merge: one warp per (sequence, query head), lane l holds dims 2l and 2l + 1.  The parts join
+// in a fixed order: the prefix's shares, then the own chunks.
+__global__ void __launch_bounds__(512) prefix_merge_kernel(const __grid_constant__ PrefixProblem P, const KCtx ctx) {
     griddep_wait();
     task_begin(ctx);
-    const int lane = threadIdx.x & 31;
-    const int pair = blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (pair < P.T * P.nkv) {
-        const int t = pair / P.nkv, kvh = pair % P.nkv;
-        // the prefix's shares [s0, s1] and this sequence's rows in their slots
-        int s0 = 0, s1 = -1;
-        size_t row0 = 0;
-        if (P.seq != nullptr) {
-            const PrefixSeq q = P.seq[t];
-            if (q.tiles > 0) {
-                const int tile = kvh * q.tiles + q.i / P.tile_seqs;
-                const int x = q.step + tile * q.steps;
-                // share s holds the steps [s total / shares, (s + 1) total / shares)
-                const long long shares = min(kPrefixShares, q.total);
-                s0 = (int)(((x + 1) * shares - 1) / q.total);
-                s1 = (int)(((x + q.steps) * shares - 1) / q.total);
-                row0 = (size_t)(q.tile + tile) * kPrefixRows + (size_t)(q.i % P.tile_seqs) * P.G;
-            }
-        }
-        int L = P.kv_len[t];
-        if (L < 0 || L > P.kv_cap) L = 0;
-        const int first = P.window > 0 ? max(0, L - P.window) : 0;
-        const int S = (L - first + P.chunk - 1) / P.chunk;
-        const float* oml = P.own_ml + (size_t)pair * P.S_max * 32;
-        const float* oacc = P.own_acc + (size_t)pair * P.S_max * 64 * 16;
-        // lane h: head h's maximum over all parts
-        const bool has = lane < P.G;
-        float M = -INFINITY;
-        for (int s = s0; s <= s1; ++s)
-            if (has) M = fmaxf(M, __ldcg(P.pre_ml + ((size_t)s * kPrefixRows + row0 + lane) * 2));
-        for (int c = 0; c < S; ++c)
-            if (has) M = fmaxf(M, __ldcg(oml + c * 32 + 2 * lane));
-        const float sub = M == -INFINITY ? 0.f : M;
-        float a[GP][2], Ls = 0.f;
-#pragma unroll
-        for (int h = 0; h < GP; ++h) a[h][0] = a[h][1] = 0.f;
-        for (int s = s0; s <= s1; ++s) {
-            const size_t r = (size_t)s * kPrefixRows + row0;
-            float w = 0.f;
-            if (has) {
-                const float2 ml = __ldcg(reinterpret_cast<const float2*>(P.pre_ml + (r + lane) * 2));
-                w = exp2f(ml.x - sub);
-                Ls = fmaf(w, ml.y, Ls);
-            }
-#pragma unroll
-            for (int h = 0; h < GP; ++h) {
-                const float wh = __shfl_sync(0xffffffffu, w, h);
-                if (h < P.G) {
-                    const float2 v = __ldcg(reinterpret_cast<const float2*>(P.pre_acc + (r + h) * 64 + 2 * lane));
-                    a[h][0] = fmaf(wh, v.x, a[h][0]);
-                    a[h][1] = fmaf(wh, v.y, a[h][1]);
-                }
-            }
-        }
-        for (int c = 0; c < S; ++c) {
-            float w = 0.f;
-            if (has) {
-                const float2 ml = __ldcg(reinterpret_cast<const float2*>(oml + c * 32 + 2 * lane));
-                w = exp2f(ml.x - sub);
-                Ls = fmaf(w, ml.y, Ls);
-            }
-#pragma unroll
-            for (int h4 = 0; h4 < GP; h4 += 4) {
-                const float4 v0 = __ldcg(reinterpret_cast<const float4*>(oacc + ((size_t)c * 64 + 2 * lane) * 16 + h4));
-                const float4 v1 = __ldcg(reinterpret_cast<const float4*>(oacc + ((size_t)c * 64 + 2 * lane + 1) * 16 + h4));
-                const float e0[4] = {v0.x, v0.y, v0.z, v0.w}, e1[4] = {v1.x, v1.y, v1.z, v1.w};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float wh = __shfl_sync(0xffffffffu, w, h4 + q);
-                    if (h4 + q < P.G) {
-                        a[h4 + q][0] = fmaf(wh, e0[q], a[h4 + q][0]);
-                        a[h4 + q][1] = fmaf(wh, e1[q], a[h4 + q][1]);
-                    }
-                }
-            }
-        }
-        // a row that sees nothing: o = 0, lse = -inf
-        const float inv = Ls == 0.f ? 0.f : 1.f / Ls;
-        bf16* o = P.o + (size_t)t * P.nq * 64 + (size_t)kvh * P.G * 64;
-#pragma unroll
-        for (int h = 0; h < GP; ++h) {
-            const float ih = __shfl_sync(0xffffffffu, inv, h);
-            if (h < P.G)
-                *reinterpret_cast<uint32_t*>(o + h * 64 + 2 * lane) = pack_bf16x2(a[h][0] * ih, a[h][1] * ih);
-        }
-        if (P.lse != nullptr && has)
-            P.lse[(size_t)t * P.nq + kvh * P.G + lane] =
-                Ls == 0.f ? -INFINITY : (M + log2f(Ls)) * 0.6931471805599453f;
+    const int lane = threadIdx.x & 31, h = threadIdx.x >> 5;
+    const int pair = blockIdx.x, t = pair / P.nkv, kvh = pair % P.nkv;
+    // the prefix's shares [s0, s0 + np) and this row in their slots
+    int s0 = 0, np = 0;
+    size_t row = 0;
+    const PrefixSeq q = P.seq[t];
+    if (q.tiles > 0) {
+        const int seq = q.i / P.tile_seqs, tile = kvh * q.tiles + seq;
+        const long long x = q.step + tile * q.steps;
+        // share s holds the steps [s total / shares, (s + 1) total / shares)
+        s0 = (int)(((x + 1) * q.shares - 1) / q.total);
+        np = (int)(((x + q.steps) * q.shares - 1) / q.total) - s0 + 1;
+        row = (size_t)(s0 + q.tile + tile) * kPrefixRows + (size_t)(q.i - seq * P.tile_seqs) * P.G + h;
     }
+    int own = P.kv_len[t];
+    if (own < 0 || own > P.kv_cap) own = 0;
+    const int seen = own - (P.window > 0 ? max(0, own - P.window) : 0);
+    const int parts = np + (seen + P.chunk - 1) / P.chunk;
+    const size_t own0 = (size_t)pair * P.S_max * 16 + h;
+    auto part_ml = [&](int k) {
+        const float* p = k < np ? P.pre_ml + (row + (size_t)k * kPrefixRows) * 2
+                                : P.own_ml + (own0 + (size_t)(k - np) * 16) * 2;
+        return __ldcg(reinterpret_cast<const float2*>(p));
+    };
+    float M = -INFINITY;
+    for (int k = lane; k < parts; k += 32) M = fmaxf(M, part_ml(k).x);
+    M = warp_max(M);
+    const float sub = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+    float2 a = make_float2(0.f, 0.f);
+    for (int k0 = 0; k0 < parts; k0 += 32) {
+        float w = 0.f;
+        if (k0 + lane < parts) {
+            const float2 ml = part_ml(k0 + lane);
+            w = ex2(ml.x - sub);
+            L = fmaf(w, ml.y, L);
+        }
+        const int nk = min(32, parts - k0);
+#pragma unroll 8
+        for (int k = 0; k < nk; ++k) {
+            const float wk = __shfl_sync(0xffffffffu, w, k);
+            const float* p = k0 + k < np ? P.pre_acc + (row + (size_t)(k0 + k) * kPrefixRows) * 64
+                                         : P.own_acc + (own0 + (size_t)(k0 + k - np) * 16) * 64;
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(p + 2 * lane));
+            a.x = fmaf(wk, v.x, a.x);
+            a.y = fmaf(wk, v.y, a.y);
+        }
+    }
+    L = warp_sum(L);
+    // a row that sees nothing: o = 0, lse = -inf
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const size_t at = (size_t)t * P.nq + kvh * P.G + h;
+    *reinterpret_cast<uint32_t*>(P.o + at * 64 + 2 * lane) = pack_bf16x2(a.x * inv, a.y * inv);
+    if (P.lse != nullptr && lane == 0)
+        P.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
     task_end(ctx);
 }
 
@@ -601,14 +842,10 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const PrefixMergeProb
 int enqueue_prefix(Launcher& L, const PrefixProblem& p, const KCtx& c) {
     const size_t smem = 1024 + 2 * 128 * 128 + kPStages * 2 * kPHalf + sizeof(PrefixBars) + sizeof(Plan);
     void* args[] = {(void*)&p, (void*)&c};
-    return L.launch((const void*)prefix_attn_kernel, dim3(kPrefixShares), dim3(kPThreads), smem, args,
-                    true);
-}
-
-int enqueue_prefix_merge(Launcher& L, const PrefixMergeProblem& p, const KCtx& c) {
-    void* args[] = {(void*)&p, (void*)&c};
-    const void* f = p.G <= 8 ? (const void*)prefix_merge_kernel<8> : (const void*)prefix_merge_kernel<16>;
-    return L.launch(f, dim3((p.T * p.nkv + 3) / 4), dim3(128), 0, args, true);
+    const void* f = p.G <= 8 ? (const void*)prefix_attn_kernel<1> : (const void*)prefix_attn_kernel<2>;
+    const int e = L.launch(f, dim3(kPrefixCtas), dim3(kPThreads), smem, args);
+    if (e) return e;
+    return L.launch((const void*)prefix_merge_kernel, dim3(p.T * p.nkv), dim3(32 * p.G), 0, args, true);
 }
 
 }  // namespace sgp

@@ -148,8 +148,6 @@ struct AttnProblem {
     // scores, V after the V product); 0: together, after the V product.  Load schedule only:
     // the results are identical either way.
     int kv_split;
-    // 1: every chunk leaves its partial and nothing is merged (o and cnt unused)
-    int part;
 };
 
 // Prefixes that sequences of a batch share (lengths and membership as device arrays).
@@ -159,18 +157,22 @@ struct PrefixRef {
     int n, cap;
 };
 
-// Attention of the batch's query heads over the prefixes they share.  Sequences with the same
-// prefix form a group; a row is one (sequence, query head) of the group and KV head.  A tile is
-// `tile_seqs` sequences' rows (at most kPrefixRows), a step is one tile against kPrefixKeys
-// positions.  The steps of all (group, KV head, tile) in order are cut into kPrefixShares equal
-// shares, one per CTA; share s's part of tile i leaves its partial in slot s + i.
+// Attention of the batch's query heads over the prefixes they share and over the sequences' own
+// caches, in one launch of kPrefixCtas CTAs of which some take the prefixes and the others the own
+// caches (split by the two parts' work, see k_prefix.cu); every part leaves partials.
+//
+// Prefixes: sequences with the same prefix form a group; a row is one (sequence, query head) of
+// the group and KV head.  A tile is `tile_seqs` sequences' rows (at most kPrefixRows), a step is
+// one tile against kPrefixKeys positions.  The steps of all (group, KV head, tile) in order are
+// cut into equal shares, one per CTA; share s's part of tile i leaves its partial in slot s + i.
+// Own caches: chunks of `chunk` positions of a (sequence, KV head), equal runs of them to a warp.
 constexpr int kPrefixRows = 256;
 constexpr int kPrefixKeys = 128;
-// Fixed, so that results never depend on the SM count: one share per SM of a 152-SM part.
-constexpr int kPrefixShares = 152;
+// Fixed, so that results never depend on the SM count: one per SM of a 152-SM part.
+constexpr int kPrefixCtas = 152;
 constexpr int kPrefixMax = 512;     // sequences, and prefixes, per call
 
-// What the merge needs of a sequence's group (written by the prefix kernel's first CTA).
+// What the merge needs of a sequence's group (written by the first CTA).
 struct PrefixSeq {
     int tile;               // first tile of the group
     int tiles;              // tiles per KV head (0: nothing visible)
@@ -178,32 +180,25 @@ struct PrefixSeq {
     int steps;              // steps per tile
     int i;                  // the sequence's place in the group
     int total;              // steps of the whole call
-    int pad[2];
+    int shares;             // shares they are cut into
+    int pad;
 };
 
 struct PrefixProblem {
-    CUtensorMap tmK, tmV;   // prefixes as 2-D [n * nkv * cap][64], box {64, kPrefixKeys}, SW128
+    CUtensorMap tmPK, tmPV; // prefixes as 2-D [n * nkv * cap][64], box {64, kPrefixKeys}, SW128
+    CUtensorMap tmK, tmV;   // own caches as 2-D [T * nkv * kv_cap][64], box {64, 64}, SW128
     const bf16* q;          // [T][nq * 64]
-    const int* kv_len;      // [T] own lengths (window)
-    PrefixRef prefix;
-    float* part_ml;         // [slot][kPrefixRows][2]  (max, sum)
-    float* part_acc;        // [slot][kPrefixRows][64]
+    const int* kv_len;      // [T]
+    PrefixRef prefix;       // n = 0: none
+    float* pre_ml;          // [slot][kPrefixRows][2]  (max, sum)
+    float* pre_acc;         // [slot][kPrefixRows][64]
+    float* own_ml;          // [T * nkv][S_max][16][2]
+    float* own_acc;         // [T * nkv][S_max][16][64]
     PrefixSeq* seq;         // [T]
-    int T, nq, nkv, G, kv_cap, window, tile_seqs;
-    float scale_log2;
-};
-
-// Joins a sequence's prefix partials and own-cache chunks.
-struct PrefixMergeProblem {
-    const float* pre_ml;
-    const float* pre_acc;
-    const PrefixSeq* seq;   // NULL: no prefixes
-    const float* own_ml;    // as AttnProblem::part_ml / part_acc
-    const float* own_acc;
-    const int* kv_len;
     bf16* o;                // [T][nq * 64]
     float* lse;             // [T][nq] or NULL
-    int T, nq, nkv, G, kv_cap, window, chunk, S_max, tile_seqs;
+    int T, nq, nkv, G, kv_cap, window, tile_seqs, chunk, S_max;
+    float scale_log2;
 };
 
 // acc[t][j][p] += sum over the group's heads of exp(scale q.k_p - lse)
@@ -325,7 +320,6 @@ int enqueue_dispatch(Launcher& L, const DispatchProblem& p, const KCtx& c);
 int enqueue_combine(Launcher& L, const CombineProblem& p, const KCtx& c);
 int enqueue_attention(Launcher& L, const AttnProblem& p, const KCtx& c);
 int enqueue_prefix(Launcher& L, const PrefixProblem& p, const KCtx& c);
-int enqueue_prefix_merge(Launcher& L, const PrefixMergeProblem& p, const KCtx& c);
 int enqueue_weights(Launcher& L, const WeightsProblem& p, const KCtx& c, int sms);
 int enqueue_evict(Launcher& L, const EvictProblem& p, const KCtx& c);
 int enqueue_lora(Launcher& L, const LoraProblem& p, const KCtx& c);

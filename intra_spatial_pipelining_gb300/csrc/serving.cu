@@ -78,14 +78,25 @@ int launched(int e, const char* what) {
 // ---- attention over shared prefixes ----------------------------------------------------
 struct PrefixLayout {
     size_t own_ml, own_acc, seq, pre_ml, pre_acc, total;
-    int S_max, tile_seqs;
+    int chunk, S_max, tile_seqs;
 };
+
+// Own positions of a work item: the longest that still gives the 64 or so streaming CTAs' 768 warps
+// about four items each (a shorter one costs its partial, 2 KB written and read for 32 KB streamed
+// at 128 positions).  64 sequences x 8 KV heads of up to 1024 positions beside a prefix of 8192:
+// chunks of 1024 left the stream at half its rate.
+int own_chunk(size_t pairs, int kv_cap) {
+    int chunk = 1024;
+    while (chunk > 128 && pairs * (size_t)((kv_cap - 1) / chunk + 1) < 3072) chunk /= 2;
+    return chunk;
+}
 
 PrefixLayout prefix_layout(const sgp_dims& d, int T, int kv_cap, int n_prefixes) {
     PrefixLayout y;
     const int G = d.n_q_heads / d.n_kv_heads;
     const size_t pairs = (size_t)T * d.n_kv_heads;
-    y.S_max = (kv_cap + kAttnChunk - 1) / kAttnChunk;
+    y.chunk = own_chunk(pairs, kv_cap);
+    y.S_max = (kv_cap - 1) / y.chunk + 1;
     y.tile_seqs = kPrefixRows / G;
     size_t off = kStatusBytes;
     auto take = [&](size_t bytes) {
@@ -93,12 +104,12 @@ PrefixLayout prefix_layout(const sgp_dims& d, int T, int kv_cap, int n_prefixes)
         off = al256(off + bytes);
         return o;
     };
-    y.own_ml = take(pairs * y.S_max * 32 * 4);
-    y.own_acc = take(pairs * y.S_max * 64 * 16 * 4);
+    y.own_ml = take(pairs * y.S_max * 16 * 2 * 4);
+    y.own_acc = take(pairs * y.S_max * 16 * 64 * 4);
     // slots: one per share and tile; a group has a started tile at most beside its full ones
     const size_t groups = n_prefixes < T ? n_prefixes : T;
     const size_t tiles = d.n_kv_heads * (groups + T / y.tile_seqs);
-    const size_t slots = n_prefixes > 0 ? kPrefixShares + tiles : 0;
+    const size_t slots = n_prefixes > 0 ? kPrefixCtas + tiles : 0;
     y.seq = take((size_t)T * sizeof(PrefixSeq));
     y.pre_ml = take(slots * kPrefixRows * 2 * 4);
     y.pre_acc = take(slots * kPrefixRows * 64 * 4);
@@ -134,78 +145,37 @@ int prefix_attention(const sgp_dims* d, const sgp_layer* cache, const sgp_prefix
     uint8_t* w = static_cast<uint8_t*>(ws);
     HostLauncher L(stream);
     const KCtx c = host_ctx(ws, OP_PREFIX);
-    const float scale_log2 = 1.4426950408889634f / sqrtf((float)d->head_dim);
-    const int G = d->n_q_heads / d->n_kv_heads;
-
-    AttnProblem a;
-    memset(&a, 0, sizeof(a));
+    PrefixProblem p;
+    memset(&p, 0, sizeof(p));
     const uint64_t own_rows = (uint64_t)T * d->n_kv_heads * cache->kv_cap;
-    const int span = cache->window > 0 && cache->window < cache->kv_cap ? cache->window : cache->kv_cap;
-    const int chunks = (span + kAttnChunk - 1) / kAttnChunk;
-    a.pos = attn_stage_pos((long long)T * d->n_kv_heads * chunks);
-    if ((r = host_tmap(&a.tmK, cache->k_cache, 64, own_rows, 64, a.pos))) return r;
-    if ((r = host_tmap(&a.tmV, cache->v_cache, 64, own_rows, 64, a.pos))) return r;
-    a.q = static_cast<const bf16*>(q);
-    a.kv_len = kv_len;
-    a.part_ml = reinterpret_cast<float*>(w + y.own_ml);
-    a.part_acc = reinterpret_cast<float*>(w + y.own_acc);
-    a.nrows = T;
-    a.nq = d->n_q_heads;
-    a.nkv = d->n_kv_heads;
-    a.G = G;
-    a.cap = cache->kv_cap;
-    a.window = cache->window;
-    a.chunk = kAttnChunk;
-    a.S_max = y.S_max;
-    a.scale_log2 = scale_log2;
-    a.n_cta = host_sms();
-    a.kv_split = 1;
-    a.part = 1;
-    if ((r = launched(enqueue_attention(L, a, c), "own-cache attention"))) return r;
-
+    if ((r = host_tmap(&p.tmK, cache->k_cache, 64, own_rows, 64, 64))) return r;
+    if ((r = host_tmap(&p.tmV, cache->v_cache, 64, own_rows, 64, 64))) return r;
     if (n > 0) {
-        PrefixProblem p;
-        memset(&p, 0, sizeof(p));
         const uint64_t pre_rows = (uint64_t)n * d->n_kv_heads * pre->cap;
-        if ((r = host_tmap(&p.tmK, pre->k, 64, pre_rows, 64, kPrefixKeys))) return r;
-        if ((r = host_tmap(&p.tmV, pre->v, 64, pre_rows, 64, kPrefixKeys))) return r;
-        p.q = a.q;
-        p.kv_len = kv_len;
+        if ((r = host_tmap(&p.tmPK, pre->k, 64, pre_rows, 64, kPrefixKeys))) return r;
+        if ((r = host_tmap(&p.tmPV, pre->v, 64, pre_rows, 64, kPrefixKeys))) return r;
         p.prefix = {pre->prefix_of, pre->len, n, pre->cap};
-        p.part_ml = reinterpret_cast<float*>(w + y.pre_ml);
-        p.part_acc = reinterpret_cast<float*>(w + y.pre_acc);
-        p.seq = reinterpret_cast<PrefixSeq*>(w + y.seq);
-        p.T = T;
-        p.nq = d->n_q_heads;
-        p.nkv = d->n_kv_heads;
-        p.G = G;
-        p.kv_cap = cache->kv_cap;
-        p.window = cache->window;
-        p.tile_seqs = y.tile_seqs;
-        p.scale_log2 = scale_log2;
-        if ((r = launched(enqueue_prefix(L, p, c), "prefix attention"))) return r;
     }
-
-    PrefixMergeProblem m;
-    memset(&m, 0, sizeof(m));
-    m.pre_ml = reinterpret_cast<const float*>(w + y.pre_ml);
-    m.pre_acc = reinterpret_cast<const float*>(w + y.pre_acc);
-    m.seq = n > 0 ? reinterpret_cast<const PrefixSeq*>(w + y.seq) : nullptr;
-    m.own_ml = a.part_ml;
-    m.own_acc = a.part_acc;
-    m.kv_len = kv_len;
-    m.o = static_cast<bf16*>(o);
-    m.lse = lse;
-    m.T = T;
-    m.nq = d->n_q_heads;
-    m.nkv = d->n_kv_heads;
-    m.G = G;
-    m.kv_cap = cache->kv_cap;
-    m.window = cache->window;
-    m.chunk = kAttnChunk;
-    m.S_max = y.S_max;
-    m.tile_seqs = y.tile_seqs;
-    return launched(enqueue_prefix_merge(L, m, c), "prefix merge");
+    p.q = static_cast<const bf16*>(q);
+    p.kv_len = kv_len;
+    p.pre_ml = reinterpret_cast<float*>(w + y.pre_ml);
+    p.pre_acc = reinterpret_cast<float*>(w + y.pre_acc);
+    p.own_ml = reinterpret_cast<float*>(w + y.own_ml);
+    p.own_acc = reinterpret_cast<float*>(w + y.own_acc);
+    p.seq = reinterpret_cast<PrefixSeq*>(w + y.seq);
+    p.o = static_cast<bf16*>(o);
+    p.lse = lse;
+    p.T = T;
+    p.nq = d->n_q_heads;
+    p.nkv = d->n_kv_heads;
+    p.G = d->n_q_heads / d->n_kv_heads;
+    p.kv_cap = cache->kv_cap;
+    p.window = cache->window;
+    p.tile_seqs = y.tile_seqs;
+    p.chunk = y.chunk;
+    p.S_max = y.S_max;
+    p.scale_log2 = 1.4426950408889634f / sqrtf((float)d->head_dim);
+    return launched(enqueue_prefix(L, p, c), "prefix attention");
 }
 
 int attention_weights(const sgp_dims* d, const sgp_layer* cache, const int32_t* kv_len,
