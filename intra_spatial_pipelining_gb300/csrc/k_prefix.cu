@@ -13,6 +13,9 @@
 // 4 d flops for every (row, position) against 256 bytes for every position; the own part is a
 // stream of the caches through warp-level products, bound by HBM.  Side by side, each has what
 // the other leaves idle.
+//
+// Instructions that run once are met cold, about 300 cycles for eight of them, so what surrounds the
+// loops is kept short: no unrolling, few divisions, one copy of what several warps need.
 #include <climits>
 
 #include "kernels.h"
@@ -44,8 +47,9 @@ struct Plan {
     int chunk0[kPrefixMax + 1];  // own chunks (all KV heads) before a sequence
     int own_first[kPrefixMax];   // first own position seen
     int own_len[kPrefixMax];
-    long long own_pos;           // own positions seen, of all sequences
-    int n_own;                   // CTAs that take the own caches; the others take the prefixes
+    int block_chunks[kPrefixMax / 32], block_pos[kPrefixMax / 32];  // of 32 sequences: own chunks, positions
+    int n_own;                   // CTAs that take the own caches; the others take the prefixes:
+    int shares, q, n_long;       // shares of q steps, the first n_long of one more
 };
 
 // exclusive prefix sums over n <= kPrefixMax values of three arrays by one warp; x[n] = total
@@ -81,15 +85,20 @@ __device__ __forceinline__ void scan3(int* a, int* b, int* c, int n, int lane) {
     }
 }
 
-// CTAs that take the own caches: what makes the slower part fastest, of the multiples of 8.  An own
-// CTA streams 100 GB/s (measured on partial pools) up to 6.6 TB/s together, a prefix CTA takes
-// 1.5 us for a step; beginning and end cost 4 and 6 us.
+// Chunks of n own positions.
+__device__ __forceinline__ int chunks_of(int n, const PrefixProblem& P) {
+    return (n + (1 << P.chunk_log2) - 1) >> P.chunk_log2;
+}
+
+// CTAs that take the own caches: what makes the slower part fastest, of the multiples of 5.  An own
+// CTA streams 85 GB/s, up to 6.6 TB/s together (measured: 77 on 8 CTAs with short chunks, 100 on
+// 40), a prefix CTA takes 1.3 us for a step; beginning and end cost 3 and 6 us.
 __device__ __forceinline__ int own_ctas(long long own_pos, int nkv, int steps, int lane) {
-    const int x = lane < 19 ? 8 * lane : kPrefixCtas, y = kPrefixCtas - x;
-    const float own = x > 0 ? 4000.f + (float)own_pos * (float)(nkv * 256) / fminf(100.f * x, 6600.f) : 0.f;
-    const float pre = y > 0 ? 6000.f + 1500.f * (float)((steps + y - 1) / y) : 0.f;
+    const int x = lane < 31 ? 5 * lane : kPrefixCtas, y = kPrefixCtas - x;
+    const float own = x > 0 ? 3000.f + __fdividef((float)own_pos * (float)(nkv * 256), fminf(85.f * x, 6600.f)) : 0.f;
+    const float pre = y > 0 ? 6000.f + 1300.f * (__fdividef((float)steps, (float)y) + 0.5f) : 0.f;
     float cost = fmaxf(own, pre);
-    if (lane > 19 || (x == 0 && own_pos > 0) || (y == 0 && steps > 0)) cost = INFINITY;
+    if ((x == 0 && own_pos > 0) || (y == 0 && steps > 0)) cost = INFINITY;
     int best = x;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -103,8 +112,14 @@ __device__ __forceinline__ int own_ctas(long long own_pos, int nkv, int steps, i
     return best;
 }
 
-__device__ void build_plan(Plan& pl, const PrefixProblem& P, const KCtx& ctx) {
-    const int tid = threadIdx.x, lane = tid & 31, n = P.prefix.n;
+// `scratch`: kPrefixMax / 32 * kPrefixMax ints (the stages, not in use yet).  Sequences are taken in
+// blocks of 32, a warp to a block, and the blocks' counts added up by whoever needs them: a warp
+// that went through 16 blocks alone took 5 us.
+__device__ void build_plan(Plan& pl, int* scratch, const PrefixProblem& P, const KCtx& ctx) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = P.prefix.n;
+    const int blocks = (P.T + 31) / 32;
+    int* count = scratch;  // [block][group]: sequences of the group in the block
+    for (int i = tid; i < blocks * n; i += kPThreads) count[i] = 0;
     for (int g = tid; g < n; g += kPThreads) {
         int len = P.prefix.len[g];
         if (len < 0 || len > P.prefix.cap) {
@@ -113,71 +128,64 @@ __device__ void build_plan(Plan& pl, const PrefixProblem& P, const KCtx& ctx) {
         }
         pl.len[g] = len;
         pl.low[g] = INT_MAX;
-        pl.base[g] = 0;  // members, until the scan
     }
-    for (int t = tid; t < P.T; t += kPThreads) {
-        int g = -1;
-        if (n > 0) {
-            g = P.prefix.of[t];
-            if (g >= n && blockIdx.x == 0) report(ctx, ST_BOUNDS, (uint32_t)g);
-            if (g >= n || g < 0) g = -1;
+    __syncthreads();
+#pragma unroll 1
+    for (int blk = warp; blk < blocks; blk += kOwnWarps) {
+        const int t = blk * 32 + lane;
+        int g = t < P.T && n > 0 ? P.prefix.of[t] : -1;
+        int own = t < P.T ? P.kv_len[t] : 0;
+        if (g >= n) {
+            if (n > 0 && blockIdx.x == 0) report(ctx, ST_BOUNDS, (uint32_t)g);
+            g = -1;
         }
-        int own = P.kv_len[t];
         if (own < 0 || own > P.kv_cap) {
             if (blockIdx.x == 0) report(ctx, ST_BOUNDS, (uint32_t)own);
             own = 0;
         }
-        pl.of[t] = g;
-        pl.own_len[t] = own;
+        g = max(g, -1);
         // a window reaches as far back in the own cache whatever lies before it
-        pl.own_first[t] = P.window > 0 ? max(0, own - P.window) : 0;
+        const int first = P.window > 0 ? max(0, own - P.window) : 0;
+        const unsigned same = __match_any_sync(0xffffffffu, g), before = same & ((1u << lane) - 1u);
+        if (g >= 0 && before == 0) count[blk * n + g] = __popc(same);
+        const int cnt = chunks_of(own - first, P) * P.nkv;
+        int incl = cnt;
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        const int pos = __reduce_add_sync(0xffffffffu, own - first);  // (a cache has < 2^31 rows)
+        if (lane == 31) {
+            pl.block_chunks[blk] = incl;
+            pl.block_pos[blk] = pos;
+        }
+        if (t < P.T) {
+            pl.of[t] = g;
+            pl.own_len[t] = own;
+            pl.own_first[t] = first;
+            pl.rank[t] = __popc(before);
+            pl.chunk0[t] = incl - cnt;
+        }
     }
     __syncthreads();
-    if (tid < 32) {
-        // place of every sequence in its group: 32 sequences a round, counts kept per group
-        if (n > 0)
-            for (int t0 = 0; t0 < P.T; t0 += 32) {
-                const int t = t0 + lane;
-                const int g = t < P.T ? pl.of[t] : -1;
-                const unsigned same = __match_any_sync(0xffffffffu, g);
-                const int before = __popc(same & ((1u << lane) - 1u));
-                const int had = g >= 0 ? pl.base[g] : 0;
-                __syncwarp();
-                if (g >= 0) {
-                    pl.rank[t] = had + before;
-                    if (before == 0) pl.base[g] = had + __popc(same);
-                }
-                __syncwarp();
-            }
-    } else if (tid < 64) {
-        int run = 0;
-        long long pos = 0;
-        for (int t0 = 0; t0 < P.T; t0 += 32) {
-            const int t = t0 + lane;
-            const int seen = t < P.T ? pl.own_len[t] - pl.own_first[t] : 0;
-            const int cnt = (seen + P.chunk - 1) / P.chunk * P.nkv;
-            int incl = cnt;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += v;
-            }
-            if (t < P.T) pl.chunk0[t] = run + incl - cnt;
-            run += __shfl_sync(0xffffffffu, incl, 31);
-            pos += seen;
+    for (int t = tid; t < P.T; t += kPThreads) {
+        const int g = pl.of[t], blk = t >> 5;
+        int chunks = 0, rank = 0;
+        for (int i = 0; i < blk; ++i) {
+            chunks += pl.block_chunks[i];
+            if (g >= 0) rank += count[i * n + g];
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) pos += __shfl_xor_sync(0xffffffffu, pos, o);
-        if (lane == 0) {
-            pl.chunk0[P.T] = run;
-            pl.own_pos = pos;
-        }
-    } else if (P.window > 0) {
-        for (int t = tid - 64; t < P.T; t += kPThreads - 64) {
-            const int g = pl.of[t];
-            if (g >= 0) atomicMin(&pl.low[g], max(0, pl.len[g] + pl.own_len[t] - P.window));
-        }
+        pl.chunk0[t] += chunks;
+        pl.rank[t] += rank;
+        if (P.window > 0 && g >= 0) atomicMin(&pl.low[g], max(0, pl.len[g] + pl.own_len[t] - P.window));
     }
+    for (int g = tid; g < n; g += kPThreads) {
+        int members = 0;
+        for (int i = 0; i < blocks; ++i) members += count[i * n + g];
+        pl.base[g] = members;
+    }
+    fence_proxy_async();  // the scratch becomes the target of TMA loads
     __syncthreads();
     for (int g = tid; g < n; g += kPThreads) {
         const int low = P.window > 0 ? pl.low[g] : 0;
@@ -186,25 +194,37 @@ __device__ void build_plan(Plan& pl, const PrefixProblem& P, const KCtx& ctx) {
         const bool some = members > 0 && low < len;
         pl.low[g] = low;
         pl.first[g] = first;
-        pl.tiles[g] = some ? (members + P.tile_seqs - 1) / P.tile_seqs : 0;
+        // members / tile_seqs rounded up, exact below 2^22 / tile_seqs
+        pl.tiles[g] = some ? (int)((unsigned)(members + P.tile_seqs - 1) * P.tile_inv >> 22) : 0;
         pl.steps[g] = some ? (len + kPrefixKeys - 1) / kPrefixKeys - first : 0;
         pl.tile0[g] = pl.tiles[g] * P.nkv;
         pl.step0[g] = pl.tile0[g] * pl.steps[g];
     }
     __syncthreads();
-    if (tid < 32) {
+    if (warp == 0) {
         scan3(pl.base, pl.tile0, pl.step0, n, lane);
+        const int chunks = __reduce_add_sync(0xffffffffu, lane < blocks ? pl.block_chunks[lane] : 0);
+        long long pos = lane < blocks ? pl.block_pos[lane] : 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) pos += __shfl_xor_sync(0xffffffffu, pos, o);
         __syncwarp();
-        const int x = own_ctas(pl.own_pos, P.nkv, pl.step0[n], lane);
-        if (lane == 0) pl.n_own = x;
+        const int x = own_ctas(pos, P.nkv, pl.step0[n], lane);
+        if (lane == 0) {
+            const int total = pl.step0[n], shares = min(kPrefixCtas - x, total);  // none empty
+            pl.chunk0[P.T] = chunks;
+            pl.n_own = x;
+            pl.q = shares > 0 ? total / shares : 1;
+            pl.n_long = total - pl.q * shares;
+            pl.shares = shares;
+        }
     }
     __syncthreads();
     for (int t = tid; t < P.T; t += kPThreads) {
-        const int g = pl.of[t], total = pl.step0[n], shares = min(kPrefixCtas - pl.n_own, total);
+        const int g = pl.of[t];
         if (g >= 0) pl.mem[pl.base[g] + pl.rank[t]] = t;
         if (blockIdx.x == 0)
-            P.seq[t] = g >= 0 ? PrefixSeq{pl.tile0[g], pl.tiles[g], pl.step0[g], pl.steps[g], pl.rank[t], total, shares, 0}
-                              : PrefixSeq{0, 0, 0, 0, 0, total, shares, 0};
+            P.seq[t] = g >= 0 ? PrefixSeq{pl.tile0[g], pl.tiles[g], pl.step0[g], pl.steps[g], pl.rank[t], pl.n_long, pl.q, 0}
+                              : PrefixSeq{0, 0, 0, 0, 0, 0, 1, 0};
     }
     __syncthreads();
 }
@@ -213,15 +233,15 @@ __device__ void build_plan(Plan& pl, const PrefixProblem& P, const KCtx& ctx) {
 struct Step {
     int g, kvh, tile, k;
 };
-__device__ __forceinline__ Step step_at(const Plan& pl, int n, int x) {
+__device__ __noinline__ Step step_at(const Plan& pl, int n, int x) {
     int lo = 0, hi = n;  // the last group that begins at or before x (empty ones begin with it)
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (pl.step0[mid] <= x) lo = mid;
         else hi = mid;
     }
-    const int r = x - pl.step0[lo], i = r / pl.steps[lo];
-    return {lo, i / pl.tiles[lo], i % pl.tiles[lo], r % pl.steps[lo]};
+    const int r = x - pl.step0[lo], i = r / pl.steps[lo], kvh = i / pl.tiles[lo];
+    return {lo, kvh, i - kvh * pl.tiles[lo], r - i * pl.steps[lo]};
 }
 
 // The own caches: independent warps, each with a private stage of 64 positions, K and V halves
@@ -239,8 +259,8 @@ __device__ __forceinline__ OwnChunk own_chunk(const Plan& pl, const PrefixProble
         else hi = mid;
     }
     const int per = (pl.chunk0[lo + 1] - pl.chunk0[lo]) / P.nkv, r = i - pl.chunk0[lo];
-    const int kvh = r / per, c = r - kvh * per, p0 = pl.own_first[lo] + c * P.chunk;
-    return {i, lo, kvh, c, p0, min(pl.own_len[lo], p0 + P.chunk)};
+    const int kvh = r / per, c = r - kvh * per, p0 = pl.own_first[lo] + (c << P.chunk_log2);
+    return {i, lo, kvh, c, p0, min(pl.own_len[lo], p0 + (1 << P.chunk_log2))};
 }
 
 template <int NT>
@@ -503,14 +523,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
     tc_fence_before();
     task_begin(ctx);
-    build_plan(pl, P, ctx);  // ends with a barrier
+    static_assert(kPrefixMax / 32 * kPrefixMax * 4 <= 2 * 128 * 128 + kPStages * 2 * kPHalf, "scratch fits");
+    build_plan(pl, reinterpret_cast<int*>(qs), P, ctx);  // ends with a barrier
     tc_fence_after();
     const uint32_t tmem = bar.tmem;
-    const int n = P.prefix.n, total = pl.step0[n];
-    const int shares = min(kPrefixCtas - pl.n_own, total);  // none of them empty
-    const int b = (int)blockIdx.x - pl.n_own;               // this CTA's share
-    const int x0 = b >= 0 && b < shares ? (int)((long long)b * total / shares) : 0;
-    const int x1 = b >= 0 && b < shares ? (int)((long long)(b + 1) * total / shares) : 0;
+    const int n = P.prefix.n;
+    const int b = (int)blockIdx.x - pl.n_own;  // this CTA's share
+    const int x0 = b * pl.q + min(b, pl.n_long);
+    const int x1 = b < pl.shares ? x0 + pl.q + (b < pl.n_long ? 1 : 0) : x0;
     volatile int* err = &bar.err;
     auto gave_up = [&](uint32_t where) {
         report(ctx, ST_TIMEOUT, where);
@@ -523,18 +543,23 @@ __global__ void __launch_bounds__(kPThreads, 1)
         if (elect_one()) {
             const uint64_t pol = policy_evict_last();  // the other row tiles read it too
             uint32_t it = 0;
-            for (int x = x0; x < x1 && !*err; ++it, ++x) {
-                const uint32_t st = it % kPStages, use = it / kPStages;
-                if (use > 0 && !mbar_wait_near(&bar.kv_empty[st], (use - 1) & 1u, ctx.timeout_ns)) {
-                    gave_up(20);
-                    break;
-                }
+            for (int x = x0; x < x1 && !*err;) {
                 const Step s = step_at(pl, n, x);
-                const int row = (s.g * P.nkv + s.kvh) * P.prefix.cap + (pl.first[s.g] + s.k) * kPrefixKeys;
-                uint8_t* dst = ring + st * 2 * kPHalf;
-                mbar_arrive_expect_tx(&bar.kv_full[st], 2 * kPHalf);
-                tma_load_2d(dst, &P.tmPK, &bar.kv_full[st], 0, row, pol);
-                tma_load_2d(dst + kPHalf, &P.tmPV, &bar.kv_full[st], 0, row, pol);
+                const int steps = min(x1 - x, pl.steps[s.g] - s.k);
+                int row = (s.g * P.nkv + s.kvh) * P.prefix.cap + (pl.first[s.g] + s.k) * kPrefixKeys;
+                x += steps;
+#pragma unroll 1
+                for (int i = 0; i < steps; ++i, ++it, row += kPrefixKeys) {
+                    const uint32_t st = it % kPStages, use = it / kPStages;
+                    if (use > 0 && !mbar_wait_near(&bar.kv_empty[st], (use - 1) & 1u, ctx.timeout_ns)) {
+                        gave_up(20);
+                        break;
+                    }
+                    uint8_t* dst = ring + st * 2 * kPHalf;
+                    mbar_arrive_expect_tx(&bar.kv_full[st], 2 * kPHalf);
+                    tma_load_2d(dst, &P.tmPK, &bar.kv_full[st], 0, row, pol);
+                    tma_load_2d(dst + kPHalf, &P.tmPV, &bar.kv_full[st], 0, row, pol);
+                }
             }
             if (*err)  // loads in flight into this CTA's shared memory (bounded)
                 for (uint32_t i = it > kPStages ? it - kPStages : 0; i < it; ++i)
@@ -638,21 +663,18 @@ __global__ void __launch_bounds__(kPThreads, 1)
             // this warp's 32 query rows, 8 lanes to a row, into the swizzled tile (zeros past the
             // tile's rows: rows do not mix, and theirs are not stored)
             {
-                uint8_t* dst = qs + h * 128 * 128;
+                const int q = r * row_of >> 16;
+                const int at = r < rows ? pl.mem[seq0 + q] * P.nq + s.kvh * P.G + r - q * P.G : -1;
+                uint8_t* dst = qs + (h * 128 + quad * 32) * 128;
                 uint4 v[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int row = h * 128 + quad * 32 + i * 4 + (lane >> 3), q = row * row_of >> 16;
+                    const int src = __shfl_sync(0xffffffffu, at, i * 4 + (lane >> 3));
                     v[i] = make_uint4(0, 0, 0, 0);
-                    if (row < rows) {
-                        const bf16* src = P.q + (size_t)pl.mem[seq0 + q] * P.nq * 64 +
-                                          (size_t)(s.kvh * P.G + row - q * P.G) * 64;
-                        v[i] = reinterpret_cast<const uint4*>(src)[lane & 7];
-                    }
+                    if (src >= 0) v[i] = reinterpret_cast<const uint4*>(P.q + (size_t)src * 64)[lane & 7];
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    *reinterpret_cast<uint4*>(dst + sw128(quad * 32 + i * 4 + (lane >> 3), lane & 7)) = v[i];
+                for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(dst + sw128(i * 4 + (lane >> 3), lane & 7)) = v[i];
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.q_full[h]);
@@ -756,13 +778,26 @@ __global__ void __launch_bounds__(kPThreads, 1)
             if (live) {
                 const size_t slot = b + (size_t)(pl.tile0[s.g] + s.kvh * pl.tiles[s.g] + s.tile);
                 const size_t at = slot * kPrefixRows + r;
-                float o[64];
-                tmem_ld_wait_x64(to, o);
-                if (r < rows) {
-                    float4* dst = reinterpret_cast<float4*>(P.pre_acc + at * 64);
+                if (r < rows) *reinterpret_cast<float2*>(P.pre_ml + at * 2) = make_float2(m, l2.x + l2.y);
+                // The rows leave through this warp's part of the query tile, 16 dims at a time: a
+                // thread's own row straight to memory is 32 lines to a store
+                float4* buf = reinterpret_cast<float4*>(qs + (h * 128 + quad * 32) * 128);  // [32][4]
+                const int row0 = h * 128 + quad * 32 + (lane >> 2);
+                float4* dst = reinterpret_cast<float4*>(P.pre_acc + (slot * kPrefixRows + row0) * 64) + (lane & 3);
+#pragma unroll 1
+                for (int c = 0; c < 64; c += 16, dst += 4) {
+                    float o[16];
+                    tmem_ld_wait_x16(to + c, o);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-                    *reinterpret_cast<float2*>(P.pre_ml + at * 2) = make_float2(m, l2.x + l2.y);
+                    for (int i = 0; i < 4; ++i)
+                        buf[lane * 4 + (i ^ (lane >> 1 & 3))] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int q = 8 * i + (lane >> 2);
+                        if (row0 + 8 * i < rows) dst[8 * i * 16] = buf[q * 4 + ((lane & 3) ^ (q >> 1 & 3))];
+                    }
+                    __syncwarp();
                 }
             }
             tc_fence_before();
@@ -772,6 +807,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, 512);
     task_end(ctx);
+}
+
+// The share that holds step x: the first n_long have q + 1 steps, the others q.
+__device__ __forceinline__ int share_of(int x, const PrefixSeq& p) {
+    const int r = x - p.n_long * (p.q + 1), less = r < 0;
+    return less ? x / (p.q + 1) : p.n_long + r / p.q;
 }
 
 // The merge: one warp per (sequence, query head), lane l holds dims 2l and 2l + 1.  The parts join
@@ -786,17 +827,16 @@ __global__ void __launch_bounds__(512) prefix_merge_kernel(const __grid_constant
     size_t row = 0;
     const PrefixSeq q = P.seq[t];
     if (q.tiles > 0) {
-        const int seq = q.i / P.tile_seqs, tile = kvh * q.tiles + seq;
-        const long long x = q.step + tile * q.steps;
-        // share s holds the steps [s total / shares, (s + 1) total / shares)
-        s0 = (int)(((x + 1) * q.shares - 1) / q.total);
-        np = (int)(((x + q.steps) * q.shares - 1) / q.total) - s0 + 1;
+        const int seq = (int)((unsigned)q.i * P.tile_inv >> 22), tile = kvh * q.tiles + seq;
+        const int x = q.step + tile * q.steps;
+        s0 = share_of(x, q);
+        np = share_of(x + q.steps - 1, q) - s0 + 1;
         row = (size_t)(s0 + q.tile + tile) * kPrefixRows + (size_t)(q.i - seq * P.tile_seqs) * P.G + h;
     }
     int own = P.kv_len[t];
     if (own < 0 || own > P.kv_cap) own = 0;
     const int seen = own - (P.window > 0 ? max(0, own - P.window) : 0);
-    const int parts = np + (seen + P.chunk - 1) / P.chunk;
+    const int parts = np + chunks_of(seen, P);
     const size_t own0 = (size_t)pair * P.S_max * 16 + h;
     auto part_ml = [&](int k) {
         const float* p = k < np ? P.pre_ml + (row + (size_t)k * kPrefixRows) * 2
@@ -817,7 +857,7 @@ __global__ void __launch_bounds__(512) prefix_merge_kernel(const __grid_constant
             L = fmaf(w, ml.y, L);
         }
         const int nk = min(32, parts - k0);
-#pragma unroll 8
+#pragma unroll 4
         for (int k = 0; k < nk; ++k) {
             const float wk = __shfl_sync(0xffffffffu, w, k);
             const float* p = k0 + k < np ? P.pre_acc + (row + (size_t)(k0 + k) * kPrefixRows) * 64

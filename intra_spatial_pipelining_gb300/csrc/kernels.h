@@ -165,7 +165,7 @@ struct PrefixRef {
 // the group and KV head.  A tile is `tile_seqs` sequences' rows (at most kPrefixRows), a step is
 // one tile against kPrefixKeys positions.  The steps of all (group, KV head, tile) in order are
 // cut into equal shares, one per CTA; share s's part of tile i leaves its partial in slot s + i.
-// Own caches: chunks of `chunk` positions of a (sequence, KV head), equal runs of them to a warp.
+// Own caches: chunks of 2^chunk_log2 positions of a (sequence, KV head), equal runs of them to a warp.
 constexpr int kPrefixRows = 256;
 constexpr int kPrefixKeys = 128;
 // Fixed, so that results never depend on the SM count: one per SM of a 152-SM part.
@@ -179,8 +179,7 @@ struct PrefixSeq {
     int step;               // first step of the group
     int steps;              // steps per tile
     int i;                  // the sequence's place in the group
-    int total;              // steps of the whole call
-    int shares;             // shares they are cut into
+    int n_long, q;          // the call's shares: the first n_long have q + 1 steps, the others q
     int pad;
 };
 
@@ -197,7 +196,8 @@ struct PrefixProblem {
     PrefixSeq* seq;         // [T]
     bf16* o;                // [T][nq * 64]
     float* lse;             // [T][nq] or NULL
-    int T, nq, nkv, G, kv_cap, window, tile_seqs, chunk, S_max;
+    int T, nq, nkv, G, kv_cap, window, tile_seqs, chunk_log2, S_max;
+    unsigned tile_inv;      // 2^22 / tile_seqs, rounded up
     float scale_log2;
 };
 

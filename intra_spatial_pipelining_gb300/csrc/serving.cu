@@ -78,25 +78,25 @@ int launched(int e, const char* what) {
 // ---- attention over shared prefixes ----------------------------------------------------
 struct PrefixLayout {
     size_t own_ml, own_acc, seq, pre_ml, pre_acc, total;
-    int chunk, S_max, tile_seqs;
+    int chunk_log2, S_max, tile_seqs;
 };
 
 // Own positions of a work item: the longest that still gives the 64 or so streaming CTAs' 768 warps
 // about four items each (a shorter one costs its partial, 2 KB written and read for 32 KB streamed
 // at 128 positions).  64 sequences x 8 KV heads of up to 1024 positions beside a prefix of 8192:
 // chunks of 1024 left the stream at half its rate.
-int own_chunk(size_t pairs, int kv_cap) {
-    int chunk = 1024;
-    while (chunk > 128 && pairs * (size_t)((kv_cap - 1) / chunk + 1) < 3072) chunk /= 2;
-    return chunk;
+int own_chunk_log2(size_t pairs, int kv_cap) {
+    int b = 10;
+    while (b > 7 && pairs * (size_t)(((kv_cap - 1) >> b) + 1) < 3072) --b;
+    return b;
 }
 
 PrefixLayout prefix_layout(const sgp_dims& d, int T, int kv_cap, int n_prefixes) {
     PrefixLayout y;
     const int G = d.n_q_heads / d.n_kv_heads;
     const size_t pairs = (size_t)T * d.n_kv_heads;
-    y.chunk = own_chunk(pairs, kv_cap);
-    y.S_max = (kv_cap - 1) / y.chunk + 1;
+    y.chunk_log2 = own_chunk_log2(pairs, kv_cap);
+    y.S_max = ((kv_cap - 1) >> y.chunk_log2) + 1;
     y.tile_seqs = kPrefixRows / G;
     size_t off = kStatusBytes;
     auto take = [&](size_t bytes) {
@@ -172,7 +172,8 @@ int prefix_attention(const sgp_dims* d, const sgp_layer* cache, const sgp_prefix
     p.kv_cap = cache->kv_cap;
     p.window = cache->window;
     p.tile_seqs = y.tile_seqs;
-    p.chunk = y.chunk;
+    p.chunk_log2 = y.chunk_log2;
+    p.tile_inv = ((1u << 22) + y.tile_seqs - 1) / y.tile_seqs;
     p.S_max = y.S_max;
     p.scale_log2 = 1.4426950408889634f / sqrtf((float)d->head_dim);
     return launched(enqueue_prefix(L, p, c), "prefix attention");
