@@ -222,9 +222,6 @@ __device__ void build_plan(Plan& pl, int* scratch, const PrefixProblem& P, const
     for (int t = tid; t < P.T; t += kPThreads) {
         const int g = pl.of[t];
         if (g >= 0) pl.mem[pl.base[g] + pl.rank[t]] = t;
-        if (blockIdx.x == 0)
-            P.seq[t] = g >= 0 ? PrefixSeq{pl.tile0[g], pl.tiles[g], pl.step0[g], pl.steps[g], pl.rank[t], pl.n_long, pl.q, 0}
-                              : PrefixSeq{0, 0, 0, 0, 0, 0, 1, 0};
     }
     __syncthreads();
 }
@@ -484,6 +481,29 @@ __device__ __forceinline__ int halves_of(const Plan& pl, const Step& s, int step
     return (min(pl.len[s.g] - p0, steps * kPrefixKeys) + kPSub - 1) / kPSub;
 }
 
+// The share that holds step x: the first n_long have q + 1 steps, the others q.
+__device__ __forceinline__ int share_of(const Plan& pl, int x) {
+    const int r = x - pl.n_long * (pl.q + 1);
+    return r < 0 ? x / (pl.q + 1) : pl.n_long + r / pl.q;
+}
+
+// The parts of every (sequence, KV head), for the merge: pairs i, i + stride, ...
+__device__ void list_parts(const Plan& pl, const PrefixProblem& P, int i, int stride) {
+    for (; i < P.T * P.nkv; i += stride) {
+        const int t = i / P.nkv, kvh = i - t * P.nkv, g = pl.of[t];
+        PrefixParts p = {0, 0, 0, chunks_of(pl.own_len[t] - pl.own_first[t], P)};
+        if (g >= 0 && pl.tiles[g] > 0) {
+            const int rank = pl.rank[t], seq = (int)((unsigned)rank * P.tile_inv >> 22);
+            const int tile = kvh * pl.tiles[g] + seq, x = pl.step0[g] + tile * pl.steps[g];
+            const int s0 = share_of(pl, x);
+            p.slot = s0 + pl.tile0[g] + tile;
+            p.row = (rank - seq * P.tile_seqs) * P.G;
+            p.n_pre = share_of(pl, x + pl.steps[g] - 1) - s0 + 1;
+        }
+        P.parts[i] = p;
+    }
+}
+
 template <int NT>
 __global__ void __launch_bounds__(kPThreads, 1)
     prefix_attn_kernel(const __grid_constant__ PrefixProblem P, const KCtx ctx) {
@@ -538,6 +558,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     };
 
     if (b < 0) {
+        if (pl.n_own == kPrefixCtas) list_parts(pl, P, blockIdx.x * kPThreads + tid, kPrefixCtas * kPThreads);
         own_part<NT>(P, pl, qs, &bar.own[0][0], ctx);
     } else if (warp == 0) {
         if (elect_one()) {
@@ -636,7 +657,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp >= 4) {
+    } else if (warp == 3) {
+        list_parts(pl, P, b * 32 + lane, (kPrefixCtas - pl.n_own) * 32);
+    } else {
         const int h = (warp - 4) >> 2, quad = warp & 3;  // a warp reads its quadrant's TMEM lanes
         const int r = h * 128 + quad * 32 + lane;        // this thread's row of the tile
         const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
@@ -809,65 +832,61 @@ __global__ void __launch_bounds__(kPThreads, 1)
     task_end(ctx);
 }
 
-// The share that holds step x: the first n_long have q + 1 steps, the others q.
-__device__ __forceinline__ int share_of(int x, const PrefixSeq& p) {
-    const int r = x - p.n_long * (p.q + 1), less = r < 0;
-    return less ? x / (p.q + 1) : p.n_long + r / p.q;
-}
-
 // The merge: one warp per (sequence, query head), lane l holds dims 2l and 2l + 1.  The parts join
-// in a fixed order: the prefix's shares, then the own chunks.
+// in a fixed order, the prefix's shares, then the own chunks, 32 at a time.  Little work behind a
+// chain of dependent loads: a part list written by the first kernel, the first accumulators loaded
+// beside the maxima.
 __global__ void __launch_bounds__(512) prefix_merge_kernel(const __grid_constant__ PrefixProblem P, const KCtx ctx) {
     griddep_wait();
     task_begin(ctx);
     const int lane = threadIdx.x & 31, h = threadIdx.x >> 5;
-    const int pair = blockIdx.x, t = pair / P.nkv, kvh = pair % P.nkv;
-    // the prefix's shares [s0, s0 + np) and this row in their slots
-    int s0 = 0, np = 0;
-    size_t row = 0;
-    const PrefixSeq q = P.seq[t];
-    if (q.tiles > 0) {
-        const int seq = (int)((unsigned)q.i * P.tile_inv >> 22), tile = kvh * q.tiles + seq;
-        const int x = q.step + tile * q.steps;
-        s0 = share_of(x, q);
-        np = share_of(x + q.steps - 1, q) - s0 + 1;
-        row = (size_t)(s0 + q.tile + tile) * kPrefixRows + (size_t)(q.i - seq * P.tile_seqs) * P.G + h;
-    }
-    int own = P.kv_len[t];
-    if (own < 0 || own > P.kv_cap) own = 0;
-    const int seen = own - (P.window > 0 ? max(0, own - P.window) : 0);
-    const int parts = np + chunks_of(seen, P);
-    const size_t own0 = (size_t)pair * P.S_max * 16 + h;
-    auto part_ml = [&](int k) {
-        const float* p = k < np ? P.pre_ml + (row + (size_t)k * kPrefixRows) * 2
-                                : P.own_ml + (own0 + (size_t)(k - np) * 16) * 2;
-        return __ldcg(reinterpret_cast<const float2*>(p));
-    };
-    float M = -INFINITY;
-    for (int k = lane; k < parts; k += 32) M = fmaxf(M, part_ml(k).x);
-    M = warp_max(M);
-    const float sub = M == -INFINITY ? 0.f : M;
-    float L = 0.f;
+    const int pair = blockIdx.x, t = pair / P.nkv, kvh = pair - t * P.nkv;
+    const PrefixParts q = P.parts[pair];
+    const size_t row = (size_t)q.slot * kPrefixRows + q.row + h;
+    const size_t own = ((size_t)pair * P.S_max - q.n_pre) * 16 + h;  // part k >= n_pre at own + 16 k
+    const int parts = q.n_pre + q.n_own;
+    float M = -INFINITY, L = 0.f;
     float2 a = make_float2(0.f, 0.f);
+#pragma unroll 1
     for (int k0 = 0; k0 < parts; k0 += 32) {
-        float w = 0.f;
-        if (k0 + lane < parts) {
-            const float2 ml = part_ml(k0 + lane);
-            w = ex2(ml.x - sub);
-            L = fmaf(w, ml.y, L);
-        }
         const int nk = min(32, parts - k0);
-#pragma unroll 4
-        for (int k = 0; k < nk; ++k) {
-            const float wk = __shfl_sync(0xffffffffu, w, k);
-            const float* p = k0 + k < np ? P.pre_acc + (row + (size_t)(k0 + k) * kPrefixRows) * 64
-                                         : P.own_acc + (own0 + (size_t)(k0 + k - np) * 16) * 64;
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(p + 2 * lane));
-            a.x = fmaf(wk, v.x, a.x);
-            a.y = fmaf(wk, v.y, a.y);
+        auto acc_of = [&](int k) {
+            const float* p = k < q.n_pre ? P.pre_acc + (row + (size_t)k * kPrefixRows) * 64
+                                         : P.own_acc + (own + (size_t)k * 16) * 64;
+            return __ldcg(reinterpret_cast<const float2*>(p) + lane);
+        };
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (lane < nk) {
+            const int k = k0 + lane;
+            const float* p = k < q.n_pre ? P.pre_ml + (row + (size_t)k * kPrefixRows) * 2
+                                         : P.own_ml + (own + (size_t)k * 16) * 2;
+            ml = __ldcg(reinterpret_cast<const float2*>(p));
+        }
+        float2 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < nk) v[i] = acc_of(k0 + i);
+        const float top = fmaxf(M, warp_max(ml.x)), sub = top == -INFINITY ? 0.f : top;
+        const float old = ex2(M - sub), w = ex2(ml.x - sub);
+        M = top;
+        L = fmaf(L, old, warp_sum(w * ml.y));
+        a.x *= old;
+        a.y *= old;
+#pragma unroll 1
+        for (int i0 = 0; i0 < nk; i0 += 8) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float wk = __shfl_sync(0xffffffffu, w, i0 + i);
+                if (i0 + i < nk) {
+                    a.x = fmaf(wk, v[i].x, a.x);
+                    a.y = fmaf(wk, v[i].y, a.y);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i0 + 8 + i < nk) v[i] = acc_of(k0 + i0 + 8 + i);
         }
     }
-    L = warp_sum(L);
     // a row that sees nothing: o = 0, lse = -inf
     const float inv = L == 0.f ? 0.f : 1.f / L;
     const size_t at = (size_t)t * P.nq + kvh * P.G + h;

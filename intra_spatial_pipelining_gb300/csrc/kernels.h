@@ -172,15 +172,10 @@ constexpr int kPrefixKeys = 128;
 constexpr int kPrefixCtas = 152;
 constexpr int kPrefixMax = 512;     // sequences, and prefixes, per call
 
-// What the merge needs of a sequence's group (written by the first CTA).
-struct PrefixSeq {
-    int tile;               // first tile of the group
-    int tiles;              // tiles per KV head (0: nothing visible)
-    int step;               // first step of the group
-    int steps;              // steps per tile
-    int i;                  // the sequence's place in the group
-    int n_long, q;          // the call's shares: the first n_long have q + 1 steps, the others q
-    int pad;
+// The parts of a (sequence, KV head): n_pre slots from `slot` on, the sequence's rows from `row`
+// on in each, and n_own own chunks.
+struct PrefixParts {
+    int slot, row, n_pre, n_own;
 };
 
 struct PrefixProblem {
@@ -193,7 +188,7 @@ struct PrefixProblem {
     float* pre_acc;         // [slot][kPrefixRows][64]
     float* own_ml;          // [T * nkv][S_max][16][2]
     float* own_acc;         // [T * nkv][S_max][16][64]
-    PrefixSeq* seq;         // [T]
+    PrefixParts* parts;     // [T * nkv]
     bf16* o;                // [T][nq * 64]
     float* lse;             // [T][nq] or NULL
     int T, nq, nkv, G, kv_cap, window, tile_seqs, chunk_log2, S_max;

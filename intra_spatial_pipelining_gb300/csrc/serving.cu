@@ -77,7 +77,7 @@ int launched(int e, const char* what) {
 
 // ---- attention over shared prefixes ----------------------------------------------------
 struct PrefixLayout {
-    size_t own_ml, own_acc, seq, pre_ml, pre_acc, total;
+    size_t own_ml, own_acc, parts, pre_ml, pre_acc, total;
     int chunk_log2, S_max, tile_seqs;
 };
 
@@ -110,7 +110,7 @@ PrefixLayout prefix_layout(const sgp_dims& d, int T, int kv_cap, int n_prefixes)
     const size_t groups = n_prefixes < T ? n_prefixes : T;
     const size_t tiles = d.n_kv_heads * (groups + T / y.tile_seqs);
     const size_t slots = n_prefixes > 0 ? kPrefixCtas + tiles : 0;
-    y.seq = take((size_t)T * sizeof(PrefixSeq));
+    y.parts = take(pairs * sizeof(PrefixParts));
     y.pre_ml = take(slots * kPrefixRows * 2 * 4);
     y.pre_acc = take(slots * kPrefixRows * 64 * 4);
     y.total = off;
@@ -162,7 +162,7 @@ int prefix_attention(const sgp_dims* d, const sgp_layer* cache, const sgp_prefix
     p.pre_acc = reinterpret_cast<float*>(w + y.pre_acc);
     p.own_ml = reinterpret_cast<float*>(w + y.own_ml);
     p.own_acc = reinterpret_cast<float*>(w + y.own_acc);
-    p.seq = reinterpret_cast<PrefixSeq*>(w + y.seq);
+    p.parts = reinterpret_cast<PrefixParts*>(w + y.parts);
     p.o = static_cast<bf16*>(o);
     p.lse = lse;
     p.T = T;
