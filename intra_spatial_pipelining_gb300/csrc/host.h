@@ -14,9 +14,9 @@ int host_fail_cuda(cudaError_t e, const char* what);
 int host_launch(cudaStream_t s, const void* func, dim3 grid, dim3 block, size_t smem, void** args,
                 bool overlap_ok);
 
-// bf16 tensor map over [rows][inner], box {box_inner, box_rows}, 128-byte swizzle.
-int host_tmap(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint32_t box_inner,
-              uint32_t box_rows);
+// bf16 tensor maps over two buffers of [rows][inner], box {box_inner, box_rows}, 128-byte swizzle.
+int host_tmap_pair(CUtensorMap* a, CUtensorMap* b, const void* base_a, const void* base_b,
+                   uint64_t inner, uint64_t rows, uint32_t box_inner, uint32_t box_rows);
 
 bool host_driver_ready();               // tensor maps can be encoded
 int host_sms();                         // SMs of the current device

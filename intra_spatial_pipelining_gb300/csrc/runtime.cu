@@ -63,6 +63,7 @@ int fail_arg(const char* what) {
 // =======================================================================================
 struct Driver {
     PFN_cuTensorMapEncodeTiled_v12000 encodeTiled = nullptr;
+    PFN_cuTensorMapReplaceAddress_v12000 replaceAddress = nullptr;
     PFN_cuGraphAddNode_v12030 graphAddNode = nullptr;
     PFN_cuKernelSetAttribute_v12000 kernelSetAttribute = nullptr;
     PFN_cuDeviceGetDevResource_v12040 devGetResource = nullptr;
@@ -92,6 +93,7 @@ Driver& drv() {
     static std::once_flag once;
     std::call_once(once, [] {
         d.core = get_entry("cuTensorMapEncodeTiled", d.encodeTiled, 12000) &&
+                 get_entry("cuTensorMapReplaceAddress", d.replaceAddress, 12000) &&
                  get_entry("cuGraphAddNode", d.graphAddNode, 12030) &&
                  get_entry("cuKernelSetAttribute", d.kernelSetAttribute, 12000);
         d.green = get_entry("cuDeviceGetDevResource", d.devGetResource, 12040) &&
@@ -960,9 +962,13 @@ int host_launch(cudaStream_t s, const void* func, dim3 grid, dim3 block, size_t 
                 bool overlap_ok) {
     return StreamLauncher(s).launch(func, grid, block, smem, args, overlap_ok);
 }
-int host_tmap(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint32_t box_inner,
-              uint32_t box_rows) {
-    return make_tmap(map, base, inner, rows, box_inner, box_rows);
+int host_tmap_pair(CUtensorMap* a, CUtensorMap* b, const void* base_a, const void* base_b,
+                   uint64_t inner, uint64_t rows, uint32_t box_inner, uint32_t box_rows) {
+    const int r = make_tmap(a, base_a, inner, rows, box_inner, box_rows);
+    if (r != SGP_OK) return r;
+    *b = *a;
+    CKD(drv().replaceAddress(b, const_cast<void*>(base_b)));
+    return SGP_OK;
 }
 bool host_driver_ready() { return drv().core; }
 int host_sms() { return device_sms(); }

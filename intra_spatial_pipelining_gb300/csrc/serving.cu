@@ -148,12 +148,10 @@ int prefix_attention(const sgp_dims* d, const sgp_layer* cache, const sgp_prefix
     PrefixProblem p;
     memset(&p, 0, sizeof(p));
     const uint64_t own_rows = (uint64_t)T * d->n_kv_heads * cache->kv_cap;
-    if ((r = host_tmap(&p.tmK, cache->k_cache, 64, own_rows, 64, 64))) return r;
-    if ((r = host_tmap(&p.tmV, cache->v_cache, 64, own_rows, 64, 64))) return r;
+    if ((r = host_tmap_pair(&p.tmK, &p.tmV, cache->k_cache, cache->v_cache, 64, own_rows, 64, 64))) return r;
     if (n > 0) {
         const uint64_t pre_rows = (uint64_t)n * d->n_kv_heads * pre->cap;
-        if ((r = host_tmap(&p.tmPK, pre->k, 64, pre_rows, 64, kPrefixKeys))) return r;
-        if ((r = host_tmap(&p.tmPV, pre->v, 64, pre_rows, 64, kPrefixKeys))) return r;
+        if ((r = host_tmap_pair(&p.tmPK, &p.tmPV, pre->k, pre->v, 64, pre_rows, 64, kPrefixKeys))) return r;
         p.prefix = {pre->prefix_of, pre->len, n, pre->cap};
     }
     p.q = static_cast<const bf16*>(q);

@@ -208,38 +208,48 @@ def _stream(stream) -> Optional[int]:
 
 
 # What the serving operators are given per call: a wrong type, size, layout or device would be
-# read as something else, so it raises here.
-_DTYPES = None
+# read as something else, so it raises here.  Called several times per launch, hence its brevity.
+def _dev() -> int:
+    """The current device's index; loads torch on first use."""
+    global torch, _BF16, _F32, _I32, _U8, _dev, _raw_stream
+    import torch
+    _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+    if not torch.cuda.is_available():
+        return 0                    # every tensor is on another device
+    torch.cuda.init()
+    _dev, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    return _dev()
 
 
-def _arg(t, kind: str, count: int, what: str, rows: bool = False) -> int:
-    global _DTYPES
-    if _DTYPES is None:
-        import torch
-        _DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32, "i32": torch.int32,
-                   "u8": torch.uint8, "device": torch.cuda.current_device}
-    if t.dtype is not _DTYPES[kind]:
-        raise ValueError(f"{what}: expected {_DTYPES[kind]}, got {t.dtype}")
-    if t.get_device() != _DTYPES["device"]():
-        raise ValueError(f"{what}: not on the current CUDA device ({t.device})")
-    if t.numel() < count or not (rows or t.is_contiguous()):
-        raise ValueError(f"{what}: expected at least {count} contiguous elements, got "
-                         f"{tuple(t.shape)} with strides {t.stride()}")
+def _bad(t, dtype, dev: int, count: int, what: str):
+    if t.dtype is not dtype:
+        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: on {t.device}, not on the current CUDA device {dev}")
+    raise ValueError(f"{what}: expected at least {count} contiguous elements, got "
+                     f"{tuple(t.shape)} with strides {t.stride()}")
+
+
+def _arg(t, dtype, dev: int, count: int, what: str) -> int:
+    if (t.dtype is not dtype or t.get_device() != dev or t.numel() < count
+            or not t.is_contiguous()):
+        _bad(t, dtype, dev, count, what)
     return t.data_ptr()
 
 
-def _rows(t, n: int, width: int, what: str):
+def _rows(t, dev: int, n: int, width: int, what: str):
     """Pointer and row stride of a [>= n][width] bf16 matrix whose rows are contiguous."""
-    _arg(t, "bf16", n * width, what, rows=True)
     shape, stride = t.shape, t.stride()
     if len(shape) != 2 or shape[0] < n or shape[1] != width or stride[1] != 1:
         raise ValueError(f"{what}: expected [{n}][{width}] with contiguous rows, got "
                          f"{tuple(shape)} with strides {stride}")
+    if t.dtype is not _BF16 or t.get_device() != dev:
+        _bad(t, _BF16, dev, n * width, what)
     return t.data_ptr(), stride[0] if shape[0] > 1 else width
 
 
-def _ws(t):
-    return _arg(t, "u8", 64, "workspace"), t.numel()
+def _on(stream, dev: int) -> int:
+    return _raw_stream(dev) if stream is None else getattr(stream, "cuda_stream", stream)
 
 
 # --------------------------------------------------------------------------------------
@@ -271,9 +281,10 @@ def make_heads(n_q_heads: int, n_kv_heads: int, head_dim: int = 64) -> sgp_dims:
 
 
 def _cache4(t, what: str):
+    dev = _dev()
     if t.dim() != 4:
         raise ValueError(f"{what}: expected [n][n_kv][cap][d], got {tuple(t.shape)}")
-    return _arg(t, "bf16", t.numel(), what)
+    return _arg(t, _BF16, dev, t.numel(), what)
 
 
 def make_cache(k_cache, v_cache, window: int = 0) -> sgp_layer:
@@ -291,8 +302,8 @@ def make_prefix(k, v, length, prefix_of) -> sgp_prefix:
     if k.shape != v.shape:
         raise ValueError("the prefixes' k and v differ in shape")
     p = sgp_prefix(_cache4(k, "prefix k"), _cache4(v, "prefix v"),
-                   _arg(length, "i32", k.shape[0], "prefix length"),
-                   _arg(prefix_of, "i32", 1, "prefix_of"), int(k.shape[0]), int(k.shape[2]))
+                   _arg(length, _I32, _dev(), k.shape[0], "prefix length"),
+                   _arg(prefix_of, _I32, _dev(), 1, "prefix_of"), int(k.shape[0]), int(k.shape[2]))
     p.tensors = (k, v, length, prefix_of)
     return p
 
@@ -306,9 +317,10 @@ def make_lora(a, b, scale=None, rank=None) -> sgp_lora:
     if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
         raise ValueError(f"adapters: a {tuple(a.shape)} and b {tuple(b.shape)} do not match")
     n, r, n_in = a.shape
-    p = sgp_lora(_arg(a, "bf16", a.numel(), "a"), _arg(b, "bf16", b.numel(), "b"),
-                 None if scale is None else _arg(scale, "f32", n, "scale"),
-                 None if rank is None else _arg(rank, "i32", n, "rank"), n, n_in, b.shape[1], r)
+    dev = _dev()
+    p = sgp_lora(_arg(a, _BF16, dev, a.numel(), "a"), _arg(b, _BF16, dev, b.numel(), "b"),
+                 None if scale is None else _arg(scale, _F32, dev, n, "scale"),
+                 None if rank is None else _arg(rank, _I32, dev, n, "rank"), n, n_in, b.shape[1], r)
     p.tensors = (a, b, scale, rank)
     return p
 
@@ -426,25 +438,27 @@ def sgp_prefix_attention_workspace_bytes(dims, n_tokens: int, kv_cap: int,
 
 def sgp_prefix_attention(dims, cache: sgp_layer, prefix: Optional[sgp_prefix], kv_len, q, o, lse,
                          n_tokens: int, workspace, stream=None) -> int:
+    dev = _dev()
     rows = n_tokens * dims.n_q_heads
-    ws, nbytes = _ws(workspace)
     return check(lib().sgp_prefix_attention(
         C.byref(dims), C.byref(cache), None if prefix is None else C.byref(prefix),
-        _arg(kv_len, "i32", n_tokens, "kv_len"), _arg(q, "bf16", rows * dims.head_dim, "q"),
-        _arg(o, "bf16", rows * dims.head_dim, "o"),
-        None if lse is None else _arg(lse, "f32", rows, "lse"), n_tokens, ws, nbytes,
-        _stream(stream)), "sgp_prefix_attention")
+        _arg(kv_len, _I32, dev, n_tokens, "kv_len"), _arg(q, _BF16, dev, rows * dims.head_dim, "q"),
+        _arg(o, _BF16, dev, rows * dims.head_dim, "o"),
+        None if lse is None else _arg(lse, _F32, dev, rows, "lse"), n_tokens,
+        _arg(workspace, _U8, dev, 64, "workspace"), workspace.numel(), _on(stream, dev)),
+        "sgp_prefix_attention")
 
 
 def sgp_attention_weights(dims, cache: sgp_layer, kv_len, q, lse, acc, n_tokens: int, workspace,
                           stream=None) -> int:
+    dev = _dev()
     rows = n_tokens * dims.n_q_heads
-    ws, nbytes = _ws(workspace)
     return check(lib().sgp_attention_weights(
-        C.byref(dims), C.byref(cache), _arg(kv_len, "i32", n_tokens, "kv_len"),
-        _arg(q, "bf16", rows * dims.head_dim, "q"), _arg(lse, "f32", rows, "lse"),
-        _arg(acc, "f32", n_tokens * dims.n_kv_heads * cache.kv_cap, "acc"), n_tokens, ws, nbytes,
-        _stream(stream)), "sgp_attention_weights")
+        C.byref(dims), C.byref(cache), _arg(kv_len, _I32, dev, n_tokens, "kv_len"),
+        _arg(q, _BF16, dev, rows * dims.head_dim, "q"), _arg(lse, _F32, dev, rows, "lse"),
+        _arg(acc, _F32, dev, n_tokens * dims.n_kv_heads * cache.kv_cap, "acc"), n_tokens,
+        _arg(workspace, _U8, dev, 64, "workspace"), workspace.numel(), _on(stream, dev)),
+        "sgp_attention_weights")
 
 
 def sgp_kv_evict_workspace_bytes(dims, n_tokens: int, budget: int) -> int:
@@ -453,27 +467,29 @@ def sgp_kv_evict_workspace_bytes(dims, n_tokens: int, budget: int) -> int:
 
 def sgp_kv_evict(dims, source: sgp_layer, target: sgp_layer, policy: sgp_evict, kv_len,
                  kv_len_out, acc, acc_out, kept, n_tokens: int, workspace, stream=None) -> int:
+    dev = _dev()
     pairs = n_tokens * dims.n_kv_heads
-    ws, nbytes = _ws(workspace)
     return check(lib().sgp_kv_evict(
         C.byref(dims), C.byref(source), C.byref(target), C.byref(policy),
-        _arg(kv_len, "i32", n_tokens, "kv_len"), _arg(kv_len_out, "i32", n_tokens, "kv_len_out"),
-        _arg(acc, "f32", pairs * source.kv_cap, "acc"),
-        _arg(acc_out, "f32", pairs * target.kv_cap, "acc_out"),
-        None if kept is None else _arg(kept, "i32", pairs * policy.budget, "kept"), n_tokens, ws,
-        nbytes, _stream(stream)), "sgp_kv_evict")
+        _arg(kv_len, _I32, dev, n_tokens, "kv_len"),
+        _arg(kv_len_out, _I32, dev, n_tokens, "kv_len_out"),
+        _arg(acc, _F32, dev, pairs * source.kv_cap, "acc"),
+        _arg(acc_out, _F32, dev, pairs * target.kv_cap, "acc_out"),
+        None if kept is None else _arg(kept, _I32, dev, pairs * policy.budget, "kept"), n_tokens,
+        _arg(workspace, _U8, dev, 64, "workspace"), workspace.numel(), _on(stream, dev)),
+        "sgp_kv_evict")
 
 
 def sgp_lora_apply(lora: sgp_lora, adapter_of, x, y_in, y_out, n_tokens: int, workspace,
                    stream=None) -> int:
-    n_in = getattr(lora, "in")
-    px, ld_x = _rows(x, n_tokens, n_in, "x")
-    pi, ld_i = _rows(y_in, n_tokens, lora.out, "y_in")
-    po, ld_o = _rows(y_out, n_tokens, lora.out, "y_out")
-    ws, nbytes = _ws(workspace)
-    return check(lib().sgp_lora_apply(C.byref(lora), _arg(adapter_of, "i32", n_tokens, "adapter_of"),
-                                      px, ld_x, pi, ld_i, po, ld_o, n_tokens, ws, nbytes,
-                                      _stream(stream)), "sgp_lora_apply")
+    dev = _dev()
+    px, ld_x = _rows(x, dev, n_tokens, getattr(lora, "in"), "x")
+    pi, ld_i = _rows(y_in, dev, n_tokens, lora.out, "y_in")
+    po, ld_o = _rows(y_out, dev, n_tokens, lora.out, "y_out")
+    return check(lib().sgp_lora_apply(
+        C.byref(lora), _arg(adapter_of, _I32, dev, n_tokens, "adapter_of"), px, ld_x, pi, ld_i, po,
+        ld_o, n_tokens, _arg(workspace, _U8, dev, 64, "workspace"), workspace.numel(),
+        _on(stream, dev)), "sgp_lora_apply")
 
 
 def sgp_status_from_workspace(workspace, stream=None) -> int:

@@ -172,7 +172,7 @@ def test_binding_refuses_what_the_abi_cannot_see(lib):
         sgp.make_cache(f.bfloat16(), f.bfloat16()[:, :, :4])   # shapes differ
     with pytest.raises(ValueError):
         sgp.make_lora(torch.zeros(2, 16, 64), torch.zeros(2, 96, 8))
-    with pytest.raises((ValueError, RuntimeError, AssertionError)):
+    with pytest.raises(ValueError):
         sgp.make_cache(f.bfloat16(), f.bfloat16())             # not on a GPU
 
 
