@@ -450,10 +450,10 @@ __device__ void own_part(const PrefixProblem& P, const Plan& pl, uint8_t* ring_a
 //     S = Q K^T   (M = 128 rows, N = 64 positions, K = 64), accumulators in tensor memory;
 //     P = exp2(scale S - m) by the group's threads, one row each, back to tensor memory as bf16;
 //     O += P V    (M = 128, N = 64 dims, K = 64), P read from tensor memory.
-// S and P have two buffers each, and a half takes one signal either way: the softmax's "P(i) is
-// written" also frees S(i), and the products' "S(i + 2) is complete" also says that O holds P(i)
-// (it was issued behind it).  What a wait costs, 100 to 250 cycles although it passes at once, is
-// what a half has to be long against.
+// S and P have two buffers each: "P(i) is written" also frees S(i), S(i + 2) is issued behind the
+// product of P(i), and that product has a barrier of its own (S(i + 2) being complete does not say
+// that it is: the two do not finish in order).  What a wait costs, 100 to 250 cycles although it
+// passes at once, is what a half has to be long against.
 // The weights are taken against a maximum m that is only raised when a row's scores pass it by
 // more than 2^8 (weights up to 256 lose nothing in bf16 or fp32); the half's own maximum is found
 // beside the exponentials, and in the rare case that it does, O and the sum are rescaled and the
@@ -466,9 +466,9 @@ constexpr uint32_t kTmemS = 0, kTmemP = 256, kTmemO = 384;  // columns; per grou
 struct PrefixBars {
     uint64_t kv_full[kPStages], kv_empty[kPStages];
     uint64_t q_full[2];        // the group's query rows are in shared memory
-    uint64_t s_full[2][2];     // [group][buffer]; the group's half i uses buffer i & 1
+    uint64_t s_full[2][2];     // [group][buffer]; the group's half i uses buffer i & 1, phase i >> 1
     uint64_t p_full[2][2];
-    uint64_t pv_done[2];       // phase i: O holds half i (a rescale and a tile's end wait for it)
+    uint64_t pv_done[2][2];    // O holds half i, P's buffer is free
     uint64_t own[kOwnWarps][2];  // an own warp's K and V halves
     uint32_t tmem;
     int err;
@@ -524,10 +524,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
         for (int h = 0; h < 2; ++h) {
             mbar_init(&bar.q_full[h], 4);
-            mbar_init(&bar.pv_done[h], 1);
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&bar.s_full[h][i], 1);
                 mbar_init(&bar.p_full[h][i], 4);
+                mbar_init(&bar.pv_done[h][i], 1);
             }
         }
         for (int i = 0; i < kOwnWarps; ++i) {
@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
 #pragma unroll
                     for (int k = 0; k < kPSub / 16; ++k)  // O += P V
                         tc_mma_bf16_ta(to, tp + 32 * buf + 8 * k, dv + k * (16 * 128 / 16), id_o, !(j == 0 && k == 0));
-                    tc_commit(&bar.pv_done[h]);
+                    tc_commit(&bar.pv_done[h][buf]);
                     if ((j & 1) || j + 1 == halves) {
                         tc_commit(&bar.kv_empty[st_p]);
                         if (++st_p == kPStages) st_p = 0;
@@ -743,6 +743,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                         tmem_st_wait();
                     }
                     const float2 l_old = l2;
+                    bool first = true;
                     while (true) {
                         // a row that has seen nothing yet: every score is -inf, every weight 0
                         const float sub = m == -INFINITY ? 0.f : -m;
@@ -764,8 +765,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
                                 // the weight's rounding to bf16, the second product's operand type
                                 w[e] = pack_bf16x2(v.x, v.y);
                             }
+                            if (c == 0 && first && it > 1) {  // P(it - 2) has been multiplied
+                                if (!(ok = wait(&bar.pv_done[h][buf], ((it >> 1) & 1u) ^ 1u, 33))) break;
+                                tc_fence_after();
+                            }
                             tmem_st_x16(tp + 32 * buf + 16 * c, w);
                         }
+                        if (!ok) break;
+                        first = false;
                         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * P.scale_log2;
                         // the first half also raises from below: its scores may be far under 0
                         const bool far = top > m + kPRaise || (j == 0 && m == 0.f && top < -kPRaise);
@@ -774,8 +781,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
                         const float c = j == 0 || m == -INFINITY ? 0.f : ex2(m - nm);
                         m = nm;
                         l2 = make_float2(l_old.x * c, l_old.y * c);
+                        tmem_st_wait();
                         if (j == 0) continue;
-                        if (!(ok = wait(&bar.pv_done[h], (it - 1) & 1u, 25))) break;
+                        if (!(ok = wait(&bar.pv_done[h][buf ^ 1u], ((it - 1) >> 1) & 1u, 25))) break;
                         tc_fence_after();
 #pragma unroll 1
                         for (int q = 0; q < 64; q += 16) {
@@ -796,7 +804,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             }
             if (!ok) break;
             // the last product, then this row's partial
-            if (!wait(&bar.pv_done[h], (it - 1) & 1u, 26)) break;
+            if (!wait(&bar.pv_done[h][(it - 1) & 1u], ((it - 1) >> 1) & 1u, 26)) break;
             tc_fence_after();
             if (live) {
                 const size_t slot = b + (size_t)(pl.tile0[s.g] + s.kvh * pl.tiles[s.g] + s.tile);

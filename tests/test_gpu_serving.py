@@ -134,6 +134,31 @@ def test_prefix_attention(name):
     assert torch.equal(first, x.o)
 
 
+@pytest.mark.parametrize("T,nq,nkv,p_lens,own,of,window", [
+    (64, 64, 8, [4096], [(t * 53) % 600 for t in range(64)], [0] * 64, 0),
+    (300, 8, 1, [9000, 2000], [(t * 7) % 90 for t in range(300)], [t % 2 for t in range(300)], 0),
+    (128, 32, 4, [5000], [(t * 5) % 128 for t in range(128)], [0] * 128, 3000)])
+def test_prefix_attention_same_bits_every_time(T, nq, nkv, p_lens, own, of, window):
+    """Every SM busy for many steps: a buffer taken too early would show as another result."""
+    x = Prefix(77, T, nq, nkv, p_lens, own, of, window)
+    x.run()
+    assert x.status() == sgp.SGP_OK
+    o, lse = x.o.clone(), x.lse.clone()
+    other = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(60):
+        x.o.zero_()
+        x.run()
+        other += (x.o != o).any() | (x.lse != lse).any()
+    assert int(other) == 0
+    keep = [0, T // 2, T - 1]
+    y = Prefix(77, T, nq, nkv, p_lens, own, of, window)
+    z = lambda t: np.nan_to_num(f64(t))
+    want = S.prefix_attention(f64(y.q[keep]), z(y.k[keep]), z(y.v[keep]), [own[t] for t in keep], z(y.pk),
+                              z(y.pv), p_lens, [of[t] for t in keep], window)
+    within("o", o[keep], want[0], want[2])
+    within("lse", lse[keep], want[1], want[3])
+
+
 def test_prefix_attention_large_scores():
     """Scores of a few hundred: the running maximum moves by more than fp32's exponent range of
     a weight, and most weights vanish."""
