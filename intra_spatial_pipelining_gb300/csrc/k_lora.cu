@@ -5,7 +5,8 @@
 // eight CTAs takes a tile.  First product: the 64 warps of the cluster split the input features,
 // M = 16 sequences, N = 8 ranks, fragments straight from global memory (both operands read the
 // same permutation of the features, so that every lane loads 16 bytes); the warps' sums join in
-// shared memory, the CTAs' in distributed shared memory, both in a fixed order.  Second product:
+// shared memory, the CTAs' in distributed shared memory, both in a fixed order (stored into every
+// other CTA instead of loaded from there, the sums came 1 us later).  Second product:
 // the warps split the output features.  The intermediate A x is kept as the sum of two bf16 (16
 // bits of mantissa), so that it loses nothing against y's own rounding.
 // Each adapter's A and B are read once per tile; with few sequences per adapter they are what
@@ -24,6 +25,7 @@ constexpr int kLWarps = kLThreads / 32;
 constexpr int kLCluster = 8;
 constexpr int kLTile = 16;
 constexpr int kLMaxT = 512;
+constexpr int kLBlocks = kLMaxT / 32;
 constexpr int kLClusters = 64;  // at most, per launch
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -31,16 +33,27 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_sync() {
+__device__ __forceinline__ void cluster_arrive() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float dsmem_ld(const float* p, uint32_t rank) {
+__device__ __forceinline__ float4 dsmem_ld(uint32_t p, uint32_t rank) {
     uint32_t a;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    float4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(p), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(a)
+                 : "memory");
     return v;
+}
+__device__ __forceinline__ void add4(float4& a, const float4& b) {
+    a.x += b.x;
+    a.y += b.y;
+    a.z += b.z;
+    a.w += b.w;
 }
 
 __host__ __device__ inline int lora_rank_pad(int r) { return (r + 15) & ~15; }
@@ -48,12 +61,12 @@ inline size_t lora_smem_bytes(int n, int r) {
     const size_t rp = lora_rank_pad(r);
     return (size_t)(kLWarps + 1) * kLTile * rp * 4   // warps' sums, the CTA's sum
            + 2 * kLTile * (rp + 8) * 2               // A x as two bf16
-           + (3 * kLMaxT + kLTile + n + 1) * 4;
+           + (4 * kLMaxT + kLTile + kLBlocks + n + 1) * 4 + kLBlocks * kLMaxT;
 }
 
 // RP: rank, rounded up to 16, at most
 template <int RP>
-__global__ void __cluster_dims__(kLCluster, 1, 1) __launch_bounds__(kLThreads)
+__global__ void __cluster_dims__(kLCluster, 1, 1) __launch_bounds__(kLThreads, RP <= 64 ? 2 : 1)
     lora_kernel(const LoraProblem P, const KCtx ctx) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     constexpr int kNT = RP / 8, kKS = RP / 16;
@@ -63,43 +76,69 @@ __global__ void __cluster_dims__(kLCluster, 1, 1) __launch_bounds__(kLThreads)
     bf16* hi = reinterpret_cast<bf16*>(part + kLTile * rp);  // [16][rp + 8]
     bf16* lo = hi + kLTile * (rp + 8);
     int* adp = reinterpret_cast<int*>(lo + kLTile * (rp + 8));  // [T] adapter, n: none
-    int* rnk = adp + kLMaxT;                                 // [T] place in the group
+    int* key = adp + kLMaxT;                                 // [T] first sequence with the adapter
+    int* rnk = key + kLMaxT;                                 // [T] place in the group
     int* lead = rnk + kLMaxT;                                // [units] first sequence of a tile
     int* tok = lead + kLMaxT;                                // [16]
-    int* cnt = tok + kLTile;                                 // [n + 1]
-    __shared__ int n_units;
+    int* leads = tok + kLTile;                               // [blocks] tiles that begin in a block
+    int* first = leads + kLBlocks;                           // [n + 1] first sequence with an adapter
+    uint8_t* count = reinterpret_cast<uint8_t*>(first + P.n + 1);  // [blocks][T] sequences by key
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, cq = lane & 3;
     const uint32_t cr = cluster_rank();
     const int cluster = blockIdx.x / kLCluster, clusters = gridDim.x / kLCluster;
+    const int blocks = (P.T + 31) >> 5;
     griddep_wait();
     task_begin(ctx);
 
-    for (int i = tid; i <= P.n; i += kLThreads) cnt[i] = 0;
+    // The tiles.  Every CTA makes the same list, sequences in blocks of 32, a warp to a block: the
+    // blocks' counts by group are added up by whoever needs them.
+#pragma unroll 1
+    for (int i = tid; i <= P.n; i += kLThreads) first[i] = kLMaxT;
+#pragma unroll 1
+    for (int i = tid; i < blocks * kLMaxT / 4; i += kLThreads) reinterpret_cast<uint32_t*>(count)[i] = 0;
+    __syncthreads();
+#pragma unroll 1
     for (int t = tid; t < P.T; t += kLThreads) {
         int a = P.adapter_of[t];
         if (a >= P.n && blockIdx.x == 0) report(ctx, ST_BOUNDS, (uint32_t)a);
-        adp[t] = a >= 0 && a < P.n ? a : P.n;
+        a = a >= 0 && a < P.n ? a : P.n;
+        adp[t] = a;
+        atomicMin(&first[a], t);
     }
     __syncthreads();
-    if (warp == 0) {
-        int units = 0;
-        for (int t0 = 0; t0 < P.T; t0 += 32) {
-            const int t = t0 + lane;
-            const int a = t < P.T ? adp[t] : -1;
-            const uint32_t same = __match_any_sync(0xffffffffu, a), below = (1u << lane) - 1u;
-            const int had = a >= 0 ? cnt[a] : 0, r = had + __popc(same & below);
-            __syncwarp();
-            if (a >= 0) {
-                rnk[t] = r;
-                if ((same & below) == 0) cnt[a] = had + __popc(same);
-            }
-            const bool first = a >= 0 && r % kLTile == 0;
-            const uint32_t m = __ballot_sync(0xffffffffu, first);
-            if (first) lead[units + __popc(m & below)] = t;
-            units += __popc(m);
-            __syncwarp();
+    const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 1
+    for (int t = tid; t < blocks * 32; t += kLThreads) {
+        const int k = t < P.T ? first[adp[t]] : -1;
+        const uint32_t same = __match_any_sync(0xffffffffu, k);
+        if (k >= 0) {
+            key[t] = k;
+            rnk[t] = __popc(same & below);
+            if ((same & below) == 0) count[(t >> 5) * kLMaxT + k] = (uint8_t)__popc(same);
         }
-        if (lane == 0) n_units = units;
+    }
+    __syncthreads();
+    uint32_t starts[kLMaxT / kLThreads];  // tiles that begin in this warp's blocks
+#pragma unroll
+    for (int i = 0; i < kLMaxT / kLThreads; ++i) {
+        const int t = i * kLThreads + tid;
+        int r = 1;
+        if (t < P.T) {
+            r = rnk[t];
+#pragma unroll 1
+            for (int b = 0; b < (t >> 5); ++b) r += count[b * kLMaxT + key[t]];
+            rnk[t] = r;
+        }
+        starts[i] = __ballot_sync(0xffffffffu, t < P.T && r % kLTile == 0);
+        if (lane == 0) leads[t >> 5] = __popc(starts[i]);
+    }
+    __syncthreads();
+    const int n_units = __reduce_add_sync(0xffffffffu, lane < kLBlocks ? leads[lane] : 0);
+#pragma unroll
+    for (int i = 0; i < kLMaxT / kLThreads; ++i) {
+        const int t = i * kLThreads + tid;
+        const int before = __reduce_add_sync(0xffffffffu, lane < (t >> 5) ? leads[lane] : 0);
+        if (starts[i] >> lane & 1) lead[before + __popc(starts[i] & below)] = t;
     }
     __syncthreads();
 
@@ -108,10 +147,12 @@ __global__ void __cluster_dims__(kLCluster, 1, 1) __launch_bounds__(kLThreads)
     const int kb0 = gw * k_blocks / (kLCluster * kLWarps), kb1 = (gw + 1) * k_blocks / (kLCluster * kLWarps);
     const int ob0 = gw * o_blocks / (kLCluster * kLWarps), ob1 = (gw + 1) * o_blocks / (kLCluster * kLWarps);
     for (int u = cluster; u < n_units; u += clusters) {
-        const int a = adp[lead[u]], tile = rnk[lead[u]] / kLTile;
-        const int m = min(kLTile, cnt[a] - tile * kLTile);
+        const int t0 = lead[u], a = adp[t0], k0 = key[t0], tile = rnk[t0] / kLTile;
+        const int all = __reduce_add_sync(0xffffffffu, lane < blocks ? (int)count[lane * kLMaxT + k0] : 0);
+        const int m = min(kLTile, all - tile * kLTile);
+#pragma unroll 1
         for (int t = tid; t < P.T; t += kLThreads)
-            if (adp[t] == a && rnk[t] / kLTile == tile) tok[rnk[t] % kLTile] = t;
+            if (key[t] == k0 && rnk[t] / kLTile == tile) tok[rnk[t] % kLTile] = t;
         __syncthreads();
         const int t_lo = tok[g < m ? g : 0], t_hi = tok[g + 8 < m ? g + 8 : 0];
         int rank = 0;
@@ -122,6 +163,7 @@ __global__ void __cluster_dims__(kLCluster, 1, 1) __launch_bounds__(kLThreads)
                 rank = 0;
             }
         }
+        const float scale = rank > 0 && P.scale ? P.scale[a] : 1.f;
         if (rank == 0) {  // no adapter: the rows pass through
             if (P.y_out != P.y_in)
                 for (int i = 0; i < m; ++i) {
@@ -134,26 +176,54 @@ __global__ void __cluster_dims__(kLCluster, 1, 1) __launch_bounds__(kLThreads)
             continue;
         }
 
+        const bf16* B = P.b + (size_t)a * P.out * P.max_rank;
+        uint2 wb[kKS][4];
+        uint4 yb[2];
+        auto load_out = [&](int ob) {
+#pragma unroll
+            for (int ks = 0; ks < kKS; ++ks) {
+                const int k = ks * 16 + cq * 4;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    // column 2c of tile j is feature 8c + 2j: a lane's outputs are neighbours
+                    const int f = ob * 32 + (g >> 1) * 8 + j * 2 + (g & 1);
+                    wb[ks][j] = k < rank ? *reinterpret_cast<const uint2*>(B + (size_t)f * P.max_rank + k)
+                                         : make_uint2(0, 0);
+                }
+            }
+            if (g < m) yb[0] = *reinterpret_cast<const uint4*>(P.y_in + (size_t)t_lo * P.ld_y_in + ob * 32 + cq * 8);
+            if (g + 8 < m) yb[1] = *reinterpret_cast<const uint4*>(P.y_in + (size_t)t_hi * P.ld_y_in + ob * 32 + cq * 8);
+        };
         // ---- A x: this warp's input features ----
         float acc[kNT][4];
 #pragma unroll
         for (int j = 0; j < kNT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
         const bf16* A = P.a + (size_t)a * P.max_rank * P.in;
         const uint4 z = make_uint4(0, 0, 0, 0);
-        for (int kb = kb0; kb < kb1; ++kb) {
+        uint4 xa[2], w[kNT];
+        auto load_in = [&](int kb) {
             const int k = kb * 32 + cq * 8;
-            const uint4 x0 = g < m ? *reinterpret_cast<const uint4*>(P.x + (size_t)t_lo * P.ld_x + k) : z;
-            const uint4 x1 = g + 8 < m ? *reinterpret_cast<const uint4*>(P.x + (size_t)t_hi * P.ld_x + k) : z;
-            uint4 w[kNT];
+            xa[0] = g < m ? *reinterpret_cast<const uint4*>(P.x + (size_t)t_lo * P.ld_x + k) : z;
+            xa[1] = g + 8 < m ? *reinterpret_cast<const uint4*>(P.x + (size_t)t_hi * P.ld_x + k) : z;
 #pragma unroll
             for (int j = 0; j < kNT; ++j)
                 w[j] = j * 8 + g < rank ? *reinterpret_cast<const uint4*>(A + (size_t)(j * 8 + g) * P.in + k) : z;
-            const uint32_t f0[4] = {x0.x, x1.x, x0.y, x1.y}, f1[4] = {x0.z, x1.z, x0.w, x1.w};
+        };
+        if (kb0 < kb1) load_in(kb0);
+#pragma unroll 1
+        for (int kb = kb0; kb < kb1; ++kb) {
+            const uint32_t f0[4] = {xa[0].x, xa[1].x, xa[0].y, xa[1].y}, f1[4] = {xa[0].z, xa[1].z, xa[0].w, xa[1].w};
+            uint4 c[kNT];
+#pragma unroll
+            for (int j = 0; j < kNT; ++j) c[j] = w[j];
+            // the next block is on its way during the products (where registers allow)
+            if (RP <= 32 && kb + 1 < kb1) load_in(kb + 1);
 #pragma unroll
             for (int j = 0; j < kNT; ++j) {
-                mma16816(acc[j], f0, w[j].x, w[j].y);
-                mma16816(acc[j], f1, w[j].z, w[j].w);
+                mma16816(acc[j], f0, c[j].x, c[j].y);
+                mma16816(acc[j], f1, c[j].z, c[j].w);
             }
+            if (RP > 32 && kb + 1 < kb1) load_in(kb + 1);
         }
 #pragma unroll
         for (int j = 0; j < kNT; ++j)
@@ -162,29 +232,42 @@ __global__ void __cluster_dims__(kLCluster, 1, 1) __launch_bounds__(kLThreads)
                 *reinterpret_cast<float2*>(r + g * rp) = make_float2(acc[j][0], acc[j][1]);
                 *reinterpret_cast<float2*>(r + (g + 8) * rp) = make_float2(acc[j][2], acc[j][3]);
             }
+        if (ob0 < ob1) load_out(ob0);  // on its way while the sums are joined
         __syncthreads();
-        for (int i = tid; i < kLTile * rp; i += kLThreads) {
-            float s = 0.f;
+        const int n4 = kLTile * rp / 4;
+        for (int i = tid; i < n4; i += kLThreads) {
+            float4 s = reinterpret_cast<const float4*>(red)[i];
 #pragma unroll
-            for (int w = 0; w < kLWarps; ++w) s += red[(size_t)w * kLTile * rp + i];
-            part[i] = s;
+            for (int w = 1; w < kLWarps; ++w) add4(s, reinterpret_cast<const float4*>(red)[w * n4 + i]);
+            reinterpret_cast<float4*>(part)[i] = s;
         }
-        cluster_sync();
-        const float scale = P.scale ? P.scale[a] : 1.f;
-        for (int i = tid; i < kLTile * rp; i += kLThreads) {
-            float s = 0.f;
+        cluster_arrive();
+        cluster_wait();
+        for (int i = tid; i < n4; i += kLThreads) {
+            float4 v[kLCluster];
 #pragma unroll
-            for (int c = 0; c < kLCluster; ++c) s += dsmem_ld(part + i, c);
-            s *= scale;
-            const bf16 h = __float2bfloat16_rn(s);
-            const int at = (i / rp) * (rp + 8) + i % rp;
-            hi[at] = h;
-            lo[at] = __float2bfloat16_rn(s - __bfloat162float(h));
+            for (int c = 0; c < kLCluster; ++c) v[c] = dsmem_ld(smem_u32(part + 4 * i), c);
+#pragma unroll
+            for (int c = 1; c < kLCluster; ++c) add4(v[0], v[c]);
+            const float s[4] = {v[0].x * scale, v[0].y * scale, v[0].z * scale, v[0].w * scale};
+            float r[4];
+            uint2 h, l;
+            h.x = pack_bf16x2(s[0], s[1]);
+            h.y = pack_bf16x2(s[2], s[3]);
+            r[0] = s[0] - __uint_as_float(h.x << 16);
+            r[1] = s[1] - __uint_as_float(h.x & 0xffff0000u);
+            r[2] = s[2] - __uint_as_float(h.y << 16);
+            r[3] = s[3] - __uint_as_float(h.y & 0xffff0000u);
+            l.x = pack_bf16x2(r[0], r[1]);
+            l.y = pack_bf16x2(r[2], r[3]);
+            const int row = 4 * i / rp, at = row * (rp + 8) + 4 * i - row * rp;
+            *reinterpret_cast<uint2*>(hi + at) = h;
+            *reinterpret_cast<uint2*>(lo + at) = l;
         }
-        cluster_sync();  // every CTA has read the others' sums (and hi, lo are complete)
+        cluster_arrive();  // this CTA has read the others' sums
+        __syncthreads();   // hi and lo are complete
 
         // ---- y += B (A x): this warp's output features, 32 at a time ----
-        const bf16* B = P.b + (size_t)a * P.out * P.max_rank;
         for (int ob = ob0; ob < ob1; ++ob) {
             float d[4][4];
 #pragma unroll
@@ -193,17 +276,13 @@ __global__ void __cluster_dims__(kLCluster, 1, 1) __launch_bounds__(kLThreads)
             for (int ks = 0; ks < kKS; ++ks) {
                 const int k = ks * 16 + cq * 4;
                 if (ks * 16 >= rank) break;
-                uint2 w[4];
+                if (k + 3 >= rank) {  // what lies behind the rank is not the adapter's
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    // column 2c of tile j is feature 8c + 2j: a lane's outputs are neighbours
-                    const int f = ob * 32 + (g >> 1) * 8 + j * 2 + (g & 1);
-                    w[j] = k < rank ? *reinterpret_cast<const uint2*>(B + (size_t)f * P.max_rank + k)
-                                    : make_uint2(0, 0);
-                    // what lies behind the rank is not the adapter's
-                    if (k + 1 >= rank) w[j].x &= 0xffffu;
-                    if (k + 2 >= rank) w[j].y = 0u;
-                    else if (k + 3 >= rank) w[j].y &= 0xffffu;
+                    for (int j = 0; j < 4; ++j) {
+                        if (k + 1 >= rank) wb[ks][j].x &= 0xffffu;
+                        if (k + 2 >= rank) wb[ks][j].y = 0u;
+                        else wb[ks][j].y &= 0xffffu;
+                    }
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -212,16 +291,18 @@ __global__ void __cluster_dims__(kLCluster, 1, 1) __launch_bounds__(kLThreads)
                     const uint2 v1 = *reinterpret_cast<const uint2*>(v + (g + 8) * (rp + 8) + k);
                     const uint32_t f[4] = {v0.x, v1.x, v0.y, v1.y};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) mma16816(d[j], f, w[j].x, w[j].y);
+                    for (int j = 0; j < 4; ++j) mma16816(d[j], f, wb[ks][j].x, wb[ks][j].y);
                 }
             }
+            const uint4 y0[2] = {yb[0], yb[1]};
+            if (ob + 1 < ob1) load_out(ob + 1);
             const int f0 = ob * 32 + cq * 8;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if (g + 8 * h >= m) continue;
                 const size_t t = h ? t_hi : t_lo;
                 float y[8];
-                unpack8(*reinterpret_cast<const uint4*>(P.y_in + t * P.ld_y_in + f0), y);
+                unpack8(y0[h], y);
                 uint4 o;
                 o.x = pack_bf16x2(y[0] + d[0][2 * h], y[1] + d[0][2 * h + 1]);
                 o.y = pack_bf16x2(y[2] + d[1][2 * h], y[3] + d[1][2 * h + 1]);
@@ -230,6 +311,7 @@ __global__ void __cluster_dims__(kLCluster, 1, 1) __launch_bounds__(kLThreads)
                 *reinterpret_cast<uint4*>(P.y_out + t * P.ld_y_out + f0) = o;
             }
         }
+        cluster_wait();   // every CTA has read this one's sum
         __syncthreads();  // hi, lo and tok are free
     }
     task_end(ctx);
