@@ -59,7 +59,7 @@ __device__ __forceinline__ void add4(float4& a, const float4& b) {
 __host__ __device__ inline int lora_rank_pad(int r) { return (r + 15) & ~15; }
 inline size_t lora_smem_bytes(int n, int r) {
     const size_t rp = lora_rank_pad(r);
-    return (size_t)(kLWarps + 1) * kLTile * rp * 4   // warps' sums, the CTA's sum
+    return (size_t)(kLWarps / (rp <= 32 ? 1 : rp <= 64 ? 2 : 4) + 1) * kLTile * rp * 4  // warps' sums, the CTA's sum
            + 2 * kLTile * (rp + 8) * 2               // A x as two bf16
            + (4 * kLMaxT + kLTile + kLBlocks + n + 1) * 4 + kLBlocks * kLMaxT;
 }
@@ -69,10 +69,13 @@ template <int RP>
 __global__ void __cluster_dims__(kLCluster, 1, 1) __launch_bounds__(kLThreads, RP <= 64 ? 2 : 1)
     lora_kernel(const LoraProblem P, const KCtx ctx) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    constexpr int kNT = RP / 8, kKS = RP / 16;
+    // a warp takes 32 ranks at most: more of them share its input features between warps, so that
+    // the next block's loads can be in flight during the products (64 ranks to a warp spilled)
+    constexpr int kRG = RP <= 32 ? 1 : RP / 32, kKW = kLWarps / kRG;
+    constexpr int kNT = (RP <= 32 ? RP : 32) / 8, kKS = RP / 16;
     const int rp = lora_rank_pad(P.max_rank);
-    float* red = reinterpret_cast<float*>(smem_raw);         // [warps][16][rp]
-    float* part = red + kLWarps * kLTile * rp;               // [16][rp]
+    float* red = reinterpret_cast<float*>(smem_raw);         // [kKW warps][16][rp]
+    float* part = red + kKW * kLTile * rp;                   // [16][rp]
     bf16* hi = reinterpret_cast<bf16*>(part + kLTile * rp);  // [16][rp + 8]
     bf16* lo = hi + kLTile * (rp + 8);
     int* adp = reinterpret_cast<int*>(lo + kLTile * (rp + 8));  // [T] adapter, n: none
@@ -143,8 +146,9 @@ __global__ void __cluster_dims__(kLCluster, 1, 1) __launch_bounds__(kLThreads, R
     __syncthreads();
 
     const int gw = (int)cr * kLWarps + warp;  // warp of the cluster
+    const int kw = warp % kKW, r0 = warp / kKW * 32, gk = (int)cr * kKW + kw;
     const int k_blocks = P.in >> 5, o_blocks = P.out >> 5;
-    const int kb0 = gw * k_blocks / (kLCluster * kLWarps), kb1 = (gw + 1) * k_blocks / (kLCluster * kLWarps);
+    const int kb0 = gk * k_blocks / (kLCluster * kKW), kb1 = (gk + 1) * k_blocks / (kLCluster * kKW);
     const int ob0 = gw * o_blocks / (kLCluster * kLWarps), ob1 = (gw + 1) * o_blocks / (kLCluster * kLWarps);
     for (int u = cluster; u < n_units; u += clusters) {
         const int t0 = lead[u], a = adp[t0], k0 = key[t0], tile = rnk[t0] / kLTile;
@@ -207,7 +211,7 @@ __global__ void __cluster_dims__(kLCluster, 1, 1) __launch_bounds__(kLThreads, R
             xa[1] = g + 8 < m ? *reinterpret_cast<const uint4*>(P.x + (size_t)t_hi * P.ld_x + k) : z;
 #pragma unroll
             for (int j = 0; j < kNT; ++j)
-                w[j] = j * 8 + g < rank ? *reinterpret_cast<const uint4*>(A + (size_t)(j * 8 + g) * P.in + k) : z;
+                w[j] = r0 + j * 8 + g < rank ? *reinterpret_cast<const uint4*>(A + (size_t)(r0 + j * 8 + g) * P.in + k) : z;
         };
         if (kb0 < kb1) load_in(kb0);
 #pragma unroll 1
@@ -216,19 +220,17 @@ __global__ void __cluster_dims__(kLCluster, 1, 1) __launch_bounds__(kLThreads, R
             uint4 c[kNT];
 #pragma unroll
             for (int j = 0; j < kNT; ++j) c[j] = w[j];
-            // the next block is on its way during the products (where registers allow)
-            if (RP <= 32 && kb + 1 < kb1) load_in(kb + 1);
+            if (kb + 1 < kb1) load_in(kb + 1);
 #pragma unroll
             for (int j = 0; j < kNT; ++j) {
                 mma16816(acc[j], f0, c[j].x, c[j].y);
                 mma16816(acc[j], f1, c[j].z, c[j].w);
             }
-            if (RP > 32 && kb + 1 < kb1) load_in(kb + 1);
         }
 #pragma unroll
         for (int j = 0; j < kNT; ++j)
-            if (j * 8 < rp) {
-                float* r = red + (size_t)warp * kLTile * rp + j * 8 + 2 * cq;
+            if (r0 + j * 8 < rp) {
+                float* r = red + (size_t)kw * kLTile * rp + r0 + j * 8 + 2 * cq;
                 *reinterpret_cast<float2*>(r + g * rp) = make_float2(acc[j][0], acc[j][1]);
                 *reinterpret_cast<float2*>(r + (g + 8) * rp) = make_float2(acc[j][2], acc[j][3]);
             }
@@ -238,7 +240,7 @@ __global__ void __cluster_dims__(kLCluster, 1, 1) __launch_bounds__(kLThreads, R
         for (int i = tid; i < n4; i += kLThreads) {
             float4 s = reinterpret_cast<const float4*>(red)[i];
 #pragma unroll
-            for (int w = 1; w < kLWarps; ++w) add4(s, reinterpret_cast<const float4*>(red)[w * n4 + i]);
+            for (int w = 1; w < kKW; ++w) add4(s, reinterpret_cast<const float4*>(red)[w * n4 + i]);
             reinterpret_cast<float4*>(part)[i] = s;
         }
         cluster_arrive();
