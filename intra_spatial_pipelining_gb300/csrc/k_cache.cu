@@ -150,14 +150,21 @@ __global__ void __launch_bounds__(kWThreads, 2) weights_kernel(const WeightsProb
 }
 
 // ---------------------------------------------------------------------------------------
-// Eviction, first kernel: which positions stay.  One CTA per (sequence, KV head).  The keys of
-// the positions between the sinks and the recent ones (acc mapped to unsigned integers of the
-// same order) stay in registers: warp w holds a run of 32 KPT of them, lane by lane.  The
-// threshold, the need-th largest key, is found two bits a round from counts; the positions
-// above it stay, and of those equal to it the first ones.
+// Eviction: which positions stay, then the move of their rows.
+//
+// The keys of the positions between the sinks and the recent ones (acc mapped to unsigned integers
+// of the same order) stay in registers, position (i W + w) 32 + lane in register i of warp w.  The
+// threshold, the need-th largest key, is found two bits a round from counts, until exactly `need`
+// keys reach it; the positions above it stay, and of those equal to it the first ones.
+//
+// Into another cache one kernel does both: a few CTAs to a (sequence, KV head), each of which makes
+// the whole selection (they write the same list) and moves its part of the rows, so that nothing is
+// waited for and one CTA's selection runs beside another's copies.  In place the selection is a
+// kernel of its own, because the move overwrites what it reads.
 // ---------------------------------------------------------------------------------------
-constexpr int kEThreads = 1024;
+constexpr int kEThreads = 512;
 constexpr int kEWarps = kEThreads / 32;
+constexpr int kEUnroll = 4;
 
 __device__ __forceinline__ uint32_t order_key(float v) {
     if (v != v) return 0u;             // NaN: below -inf
@@ -167,108 +174,99 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 }
 
 template <int KPT>
-__global__ void __launch_bounds__(kEThreads, KPT <= 8 ? 2 : 1)
-    evict_select_kernel(const EvictProblem P, const KCtx ctx) {
-    __shared__ int cnt[2][3][kEWarps];
-    __shared__ int base[2][kEWarps];
-    griddep_launch();
-    griddep_wait();
-    task_begin(ctx);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int kvh = blockIdx.x, t = blockIdx.y, pair = t * P.nkv + kvh;
-    const int L = P.kv_len[t];
-    const bool bad = L < 0 || L > P.cap || min(L, P.budget) > P.cap_out;
-    if (bad && kvh == 0 && tid == 0) report(ctx, ST_BOUNDS, (uint32_t)L);
-    const int count = bad ? -1 : min(L, P.budget);
-    if (kvh == 0 && tid == 0) P.count[t] = count;
-    int* kept = P.kept + (size_t)pair * P.budget;
-    int* user = P.user_kept ? P.user_kept + (size_t)pair * P.budget : nullptr;
-    auto put = [&](int i, int p) {
-        kept[i] = p;
-        if (user) user[i] = p;
+struct SelectSmem {
+    int cnt[2][3][kEWarps];
+    int base[2][KPT * kEWarps];  // larger and equal keys before 32 positions
+};
+
+// Writes the positions that stay of `n` candidates from position `a` on to kept[a, a + need).
+template <int KPT>
+__device__ void select_kept(SelectSmem<KPT>& sm, const float* acc, int a, int n, int need, int* kept,
+                            int* user) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kRun = KPT * kEThreads;  // keys that fit the registers; longer caches take more runs
+    const int runs = (n + kRun - 1) / kRun;
+    uint32_t key[KPT];
+    int slots = 0;  // registers in use
+    auto load = [&](int run) {
+        const int left = n - run * kRun;
+        slots = min(KPT, (left + kEThreads - 1) / kEThreads);
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) {
+            const int p = i * kEThreads + threadIdx.x;
+            // past the end: below every threshold but 0, and never taken
+            key[i] = i < slots && p < left ? order_key(acc[a + run * kRun + p]) : 0u;
+        }
     };
-    if (user)
-        for (int i = max(0, count) + tid; i < P.budget; i += kEThreads) user[i] = -1;
-    if (!bad && L <= P.budget) {
-        for (int i = tid; i < L; i += kEThreads) put(i, i);
-    } else if (!bad) {
-        const float* acc = P.acc + (size_t)pair * P.cap;
-        const int a = P.n_sink, n = L - P.n_recent - a;       // candidates [a, a + n)
-        const int need = P.budget - P.n_recent - a;
-        for (int i = tid; i < a; i += kEThreads) put(i, i);
-        for (int i = tid; i < P.n_recent; i += kEThreads) put(a + need + i, L - P.n_recent + i);
-        // runs of 32 KPT kEWarps candidates; more than one only beyond the registers
-        constexpr int kRun = 32 * KPT * kEWarps;
-        const int runs = (n + kRun - 1) / kRun;
-        uint32_t key[KPT];
-        auto load = [&](int run) {
+    if (runs == 1) load(0);
+    uint32_t thr = 0;  // the largest value that at least `need` keys reach
+    int reach = n;     // keys that reach it
+    for (int bit = 30, ph = 0; bit >= 0 && reach != need; bit -= 2, ph ^= 1) {
+        int c[3] = {0, 0, 0};
+        for (int run = 0; run < runs; ++run) {
+            if (runs > 1) load(run);
 #pragma unroll
-            for (int i = 0; i < KPT; ++i) {
-                const int p = run * kRun + (warp * KPT + i) * 32 + lane;
-                // past the end: never counted (a key of 0 is only ever >= the threshold 0)
-                key[i] = p < n ? order_key(acc[a + p]) : 0u;
-            }
-        };
-        auto in = [&](int run, int i) { return run * kRun + (warp * KPT + i) * 32 + lane < n; };
-        uint32_t thr = 0;  // largest value with at least `need` keys >= it
-        if (need > 0) {  // need < n: L is past the budget
-            if (runs == 1) load(0);
-            for (int bit = 30, ph = 0; bit >= 0; bit -= 2, ph ^= 1) {
-                int c[3] = {0, 0, 0};
-                for (int run = 0; run < runs; ++run) {
-                    if (runs > 1) load(run);
+            for (int i = 0; i < KPT; ++i)
+                if (i < slots)
 #pragma unroll
-                    for (int i = 0; i < KPT; ++i)
+                    for (int b = 0; b < 3; ++b) c[b] += key[i] >= (thr | ((uint32_t)(b + 1) << bit));
+        }
 #pragma unroll
-                        for (int b = 0; b < 3; ++b) c[b] += key[i] >= (thr | ((uint32_t)(b + 1) << bit));
-                }
+        for (int b = 0; b < 3; ++b) {
+            const int s = __reduce_add_sync(0xffffffffu, c[b]);
+            if (lane == 0) sm.cnt[ph][b][warp] = s;
+        }
+        __syncthreads();
 #pragma unroll
-                for (int b = 0; b < 3; ++b) {
-                    const int s = __reduce_add_sync(0xffffffffu, c[b]);
-                    if (lane == 0) cnt[ph][b][warp] = s;
-                }
-                __syncthreads();
-#pragma unroll
-                for (int b = 2; b >= 0; --b) {
-                    const int s = __reduce_add_sync(0xffffffffu, cnt[ph][b][lane]);
-                    if (s >= need) {
-                        thr |= (uint32_t)(b + 1) << bit;
-                        break;
-                    }
-                }
+        for (int b = 2; b >= 0; --b) {
+            const int s = __reduce_add_sync(0xffffffffu, lane < kEWarps ? sm.cnt[ph][b][lane] : 0);
+            if (s >= need) {
+                thr |= (uint32_t)(b + 1) << bit;
+                reach = s;
+                break;
             }
         }
-        if (need > 0) {
-            // keys above the threshold, then how many equal ones are taken
-            int c = 0;
-            for (int run = 0; run < runs; ++run) {
-                if (runs > 1) load(run);
+    }
+    // keys above `top` all stay, and of those equal to it the first need - (their number)
+    const bool ties = reach != need;
+    const uint32_t top = ties ? thr : thr - 1;  // (thr > 0 when reach == need < n)
+    int above = need;
+    if (ties) {
+        int c = 0;
+        for (int run = 0; run < runs; ++run) {
+            if (runs > 1) load(run);
 #pragma unroll
-                for (int i = 0; i < KPT; ++i) c += key[i] > thr;
-            }
-            c = __reduce_add_sync(0xffffffffu, c);
-            __syncthreads();
-            if (lane == 0) cnt[0][0][warp] = c;
-            __syncthreads();
-            const int above = __reduce_add_sync(0xffffffffu, cnt[0][0][lane]);
-            const int ties = need - above;
-            int out0 = 0, eq0 = 0;  // taken / equal ones in earlier runs
-            for (int run = 0; run < runs; ++run) {
-                if (runs > 1) load(run);
-                int c_gt = 0, c_eq = 0;
+            for (int i = 0; i < KPT; ++i) c += i < slots && key[i] > top;
+        }
+        c = __reduce_add_sync(0xffffffffu, c);
+        __syncthreads();
+        if (lane == 0) sm.cnt[0][0][warp] = c;
+        __syncthreads();
+        above = __reduce_add_sync(0xffffffffu, lane < kEWarps ? sm.cnt[0][0][lane] : 0);
+    }
+    const int take_eq = need - above;
+    int out0 = 0, eq0 = 0;  // taken / equal ones in earlier runs
+    for (int run = 0; run < runs; ++run) {
+        if (runs > 1) load(run);
+        __syncthreads();
 #pragma unroll
-                for (int i = 0; i < KPT; ++i) {
-                    const bool x = in(run, i);
-                    c_gt += __popc(__ballot_sync(0xffffffffu, x && key[i] > thr));
-                    c_eq += __popc(__ballot_sync(0xffffffffu, x && key[i] == thr));
-                }
-                __syncthreads();
+        for (int i = 0; i < KPT; ++i)
+            if (i < slots) {
+                const int gt = __popc(__ballot_sync(0xffffffffu, key[i] > top));
+                const int eq = __popc(__ballot_sync(0xffffffffu, ties && key[i] == top && run * kRun + i * kEThreads + (int)threadIdx.x < n));
                 if (lane == 0) {
-                    base[0][warp] = c_gt;
-                    base[1][warp] = c_eq;
+                    sm.base[0][i * kEWarps + warp] = gt;
+                    sm.base[1][i * kEWarps + warp] = eq;
                 }
-                __syncthreads();
-                int gt = base[0][lane], eq = base[1][lane];
+            }
+        __syncthreads();
+        if (warp == 0) {  // exclusive sums, in the order of the positions
+            int gt0 = 0, e0 = 0;
+            for (int j0 = 0; j0 < slots * kEWarps; j0 += 32) {
+                const int j = j0 + lane;
+                const bool in = j < slots * kEWarps;
+                int gt = in ? sm.base[0][j] : 0, eq = in ? sm.base[1][j] : 0;
+                const int g = gt, e = eq;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const int vg = __shfl_up_sync(0xffffffffu, gt, o), ve = __shfl_up_sync(0xffffffffu, eq, o);
@@ -277,41 +275,119 @@ __global__ void __launch_bounds__(kEThreads, KPT <= 8 ? 2 : 1)
                         eq += ve;
                     }
                 }
-                const int run_gt = __shfl_sync(0xffffffffu, gt, 31), run_eq = __shfl_sync(0xffffffffu, eq, 31);
-                int my_gt = __shfl_sync(0xffffffffu, gt, warp) - c_gt;
-                int my_eq = eq0 + __shfl_sync(0xffffffffu, eq, warp) - c_eq;
-                // taken before this warp's run: every larger key, and the first `ties` equal ones
-                int out = out0 + my_gt + min(my_eq, ties) - min(eq0, ties);
-#pragma unroll
-                for (int i = 0; i < KPT; ++i) {
-                    const bool x = in(run, i);
-                    const bool is_eq = x && key[i] == thr;
-                    const uint32_t meq = __ballot_sync(0xffffffffu, is_eq);
-                    const uint32_t below = (1u << lane) - 1u;
-                    const bool take = x && (key[i] > thr || (is_eq && my_eq + __popc(meq & below) < ties));
-                    const uint32_t mt = __ballot_sync(0xffffffffu, take);
-                    if (take) put(a + out + __popc(mt & below), a + run * kRun + (warp * KPT + i) * 32 + lane);
-                    out += __popc(mt);
-                    my_eq += __popc(meq);
+                if (in) {
+                    sm.base[0][j] = gt0 + gt - g;
+                    sm.base[1][j] = e0 + eq - e;
                 }
-                out0 += run_gt + min(eq0 + run_eq, ties) - min(eq0, ties);
-                eq0 += run_eq;
+                gt0 += __shfl_sync(0xffffffffu, gt, 31);
+                e0 += __shfl_sync(0xffffffffu, eq, 31);
+            }
+            if (lane == 0) {
+                sm.cnt[0][0][0] = gt0;
+                sm.cnt[0][1][0] = e0;
             }
         }
+        __syncthreads();
+        const uint32_t below = (1u << lane) - 1u;
+#pragma unroll
+        for (int i = 0; i < KPT; ++i)
+            if (i < slots) {
+                const int p = run * kRun + i * kEThreads + (int)threadIdx.x;
+                const int eq_before = eq0 + sm.base[1][i * kEWarps + warp];
+                // taken before these 32: every larger key, and the first equal ones
+                const int out = out0 + sm.base[0][i * kEWarps + warp] + min(eq_before, take_eq) - min(eq0, take_eq);
+                const bool eq = ties && key[i] == top && p < n;
+                const uint32_t meq = __ballot_sync(0xffffffffu, eq);
+                const bool take = key[i] > top || (eq && eq_before + __popc(meq & below) < take_eq);
+                const uint32_t mt = __ballot_sync(0xffffffffu, take);
+                if (take) {
+                    const int at = a + out + __popc(mt & below);
+                    kept[at] = a + p;
+                    if (user) user[at] = a + p;
+                }
+            }
+        out0 += sm.cnt[0][0][0] + min(eq0 + sm.cnt[0][1][0], take_eq) - min(eq0, take_eq);
+        eq0 += sm.cnt[0][1][0];
+    }
+}
+
+template <int KPT, bool MOVE>
+__global__ void __launch_bounds__(kEThreads, KPT <= 16 ? 2 : 1)
+    evict_kernel(const EvictProblem P, const KCtx ctx) {
+    __shared__ SelectSmem<KPT> sm;
+    griddep_launch();
+    griddep_wait();
+    task_begin(ctx);
+    const int tid = threadIdx.x;
+    const int part = blockIdx.x, kvh = blockIdx.y, t = blockIdx.z, pair = t * P.nkv + kvh;
+    const int L = P.kv_len[t];
+    const bool bad = L < 0 || L > P.cap;
+    const int count = bad ? -1 : min(L, P.budget);
+    int* kept = P.kept + (size_t)pair * P.budget;
+    int* user = P.user_kept && part == 0 ? P.user_kept + (size_t)pair * P.budget : nullptr;
+    if (kvh == 0 && part == 0 && tid == 0) {
+        if (bad) report(ctx, ST_BOUNDS, (uint32_t)L);
+        // the other CTAs still read kv_len: where it is written too, a later kernel does that
+        if (!MOVE || P.kv_len_out == P.kv_len) P.count[t] = count;
+        else if (!bad) P.kv_len_out[t] = count;
+    }
+    if (user)
+        for (int i = max(0, count) + tid; i < P.budget; i += kEThreads) user[i] = -1;
+    const bool some = L > P.budget;
+    if (!bad) {
+        const int a = some ? P.n_sink : L, need = some ? P.budget - P.n_recent - a : 0;
+        auto put = [&](int i, int p) {
+            kept[i] = p;
+            if (user) user[i] = p;
+        };
+        for (int i = tid; i < a; i += kEThreads) put(i, i);
+        if (some) {
+            for (int i = tid; i < P.n_recent; i += kEThreads) put(a + need + i, L - P.n_recent + i);
+            // need < candidates: L is past the budget
+            if (need > 0)
+                select_kept<KPT>(sm, P.acc + (size_t)pair * P.cap, a, L - P.n_recent - a, need, kept, user);
+        }
+    }
+    __syncthreads();
+    if (MOVE && !bad) {
+        const int parts = gridDim.x, r0 = (int)((long long)part * count / parts), r1 = (int)((long long)(part + 1) * count / parts);
+        const size_t so = (size_t)pair * P.cap, to = (size_t)pair * P.cap_out;
+        const int c = tid & 7;  // 16-byte column of a row
+        constexpr int kRows = kEThreads / 8;
+        for (int w = 0; w < 2; ++w) {
+            const uint4* src = reinterpret_cast<const uint4*>(w ? P.v : P.k) + so * 8 + c;
+            uint4* dst = reinterpret_cast<uint4*>(w ? P.v_out : P.k_out) + to * 8 + c;
+            for (int r = r0 + (tid >> 3); r < r1; r += kRows * kEUnroll) {
+                uint4 v[kEUnroll];
+#pragma unroll
+                for (int u = 0; u < kEUnroll; ++u)
+                    if (r + u * kRows < r1) v[u] = __ldcs(src + (size_t)kept[r + u * kRows] * 8);
+#pragma unroll
+                for (int u = 0; u < kEUnroll; ++u)
+                    if (r + u * kRows < r1) __stcs(dst + (size_t)(r + u * kRows) * 8, v[u]);
+            }
+        }
+        for (int r = r0 + tid; r < r1; r += kEThreads) P.acc_out[to + r] = P.acc[so + kept[r]];
+        // a new position starts at 0
+        for (int r = count + part * kEThreads + tid; r < P.cap_out; r += parts * kEThreads) P.acc_out[to + r] = 0.f;
     }
     task_end(ctx);
 }
 
-// ---------------------------------------------------------------------------------------
-// Eviction, second kernel: the rows move.  Out of place a CTA copies a run of kept rows.  In
-// place (a row only ever moves down: kept[i] >= i) the CTAs of a pair share it by columns, 64
-// bytes of every row of K or V each, so that no CTA's stores can reach what another has still
-// to load; a CTA loads a run of rows, waits, and stores it, and run r's stores end below run
+__global__ void __launch_bounds__(kEThreads) evict_len_kernel(const EvictProblem P, const KCtx ctx) {
+    griddep_wait();
+    task_begin(ctx);
+    for (int t = threadIdx.x; t < P.T; t += kEThreads)
+        if (P.count[t] >= 0) P.kv_len_out[t] = P.count[t];
+    task_end(ctx);
+}
+
+// The move in place: a row only ever moves down (kept[i] >= i).  The CTAs of a pair share it by
+// columns, 64 bytes of every row of K or V each, so that no CTA's stores can reach what another has
+// still to load; a CTA loads a run of rows, waits, and stores it, and run r's stores end below run
 // r + 1's sources.  One more CTA moves acc and clears it behind the kept rows.
-// ---------------------------------------------------------------------------------------
 constexpr int kMThreads = 256;
 constexpr int kMUnroll = 8;
-constexpr int kMRows = 256;  // out of place: kept rows per CTA
 
 __global__ void __launch_bounds__(kMThreads) evict_move_kernel(const EvictProblem P, const KCtx ctx) {
     griddep_wait();
@@ -322,71 +398,48 @@ __global__ void __launch_bounds__(kMThreads) evict_move_kernel(const EvictProble
     const int* kept = P.kept + (size_t)pair * P.budget;
     if (n >= 0 && blockIdx.x == 0) {  // acc, and the new length
         if (kvh == 0 && tid == 0) P.kv_len_out[t] = n;
-        const float* src = P.acc + (size_t)pair * P.cap;
-        float* dst = P.acc_out + (size_t)pair * P.cap_out;
+        float* acc = P.acc_out + (size_t)pair * P.cap_out;
         for (int r0 = 0; r0 < n; r0 += kMThreads * kMUnroll) {
             float v[kMUnroll];
 #pragma unroll
             for (int u = 0; u < kMUnroll; ++u) {
                 const int r = r0 + u * kMThreads + tid;
-                v[u] = r < n ? src[kept[r]] : 0.f;
+                v[u] = r < n ? acc[kept[r]] : 0.f;
             }
             __syncthreads();
 #pragma unroll
             for (int u = 0; u < kMUnroll; ++u) {
                 const int r = r0 + u * kMThreads + tid;
-                if (r < n) dst[r] = v[u];
+                if (r < n) acc[r] = v[u];
             }
             __syncthreads();
         }
-        for (int r = n + tid; r < P.cap_out; r += kMThreads) dst[r] = 0.f;
+        for (int r = n + tid; r < P.cap_out; r += kMThreads) acc[r] = 0.f;
     } else if (n > 0) {
-        const size_t so = (size_t)pair * P.cap * 64, to = (size_t)pair * P.cap_out * 64;
-        if (!P.in_place) {
-            const int r0 = (blockIdx.x - 1) * kMRows, m = min(n - r0, kMRows);
-            const int c = tid & 7;  // 16-byte column of a row
-            for (int w = 0; w < 2; ++w) {
-                const uint4* src = reinterpret_cast<const uint4*>((w ? P.v : P.k) + so) + c;
-                uint4* dst = reinterpret_cast<uint4*>((w ? P.v_out : P.k_out) + to) + c;
-                uint4 v[kMUnroll];
-                static_assert(kMRows == kMThreads / 8 * kMUnroll, "one pass");
+        const int s = blockIdx.x - 1, c = (s & 1) * 4 + (tid & 3);
+        uint4* x = reinterpret_cast<uint4*>((s >= 2 ? P.v_out : P.k_out)) + (size_t)pair * P.cap_out * 8 + c;
+        // rows that stay where they are: kept[r] == r up to the first that moves
+        int lo = 0, hi = n;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (kept[mid] == mid) lo = mid + 1;
+            else hi = mid;
+        }
+        constexpr int kRun = kMThreads / 4 * kMUnroll;
+        for (int r0 = lo; r0 < n; r0 += kRun) {
+            uint4 v[kMUnroll];
 #pragma unroll
-                for (int u = 0; u < kMUnroll; ++u) {
-                    const int r = u * (kMThreads / 8) + (tid >> 3);
-                    if (r < m) v[u] = src[(size_t)kept[r0 + r] * 8];
-                }
-#pragma unroll
-                for (int u = 0; u < kMUnroll; ++u) {
-                    const int r = u * (kMThreads / 8) + (tid >> 3);
-                    if (r < m) dst[(size_t)(r0 + r) * 8] = v[u];
-                }
+            for (int u = 0; u < kMUnroll; ++u) {
+                const int r = r0 + u * (kMThreads / 4) + (tid >> 2);
+                if (r < n) v[u] = x[(size_t)kept[r] * 8];
             }
-        } else {
-            const int s = blockIdx.x - 1, c = (s & 1) * 4 + (tid & 3);
-            uint4* x = reinterpret_cast<uint4*>((s >= 2 ? P.v_out : P.k_out) + to) + c;
-            // rows that stay where they are: kept[r] == r up to the first that moves
-            int lo = 0, hi = n;
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                if (kept[mid] == mid) lo = mid + 1;
-                else hi = mid;
-            }
-            constexpr int kRun = kMThreads / 4 * kMUnroll;
-            for (int r0 = lo; r0 < n; r0 += kRun) {
-                uint4 v[kMUnroll];
+            __syncthreads();
 #pragma unroll
-                for (int u = 0; u < kMUnroll; ++u) {
-                    const int r = r0 + u * (kMThreads / 4) + (tid >> 2);
-                    if (r < n) v[u] = x[(size_t)kept[r] * 8];
-                }
-                __syncthreads();
-#pragma unroll
-                for (int u = 0; u < kMUnroll; ++u) {
-                    const int r = r0 + u * (kMThreads / 4) + (tid >> 2);
-                    if (r < n) x[(size_t)r * 8] = v[u];
-                }
-                __syncthreads();
+            for (int u = 0; u < kMUnroll; ++u) {
+                const int r = r0 + u * (kMThreads / 4) + (tid >> 2);
+                if (r < n) x[(size_t)r * 8] = v[u];
             }
+            __syncthreads();
         }
     }
     task_end(ctx);
@@ -402,14 +455,21 @@ int enqueue_weights(Launcher& L, const WeightsProblem& p, const KCtx& c, int sms
 
 int enqueue_evict(Launcher& L, const EvictProblem& p, const KCtx& c) {
     void* args[] = {(void*)&p, (void*)&c};
-    const void* f = p.cap <= 8 * kEThreads ? (const void*)evict_select_kernel<8>
-                                           : (const void*)evict_select_kernel<32>;
-    const int e = L.launch(f, dim3(p.nkv, p.T), dim3(kEThreads), 0, args);
+    // keys in registers: 16 to a thread up to 8192 positions (two CTAs to an SM), else 64
+    const bool small = p.cap <= 16 * kEThreads;
+    if (!p.in_place) {
+        // as many CTAs to a pair as give every SM two, at most 16, none with fewer than 64 rows
+        const int pairs = p.T * p.nkv, rows = std::min(p.budget, p.cap);
+        const int parts = std::max(1, std::min({16, 304 / pairs, rows / 64}));
+        const int e = L.launch(small ? (const void*)evict_kernel<16, true> : (const void*)evict_kernel<64, true>,
+                               dim3(parts, p.nkv, p.T), dim3(kEThreads), 0, args);
+        if (e || p.kv_len != p.kv_len_out) return e;
+        return L.launch((const void*)evict_len_kernel, dim3(1), dim3(kEThreads), 0, args, true);
+    }
+    const int e = L.launch(small ? (const void*)evict_kernel<16, false> : (const void*)evict_kernel<64, false>,
+                           dim3(1, p.nkv, p.T), dim3(kEThreads), 0, args);
     if (e) return e;
-    const int rows = std::min(p.budget, p.cap);
-    const int parts = p.in_place ? 4 : (rows + kMRows - 1) / kMRows;
-    return L.launch((const void*)evict_move_kernel, dim3(1 + parts, p.nkv, p.T), dim3(kMThreads), 0, args,
-                    true);
+    return L.launch((const void*)evict_move_kernel, dim3(5, p.nkv, p.T), dim3(kMThreads), 0, args, true);
 }
 
 }  // namespace sgp

@@ -392,7 +392,7 @@ def test_kv_evict(T, nkv, lens, cap, cap_out, budget, sink, recent, kind, in_pla
                     device="cuda")
     ws[:64] = 0
     n_in = ints(lens)
-    n_out = n_in if in_place else torch.full_like(n_in, -1)
+    n_out = n_in if in_place or T == 4 else torch.full_like(n_in, -1)   # the lengths in place, or not
     kept = torch.full((T, nkv, budget), -9, dtype=torch.int32, device="cuda") if T != 3 else None
     sgp.sgp_kv_evict(dims, sgp.make_cache(k, v), sgp.make_cache(ko, vo), sgp.make_evict(budget, sink, recent),
                      n_in, n_out, acc, ao, kept, T, ws)
