@@ -152,19 +152,26 @@ __global__ void __launch_bounds__(kWThreads, 2) weights_kernel(const WeightsProb
 // ---------------------------------------------------------------------------------------
 // Eviction: which positions stay, then the move of their rows.
 //
-// The keys of the positions between the sinks and the recent ones (acc mapped to unsigned integers
-// of the same order) stay in registers, position (i W + w) 32 + lane in register i of warp w.  The
+// The keys of the positions between the sinks and the recent ones are acc mapped to unsigned
+// integers of the same order, kept in shared memory (those that do not fit are read again).  The
 // threshold, the need-th largest key, is found two bits a round from counts, until exactly `need`
-// keys reach it; the positions above it stay, and of those equal to it the first ones.
+// keys reach it; the positions above it stay, and of those equal to it the first ones.  Loops, not
+// registers: unrolled over registers, the code of a short selection was met cold, 5 us of it.
 //
 // Into another cache one kernel does both: a few CTAs to a (sequence, KV head), each of which makes
-// the whole selection (they write the same list) and moves its part of the rows, so that nothing is
-// waited for and one CTA's selection runs beside another's copies.  In place the selection is a
-// kernel of its own, because the move overwrites what it reads.
+// the whole selection and moves its part of the rows, so that nothing is waited for and one CTA's
+// selection runs beside another's copies.  In place the selection is a kernel of its own, because
+// the move overwrites what it reads.
+//
+// Bound by the move: 64 sequences x 8 KV heads, 8192 -> 4096 positions, take 140 us for 815 MB
+// (5.8 TB/s), and 139 us with the rows 0, 2, 4 ... and no selection at all: every second 128-byte
+// row of the source does not read at a plain copy's rate.  Four CTAs of 256 threads to an SM took
+// 221 us, one of 1024 146 us.  Two caches of 640 -> 512 take 10 us, latency: eight rounds of counts
+// with a barrier each, then loads of the rows.
 // ---------------------------------------------------------------------------------------
 constexpr int kEThreads = 512;
 constexpr int kEWarps = kEThreads / 32;
-constexpr int kEUnroll = 4;
+constexpr int kEUnroll = 8;
 
 __device__ __forceinline__ uint32_t order_key(float v) {
     if (v != v) return 0u;             // NaN: below -inf
@@ -173,148 +180,135 @@ __device__ __forceinline__ uint32_t order_key(float v) {
     return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
-template <int KPT>
+constexpr int kESeg = 32;  // blocks of kEThreads positions that are placed at a time
+
 struct SelectSmem {
     int cnt[2][3][kEWarps];
-    int base[2][KPT * kEWarps];  // larger and equal keys before 32 positions
+    int base[2][kESeg * kEWarps];  // larger and equal keys before 32 positions
+    int total[2];
 };
 
-// Writes the positions that stay of `n` candidates from position `a` on to kept[a, a + need).
-template <int KPT>
-__device__ void select_kept(SelectSmem<KPT>& sm, const float* acc, int a, int n, int need, int* kept,
-                            int* user) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kRun = KPT * kEThreads;  // keys that fit the registers; longer caches take more runs
-    const int runs = (n + kRun - 1) / kRun;
-    uint32_t key[KPT];
-    int slots = 0;  // registers in use
-    auto load = [&](int run) {
-        const int left = n - run * kRun;
-        slots = min(KPT, (left + kEThreads - 1) / kEThreads);
-#pragma unroll
-        for (int i = 0; i < KPT; ++i) {
-            const int p = i * kEThreads + threadIdx.x;
-            // past the end: below every threshold but 0, and never taken
-            key[i] = i < slots && p < left ? order_key(acc[a + run * kRun + p]) : 0u;
-        }
-    };
-    if (runs == 1) load(0);
+// Calls put(i, p) for the positions p that stay of `n` candidates from position `a` on, i = a ... in
+// their order.  key: shared memory for n_key of the candidates' keys.
+template <typename Put>
+__device__ void select_kept(SelectSmem& sm, uint32_t* key, int n_key, const float* acc, int a, int n, int need,
+                            Put put) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int ns = min(n, n_key), n4 = (ns + 3) >> 2;
+    // (the last four are filled up with keys that no threshold of a count is below)
+#pragma unroll 4
+    for (int p = tid; p < 4 * n4; p += kEThreads) key[p] = p < ns ? order_key(acc[a + p]) : 0u;
+    __syncthreads();
+    auto key_at = [&](int p) { return p < ns ? key[p] : order_key(acc[a + p]); };
     uint32_t thr = 0;  // the largest value that at least `need` keys reach
     int reach = n;     // keys that reach it
+#pragma unroll 1
     for (int bit = 30, ph = 0; bit >= 0 && reach != need; bit -= 2, ph ^= 1) {
-        int c[3] = {0, 0, 0};
-        for (int run = 0; run < runs; ++run) {
-            if (runs > 1) load(run);
-#pragma unroll
-            for (int i = 0; i < KPT; ++i)
-                if (i < slots)
-#pragma unroll
-                    for (int b = 0; b < 3; ++b) c[b] += key[i] >= (thr | ((uint32_t)(b + 1) << bit));
+        const uint32_t t1 = thr | 1u << bit, t2 = thr | 2u << bit, t3 = thr | 3u << bit;
+        int c1 = 0, c2 = 0, c3 = 0;
+        auto add = [&](uint32_t k) {
+            c1 += k >= t1;
+            c2 += k >= t2;
+            c3 += k >= t3;
+        };
+#pragma unroll 2
+        for (int p = tid; p < n4; p += kEThreads) {
+            const uint4 k = reinterpret_cast<const uint4*>(key)[p];
+            add(k.x);
+            add(k.y);
+            add(k.z);
+            add(k.w);
         }
-#pragma unroll
-        for (int b = 0; b < 3; ++b) {
-            const int s = __reduce_add_sync(0xffffffffu, c[b]);
-            if (lane == 0) sm.cnt[ph][b][warp] = s;
+#pragma unroll 1
+        for (int p = ns + tid; p < n; p += kEThreads) add(order_key(acc[a + p]));
+        c1 = __reduce_add_sync(0xffffffffu, c1);
+        c2 = __reduce_add_sync(0xffffffffu, c2);
+        c3 = __reduce_add_sync(0xffffffffu, c3);
+        if (lane == 0) {
+            sm.cnt[ph][0][warp] = c1;
+            sm.cnt[ph][1][warp] = c2;
+            sm.cnt[ph][2][warp] = c3;
         }
         __syncthreads();
-#pragma unroll
-        for (int b = 2; b >= 0; --b) {
-            const int s = __reduce_add_sync(0xffffffffu, lane < kEWarps ? sm.cnt[ph][b][lane] : 0);
-            if (s >= need) {
-                thr |= (uint32_t)(b + 1) << bit;
-                reach = s;
-                break;
-            }
-        }
+        c1 = __reduce_add_sync(0xffffffffu, lane < kEWarps ? sm.cnt[ph][0][lane] : 0);
+        c2 = __reduce_add_sync(0xffffffffu, lane < kEWarps ? sm.cnt[ph][1][lane] : 0);
+        c3 = __reduce_add_sync(0xffffffffu, lane < kEWarps ? sm.cnt[ph][2][lane] : 0);
+        if (c3 >= need) thr = t3, reach = c3;
+        else if (c2 >= need) thr = t2, reach = c2;
+        else if (c1 >= need) thr = t1, reach = c1;
     }
     // keys above `top` all stay, and of those equal to it the first need - (their number)
     const bool ties = reach != need;
     const uint32_t top = ties ? thr : thr - 1;  // (thr > 0 when reach == need < n)
-    int above = need;
+    int take_eq = 0;
     if (ties) {
         int c = 0;
-        for (int run = 0; run < runs; ++run) {
-            if (runs > 1) load(run);
-#pragma unroll
-            for (int i = 0; i < KPT; ++i) c += i < slots && key[i] > top;
-        }
+        for (int p = tid; p < n; p += kEThreads) c += key_at(p) > top;
         c = __reduce_add_sync(0xffffffffu, c);
         __syncthreads();
         if (lane == 0) sm.cnt[0][0][warp] = c;
         __syncthreads();
-        above = __reduce_add_sync(0xffffffffu, lane < kEWarps ? sm.cnt[0][0][lane] : 0);
+        take_eq = need - __reduce_add_sync(0xffffffffu, lane < kEWarps ? sm.cnt[0][0][lane] : 0);
     }
-    const int take_eq = need - above;
-    int out0 = 0, eq0 = 0;  // taken / equal ones in earlier runs
-    for (int run = 0; run < runs; ++run) {
-        if (runs > 1) load(run);
+    int out0 = 0, eq0 = 0;  // taken / equal ones in earlier segments
+#pragma unroll 1
+    for (int p0 = 0; p0 < n; p0 += kESeg * kEThreads) {
+        const int blocks = min(kESeg, (n - p0 + kEThreads - 1) / kEThreads);
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < KPT; ++i)
-            if (i < slots) {
-                const int gt = __popc(__ballot_sync(0xffffffffu, key[i] > top));
-                const int eq = __popc(__ballot_sync(0xffffffffu, ties && key[i] == top && run * kRun + i * kEThreads + (int)threadIdx.x < n));
-                if (lane == 0) {
-                    sm.base[0][i * kEWarps + warp] = gt;
-                    sm.base[1][i * kEWarps + warp] = eq;
-                }
-            }
-        __syncthreads();
-        if (warp == 0) {  // exclusive sums, in the order of the positions
-            int gt0 = 0, e0 = 0;
-            for (int j0 = 0; j0 < slots * kEWarps; j0 += 32) {
-                const int j = j0 + lane;
-                const bool in = j < slots * kEWarps;
-                int gt = in ? sm.base[0][j] : 0, eq = in ? sm.base[1][j] : 0;
-                const int g = gt, e = eq;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int vg = __shfl_up_sync(0xffffffffu, gt, o), ve = __shfl_up_sync(0xffffffffu, eq, o);
-                    if (lane >= o) {
-                        gt += vg;
-                        eq += ve;
-                    }
-                }
-                if (in) {
-                    sm.base[0][j] = gt0 + gt - g;
-                    sm.base[1][j] = e0 + eq - e;
-                }
-                gt0 += __shfl_sync(0xffffffffu, gt, 31);
-                e0 += __shfl_sync(0xffffffffu, eq, 31);
-            }
+#pragma unroll 1
+        for (int i = 0; i < blocks; ++i) {
+            const int p = p0 + i * kEThreads + tid;
+            const uint32_t k = p < n ? key_at(p) : 0u;
+            const int gt = __popc(__ballot_sync(0xffffffffu, k > top));
+            const int eq = __popc(__ballot_sync(0xffffffffu, ties && k == top && p < n));
             if (lane == 0) {
-                sm.cnt[0][0][0] = gt0;
-                sm.cnt[0][1][0] = e0;
+                sm.base[0][i * kEWarps + warp] = gt;
+                sm.base[1][i * kEWarps + warp] = eq;
             }
         }
         __syncthreads();
-        const uint32_t below = (1u << lane) - 1u;
+        if (warp < 2) {  // exclusive sums, in the order of the positions: one warp to each
+            int run = 0;
+#pragma unroll 1
+            for (int j0 = 0; j0 < blocks * kEWarps; j0 += 32) {
+                const int j = j0 + lane, v = j < blocks * kEWarps ? sm.base[warp][j] : 0;
+                int incl = v;
 #pragma unroll
-        for (int i = 0; i < KPT; ++i)
-            if (i < slots) {
-                const int p = run * kRun + i * kEThreads + (int)threadIdx.x;
-                const int eq_before = eq0 + sm.base[1][i * kEWarps + warp];
-                // taken before these 32: every larger key, and the first equal ones
-                const int out = out0 + sm.base[0][i * kEWarps + warp] + min(eq_before, take_eq) - min(eq0, take_eq);
-                const bool eq = ties && key[i] == top && p < n;
-                const uint32_t meq = __ballot_sync(0xffffffffu, eq);
-                const bool take = key[i] > top || (eq && eq_before + __popc(meq & below) < take_eq);
-                const uint32_t mt = __ballot_sync(0xffffffffu, take);
-                if (take) {
-                    const int at = a + out + __popc(mt & below);
-                    kept[at] = a + p;
-                    if (user) user[at] = a + p;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int x = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += x;
                 }
+                if (j < blocks * kEWarps) sm.base[warp][j] = run + incl - v;
+                run += __shfl_sync(0xffffffffu, incl, 31);
             }
-        out0 += sm.cnt[0][0][0] + min(eq0 + sm.cnt[0][1][0], take_eq) - min(eq0, take_eq);
-        eq0 += sm.cnt[0][1][0];
+            if (lane == 0) sm.total[warp] = run;
+        }
+        __syncthreads();
+        const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 1
+        for (int i = 0; i < blocks; ++i) {
+            const int p = p0 + i * kEThreads + tid;
+            const uint32_t k = p < n ? key_at(p) : 0u;
+            const int eq_before = eq0 + sm.base[1][i * kEWarps + warp];
+            // taken before these 32: every larger key, and the first equal ones
+            const int out = out0 + sm.base[0][i * kEWarps + warp] + min(eq_before, take_eq) - min(eq0, take_eq);
+            const bool eq = ties && k == top && p < n;
+            const uint32_t meq = __ballot_sync(0xffffffffu, eq);
+            const bool take = k > top || (eq && eq_before + __popc(meq & below) < take_eq);
+            const uint32_t mt = __ballot_sync(0xffffffffu, take);
+            if (take) put(a + out + __popc(mt & below), a + p);
+        }
+        out0 += sm.total[0] + min(eq0 + sm.total[1], take_eq) - min(eq0, take_eq);
+        eq0 += sm.total[1];
     }
 }
 
-template <int KPT, bool MOVE>
-__global__ void __launch_bounds__(kEThreads, KPT <= 16 ? 2 : 1)
-    evict_kernel(const EvictProblem P, const KCtx ctx) {
-    __shared__ SelectSmem<KPT> sm;
+// n_key, n_list: keys and kept positions that shared memory holds; with n_list = 0 the list is in P.kept.
+template <bool MOVE>
+__global__ void __launch_bounds__(kEThreads, 2)
+    evict_kernel(const EvictProblem P, const int n_key, const int n_list, const KCtx ctx) {
+    extern __shared__ uint32_t dyn[];  // [n_key] keys, [n_list] kept positions, SelectSmem
+    SelectSmem& sm = *reinterpret_cast<SelectSmem*>(dyn + n_key + (MOVE ? n_list : 0));
     griddep_launch();
     griddep_wait();
     task_begin(ctx);
@@ -323,7 +317,8 @@ __global__ void __launch_bounds__(kEThreads, KPT <= 16 ? 2 : 1)
     const int L = P.kv_len[t];
     const bool bad = L < 0 || L > P.cap;
     const int count = bad ? -1 : min(L, P.budget);
-    int* kept = P.kept + (size_t)pair * P.budget;
+    // (the pair's CTAs write the same)
+    int* kept = MOVE && n_list ? reinterpret_cast<int*>(dyn) + n_key : P.kept + (size_t)pair * P.budget;
     int* user = P.user_kept && part == 0 ? P.user_kept + (size_t)pair * P.budget : nullptr;
     if (kvh == 0 && part == 0 && tid == 0) {
         if (bad) report(ctx, ST_BOUNDS, (uint32_t)L);
@@ -333,30 +328,34 @@ __global__ void __launch_bounds__(kEThreads, KPT <= 16 ? 2 : 1)
     }
     if (user)
         for (int i = max(0, count) + tid; i < P.budget; i += kEThreads) user[i] = -1;
-    const bool some = L > P.budget;
+    auto put = [&](int i, int p) {
+        kept[i] = p;
+        if (user) user[i] = p;
+    };
     if (!bad) {
+        const bool some = L > P.budget;
         const int a = some ? P.n_sink : L, need = some ? P.budget - P.n_recent - a : 0;
-        auto put = [&](int i, int p) {
-            kept[i] = p;
-            if (user) user[i] = p;
-        };
         for (int i = tid; i < a; i += kEThreads) put(i, i);
-        if (some) {
+        if (some)
             for (int i = tid; i < P.n_recent; i += kEThreads) put(a + need + i, L - P.n_recent + i);
-            // need < candidates: L is past the budget
-            if (need > 0)
-                select_kept<KPT>(sm, P.acc + (size_t)pair * P.cap, a, L - P.n_recent - a, need, kept, user);
-        }
+        // need < candidates: L is past the budget
+        if (need > 0)
+            select_kept(sm, dyn, n_key, P.acc + (size_t)pair * P.cap, a, L - P.n_recent - a, need, put);
     }
     __syncthreads();
     if (MOVE && !bad) {
-        const int parts = gridDim.x, r0 = (int)((long long)part * count / parts), r1 = (int)((long long)(part + 1) * count / parts);
+        const int parts = gridDim.x;
+        const int r0 = (int)((long long)part * count / parts), r1 = (int)((long long)(part + 1) * count / parts);
         const size_t so = (size_t)pair * P.cap, to = (size_t)pair * P.cap_out;
+        // acc first: its few loads are under way while the rows' begin
+        for (int r = r0 + tid; r < r1; r += kEThreads) P.acc_out[to + r] = P.acc[so + kept[r]];
         const int c = tid & 7;  // 16-byte column of a row
         constexpr int kRows = kEThreads / 8;
+#pragma unroll 1
         for (int w = 0; w < 2; ++w) {
             const uint4* src = reinterpret_cast<const uint4*>(w ? P.v : P.k) + so * 8 + c;
             uint4* dst = reinterpret_cast<uint4*>(w ? P.v_out : P.k_out) + to * 8 + c;
+#pragma unroll 1
             for (int r = r0 + (tid >> 3); r < r1; r += kRows * kEUnroll) {
                 uint4 v[kEUnroll];
 #pragma unroll
@@ -367,7 +366,6 @@ __global__ void __launch_bounds__(kEThreads, KPT <= 16 ? 2 : 1)
                     if (r + u * kRows < r1) __stcs(dst + (size_t)(r + u * kRows) * 8, v[u]);
             }
         }
-        for (int r = r0 + tid; r < r1; r += kEThreads) P.acc_out[to + r] = P.acc[so + kept[r]];
         // a new position starts at 0
         for (int r = count + part * kEThreads + tid; r < P.cap_out; r += parts * kEThreads) P.acc_out[to + r] = 0.f;
     }
@@ -454,22 +452,25 @@ int enqueue_weights(Launcher& L, const WeightsProblem& p, const KCtx& c, int sms
 }
 
 int enqueue_evict(Launcher& L, const EvictProblem& p, const KCtx& c) {
-    void* args[] = {(void*)&p, (void*)&c};
-    // keys in registers: 16 to a thread up to 8192 positions (two CTAs to an SM), else 64
-    const bool small = p.cap <= 16 * kEThreads;
+    // Shared memory for every key up to 8192 positions (two CTAs to an SM then), else for 24,576,
+    // and for the list where it is no longer than that.
+    const int n_key = p.cap <= 8192 ? (p.cap + 255) & ~255 : 24576;
+    const int n_list = p.budget <= n_key ? (p.budget + 255) & ~255 : 0;
+    void* args[] = {(void*)&p, (void*)&n_key, (void*)&n_list, (void*)&c};
+    void* args2[] = {(void*)&p, (void*)&c};
     if (!p.in_place) {
         // as many CTAs to a pair as give every SM two, at most 16, none with fewer than 64 rows
         const int pairs = p.T * p.nkv, rows = std::min(p.budget, p.cap);
         const int parts = std::max(1, std::min({16, 304 / pairs, rows / 64}));
-        const int e = L.launch(small ? (const void*)evict_kernel<16, true> : (const void*)evict_kernel<64, true>,
-                               dim3(parts, p.nkv, p.T), dim3(kEThreads), 0, args);
+        const int e = L.launch((const void*)evict_kernel<true>, dim3(parts, p.nkv, p.T), dim3(kEThreads),
+                               (size_t)(n_key + n_list) * 4 + sizeof(SelectSmem), args);
         if (e || p.kv_len != p.kv_len_out) return e;
-        return L.launch((const void*)evict_len_kernel, dim3(1), dim3(kEThreads), 0, args, true);
+        return L.launch((const void*)evict_len_kernel, dim3(1), dim3(kEThreads), 0, args2, true);
     }
-    const int e = L.launch(small ? (const void*)evict_kernel<16, false> : (const void*)evict_kernel<64, false>,
-                           dim3(1, p.nkv, p.T), dim3(kEThreads), 0, args);
+    const int e = L.launch((const void*)evict_kernel<false>, dim3(1, p.nkv, p.T), dim3(kEThreads),
+                           (size_t)n_key * 4 + sizeof(SelectSmem), args);
     if (e) return e;
-    return L.launch((const void*)evict_move_kernel, dim3(5, p.nkv, p.T), dim3(kMThreads), 0, args, true);
+    return L.launch((const void*)evict_move_kernel, dim3(5, p.nkv, p.T), dim3(kMThreads), 0, args2, true);
 }
 
 }  // namespace sgp

@@ -87,7 +87,7 @@ struct PrefixLayout {
 // chunks of 1024 left the stream at half its rate.
 int own_chunk_log2(size_t pairs, int kv_cap) {
     int b = 10;
-    while (b > 7 && pairs * (size_t)(((kv_cap - 1) >> b) + 1) < 3072) --b;
+    while (b > 7 && pairs * (size_t)(((kv_cap - 1) >> b) + 1) < 3000) --b;
     return b;
 }
 
