@@ -297,8 +297,10 @@ size_t sgp_prefix_attention_workspace_bytes(const sgp_dims* dims, int n_tokens, 
  *   q, o    device bf16 [n_tokens][n_q d]; o may equal q
  *   lse     device fp32 [n_tokens][n_q] or NULL: log of the sum of exp(q.k / sqrt(d)) (natural)
  * A sequence that sees no position gets o = 0 and lse = -inf.  A prefix index past n_prefixes
- * counts as none, a prefix length out of range as 0.  What caches hold behind their lengths is
- * not looked at (it may be NaN).
+ * counts as none, a prefix length out of range as 0.  What caches hold behind their lengths, or
+ * before every window, is not looked at (it may be NaN).  An infinity or NaN in v at a prefix
+ * position that the window of one sequence still holds may also reach the other sequences of that
+ * prefix, whose windows begin behind it (one matrix product serves them, with weights of 0).
  * Returns SGP_OK, SGP_ERR_INVALID_ARG, SGP_ERR_UNSUPPORTED or SGP_ERR_CUDA. */
 int sgp_prefix_attention(const sgp_dims* dims, const sgp_layer* cache, const sgp_prefix* prefix,
                          const int32_t* kv_len, const void* q, void* o, float* lse, int n_tokens,
@@ -339,7 +341,8 @@ size_t sgp_kv_evict_workspace_bytes(const sgp_dims* dims, int n_tokens, int budg
  *   from, to   caches of n_tokens sequences; `to` may be the same cache (k, v, acc and kv_cap all
  *              the same: in place) or share no byte with `from`; its kv_cap >= budget
  *   kv_len     device int32 [n_tokens], 0 <= kv_len[b] <= from->kv_cap (out of range: the
- *              sequence is left as it is); kv_len_out device int32 [n_tokens], may equal kv_len
+ *              sequence is left as it is); kv_len_out device int32 [n_tokens]: kv_len itself, or
+ *              apart from it
  *   acc        device fp32 [n_tokens][n_kv][from->kv_cap]; acc_out [n_tokens][n_kv][to->kv_cap]
  *   kept       device int32 [n_tokens][n_kv][budget] or NULL: the kept positions in order, -1
  *              behind them
@@ -356,7 +359,8 @@ int sgp_kv_evict(const sgp_dims* dims, const sgp_layer* from, const sgp_layer* t
  *   scale  fp32 [n_adapters] or NULL (1)
  *   rank   int32 [n_adapters] or NULL (max_rank), 0 <= rank <= max_rank: only the first rank rows
  *          of a and columns of b are the adapter's (the rest is not looked at)
- * n_adapters <= 4096; in and out multiples of 32; max_rank a multiple of 8, 8 to 128. */
+ * n_adapters <= 4096; in and out multiples of 32; max_rank a multiple of 8, 8 to 128.  The
+ * adapters' values are finite; x and y may hold anything. */
 typedef struct sgp_lora {
     const void* a;
     const void* b;

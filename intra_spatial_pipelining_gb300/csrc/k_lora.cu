@@ -251,18 +251,21 @@ __global__ void __cluster_dims__(kLCluster, 1, 1) __launch_bounds__(kLThreads, R
             for (int c = 0; c < kLCluster; ++c) v[c] = dsmem_ld(smem_u32(part + 4 * i), c);
 #pragma unroll
             for (int c = 1; c < kLCluster; ++c) add4(v[0], v[c]);
-            const float s[4] = {v[0].x * scale, v[0].y * scale, v[0].z * scale, v[0].w * scale};
+            const int row = 4 * i / rp, col = 4 * i - row * rp, at = row * (rp + 8) + col;
+            float s[4] = {v[0].x * scale, v[0].y * scale, v[0].z * scale, v[0].w * scale};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (col + e >= rank) s[e] = 0.f;  // not the adapter's; an infinite x times 0 there is NaN
             float r[4];
             uint2 h, l;
             h.x = pack_bf16x2(s[0], s[1]);
             h.y = pack_bf16x2(s[2], s[3]);
-            r[0] = s[0] - __uint_as_float(h.x << 16);
-            r[1] = s[1] - __uint_as_float(h.x & 0xffff0000u);
-            r[2] = s[2] - __uint_as_float(h.y << 16);
-            r[3] = s[3] - __uint_as_float(h.y & 0xffff0000u);
+            const float b[4] = {__uint_as_float(h.x << 16), __uint_as_float(h.x & 0xffff0000u),
+                                __uint_as_float(h.y << 16), __uint_as_float(h.y & 0xffff0000u)};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) r[e] = fabsf(b[e]) == INFINITY ? 0.f : s[e] - b[e];  // inf stays inf
             l.x = pack_bf16x2(r[0], r[1]);
             l.y = pack_bf16x2(r[2], r[3]);
-            const int row = 4 * i / rp, at = row * (rp + 8) + 4 * i - row * rp;
             *reinterpret_cast<uint2*>(hi + at) = h;
             *reinterpret_cast<uint2*>(lo + at) = l;
         }

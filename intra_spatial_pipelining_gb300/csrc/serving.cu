@@ -213,6 +213,8 @@ int kv_evict(const sgp_dims* d, const sgp_layer* from, const sgp_layer* to, cons
         return host_fail_arg("n_sink + n_recent must be in [0, budget]");
     if (bad4(kv_len) || bad4(kv_len_out) || bad4(acc) || bad4(acc_out) || (kept && bad4(kept)))
         return host_fail_arg("kv_len, acc or kept NULL or not aligned");
+    if (kv_len != kv_len_out && overlap(kv_len, (size_t)T * 4, kv_len_out, (size_t)T * 4))
+        return host_fail_arg("kv_len and kv_len_out overlap without being the same");
     const size_t pairs = (size_t)T * d->n_kv_heads;
     const size_t n_from = pairs * from->kv_cap, n_to = pairs * to->kv_cap;
     const bool in_place = from->k_cache == to->k_cache;

@@ -501,6 +501,25 @@ def test_lora_apply_reports_bad_indices_and_ranks():
     within("y", out, want, err)
 
 
+def test_lora_apply_infinities():
+    """An infinite A x stays infinite, with the sign that B gives it."""
+    x = torch.zeros(2, 64, dtype=torch.bfloat16, device="cuda")
+    x[0, 5], x[1, 5] = float("inf"), 1.0
+    a = torch.zeros(1, 8, 64, dtype=torch.bfloat16, device="cuda")
+    a[:, :, 5] = 2.0
+    a[:, :, :5] = 1.0
+    b = torch.ones(1, 96, 8, dtype=torch.bfloat16, device="cuda")
+    b[:, 48:] = -1.0
+    y = torch.ones(2, 96, dtype=torch.bfloat16, device="cuda")
+    x[0, 6:] = 0.0
+    a[:, :, 6:] = 1.0
+    ws = torch.zeros(64, dtype=torch.uint8, device="cuda")
+    sgp.sgp_lora_apply(sgp.make_lora(a, b), ints([0, 0]), x, y, y, 2, ws)
+    assert sgp.sgp_status_from_workspace(ws) == sgp.SGP_OK
+    assert (y[0, :48] == float("inf")).all() and (y[0, 48:] == float("-inf")).all()
+    assert (y[1, :48] == 17.0).all() and (y[1, 48:] == -15.0).all()
+
+
 def test_lora_and_eviction_and_weights_captured():
     """One graph with all three, replayed on new inputs, beside a second graph on another stream."""
     def make(seed):
@@ -560,6 +579,18 @@ def test_binding_checks_on_the_gpu():
         a = dict(kv_len=x.kv_len, q=x.q, o=x.o, lse=x.lse) | kw
         with pytest.raises(ValueError):
             sgp.sgp_prefix_attention(x.dims, x.cache, x.prefix, a["kv_len"], a["q"], a["o"], a["lse"], 2, x.ws)
+    wide = sgp.make_heads(8, 2)                              # more KV heads than the caches have
+    three = sgp.make_prefix(*x.prefix.tensors[:3], x.prefix.tensors[3][:1])
+    one = sgp.make_cache(*(t[:1] for t in x.cache.tensors))
+    for dims, cache, prefix in ((wide, x.cache, x.prefix), (x.dims, one, x.prefix), (x.dims, x.cache, three)):
+        with pytest.raises(ValueError):
+            sgp.sgp_prefix_attention(dims, cache, prefix, x.kv_len, x.q, x.o, x.lse, 2, x.ws)
+    acc = torch.zeros(2, 1, x.cache.kv_cap, device="cuda")
+    with pytest.raises(ValueError):
+        sgp.sgp_attention_weights(x.dims, one, x.kv_len, x.q, x.lse, acc, 2, x.ws)
+    for a, b in ((one, x.cache), (x.cache, one)):
+        with pytest.raises(ValueError):
+            sgp.sgp_kv_evict(x.dims, a, b, sgp.make_evict(2), x.kv_len, x.kv_len, acc, acc, None, 2, x.ws)
     with pytest.raises(sgp.SgpError) as e:
         sgp.sgp_prefix_attention(x.dims, x.cache, x.prefix, x.kv_len, x.q, x.o, x.lse, 2, x.ws[:256])
     assert e.value.code == sgp.SGP_ERR_INVALID_ARG

@@ -121,7 +121,7 @@ def test_kv_evict_refuses_bad_arguments(lib, mem):
                dict(b=far), dict(b=src, wo=acc_out),                    # overlap; in place without acc
                dict(b=_cache(base, cap=19, k=0, v=20480), wo=acc),      # in place, another capacity
                dict(b=_cache(base, cap=10, k=40960, v=45000 - 45000 % 16)),  # the target's k and v
-               dict(wo=acc + 4), dict(nkv=0)):
+               dict(wo=acc + 4), dict(nkv=0), dict(kv_out=base + 4)):
         assert call(**kw) == E, kw
     d = sgp.make_heads(2, 2)
     assert sgp.sgp_kv_evict_workspace_bytes(d, 4, 8) > 4 * 2 * 8 * 4
