@@ -461,14 +461,15 @@ __device__ void own_part(const PrefixProblem& P, const Plan& pl, uint8_t* ring_a
 constexpr int kPStages = 5;
 constexpr int kPSub = 64;           // positions of a half
 constexpr float kPRaise = 8.f;
-constexpr uint32_t kTmemS = 0, kTmemP = 256, kTmemO = 384;  // columns; per group 2 x 64, 2 x 32, 64
+constexpr uint32_t kPBufs = 3;      // S (then P) of so many halves
+constexpr uint32_t kTmemS = 0, kTmemO = 384;  // columns; per group 3 x 64 and 64
 
 struct PrefixBars {
     uint64_t kv_full[kPStages], kv_empty[kPStages];
     uint64_t q_full[2];        // the group's query rows are in shared memory
-    uint64_t s_full[2][2];     // [group][buffer]; the group's half i uses buffer i & 1, phase i >> 1
-    uint64_t p_full[2][2];
-    uint64_t pv_done[2][2];    // O holds half i, P's buffer is free
+    uint64_t s_full[2][kPBufs];  // [group][buffer]; the group's half i uses buffer i % 3, phase i / 3
+    uint64_t p_full[2][kPBufs];
+    uint64_t pv_done[2][kPBufs];  // O holds the half
     uint64_t own[kOwnWarps][2];  // an own warp's K and V halves
     uint32_t tmem;
     int err;
@@ -524,7 +525,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
         for (int h = 0; h < 2; ++h) {
             mbar_init(&bar.q_full[h], 4);
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < (int)kPBufs; ++i) {
                 mbar_init(&bar.s_full[h][i], 1);
                 mbar_init(&bar.p_full[h][i], 4);
                 mbar_init(&bar.pv_done[h][i], 1);
@@ -595,8 +596,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
             const uint64_t dq = smem_desc_sw128(smem_u32(qs + h * 128 * 128));
             const uint64_t dk0 = smem_desc_sw128(smem_u32(ring)), dv0 = dk0 + kPHalf / 16;
             constexpr int kStageD = 2 * kPHalf / 16, kHalfD = kPSub * 128 / 16;
-            const uint32_t ts = tmem + kTmemS + 128 * h, to = tmem + kTmemO + 64 * h, tp = tmem + kTmemP + 64 * h;
-            uint32_t n_q = 0, n = 0;               // tiles of this group, halves whose S is issued
+            const uint32_t ts = tmem + kTmemS + 64 * kPBufs * h, to = tmem + kTmemO + 64 * h;
+            uint32_t n_q = 0;                      // tiles of this group
+            uint32_t buf_s = 0;                    // buffer of the next S
+            uint32_t buf_p = 0, ph_p = 0;          // buffer and phase of the next P
             uint32_t st_s = 0, ph_s = 0, st_p = 0;  // stages of the next S and the next product
             bool ok = true;
             auto scores = [&](int j) {  // S = Q K^T of the tile's half j
@@ -606,9 +609,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 }
                 const uint64_t dk = dk0 + st_s * kStageD + (j & 1) * kHalfD;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) tc_mma_bf16(ts + 64 * (n & 1u), dq + 2 * k, dk + 2 * k, id_s, k > 0);
-                tc_commit(&bar.s_full[h][n & 1u]);
-                ++n;
+                for (int k = 0; k < 4; ++k) tc_mma_bf16(ts + 64 * buf_s, dq + 2 * k, dk + 2 * k, id_s, k > 0);
+                tc_commit(&bar.s_full[h][buf_s]);
+                if (++buf_s == kPBufs) buf_s = 0;
                 if ((j & 1) && ++st_s == kPStages) st_s = 0, ph_s ^= 1;
             };
             for (int x = x0; x < x1 && ok;) {
@@ -630,12 +633,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                const uint32_t n0 = n;  // number of the tile's first half
-                scores(0);
-                if (ok && halves > 1) scores(1);
+                for (int j = 0; j < min(halves, (int)kPBufs) && ok; ++j) scores(j);
                 for (int j = 0; j < halves && ok; ++j) {
-                    const uint32_t i = n0 + j, buf = i & 1u;
-                    if (!(ok = mbar_wait_near(&bar.p_full[h][buf], (i >> 1) & 1u, ctx.timeout_ns))) {
+                    if (!(ok = mbar_wait_near(&bar.p_full[h][buf_p], ph_p, ctx.timeout_ns))) {
                         gave_up(21);
                         break;
                     }
@@ -643,13 +643,20 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     const uint64_t dv = dv0 + st_p * kStageD + (j & 1) * kHalfD;
 #pragma unroll
                     for (int k = 0; k < kPSub / 16; ++k)  // O += P V
-                        tc_mma_bf16_ta(to, tp + 32 * buf + 8 * k, dv + k * (16 * 128 / 16), id_o, !(j == 0 && k == 0));
-                    tc_commit(&bar.pv_done[h][buf]);
+                        tc_mma_bf16_ta(to, ts + 64 * buf_p + 8 * k, dv + k * (16 * 128 / 16), id_o, !(j == 0 && k == 0));
+                    tc_commit(&bar.pv_done[h][buf_p]);
+                    // the next S of this buffer: it may pass the product unless that is complete
+                    if (!(ok = mbar_wait_near(&bar.pv_done[h][buf_p], ph_p, ctx.timeout_ns))) {
+                        gave_up(33);
+                        break;
+                    }
+                    tc_fence_after();
                     if ((j & 1) || j + 1 == halves) {
-                        tc_commit(&bar.kv_empty[st_p]);
+                        mbar_arrive(&bar.kv_empty[st_p]);
                         if (++st_p == kPStages) st_p = 0;
                     }
-                    if (j + 2 < halves) scores(j + 2);
+                    if (++buf_p == kPBufs) buf_p = 0, ph_p ^= 1;
+                    if (j + (int)kPBufs < halves) scores(j + kPBufs);
                 }
                 if (halves & 1) {  // the last stage's second half holds no positions
                     if (++st_s == kPStages) st_s = 0, ph_s ^= 1;
@@ -663,16 +670,19 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const int h = (warp - 4) >> 2, quad = warp & 3;  // a warp reads its quadrant's TMEM lanes
         const int r = h * 128 + quad * 32 + lane;        // this thread's row of the tile
         const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
-        const uint32_t ts = tl + kTmemS + 128 * h, to = tl + kTmemO + 64 * h, tp = tl + kTmemP + 64 * h;
+        const uint32_t ts = tl + kTmemS + 64 * kPBufs * h, to = tl + kTmemO + 64 * h;
         const int row_of = (65536 + P.G - 1) / P.G;      // r / G = r * row_of >> 16 for r < 256
         const float2 sc2 = make_float2(P.scale_log2, P.scale_log2);
-        uint32_t it = 0;  // halves of this group
+        uint32_t buf = 0, ph = 0;  // buffer and phase of the half
         bool ok = true;
         // every wait's outcome is the warp's: its tensor-memory accesses are warp-wide
         auto wait = [&](uint64_t* bar_, uint32_t parity, uint32_t where) {
             if (__all_sync(0xffffffffu, mbar_wait_near(bar_, parity, ctx.timeout_ns))) return true;
             if (lane == 0) gave_up(where);
             return false;
+        };
+        auto multiplied = [&](uint32_t where) {  // the half before
+            return buf > 0 ? wait(&bar.pv_done[h][buf - 1], ph, where) : wait(&bar.pv_done[h][kPBufs - 1], ph ^ 1u, where);
         };
         for (int x = x0; x < x1 && ok;) {
             const Step s = step_at(pl, n, x);
@@ -710,9 +720,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
             float m = 0.f;  // what the weights are taken against (scaled scores, base 2)
             float2 l2 = make_float2(0.f, 0.f);
             int pos0 = (pl.first[s.g] + s.k) * kPrefixKeys;
-            for (int j = 0; j < halves; ++j, ++it, pos0 += kPSub) {
-                const uint32_t buf = it & 1u;
-                if (!(ok = wait(&bar.s_full[h][buf], (it >> 1) & 1u, 24))) break;
+            for (int j = 0; j < halves; ++j, pos0 += kPSub) {
+                if (!(ok = wait(&bar.s_full[h][buf], ph, 24))) break;
                 tc_fence_after();
                 if (pos0 + kPSub > len || pos0 < seen) {
                     // what lies behind the prefix, or before what any sequence of the group sees,
@@ -743,47 +752,47 @@ __global__ void __launch_bounds__(kPThreads, 1)
                         tmem_st_wait();
                     }
                     const float2 l_old = l2;
-                    bool first = true;
-                    while (true) {
+                    for (int tries = 0;; ++tries) {
                         // a row that has seen nothing yet: every score is -inf, every weight 0
                         const float sub = m == -INFINITY ? 0.f : -m;
                         const float2 sub2 = make_float2(sub, sub);
-                        float sr[64], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                        tmem_ld_wait_x64(ts + 64 * buf, sr);
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            uint32_t w[16];
+                        float sa[32], sb[32], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        uint32_t wa[16], wb[16];
+                        auto weights = [&](const float (&sr)[32], uint32_t (&w)[16]) {
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
-                                float2 v = make_float2(sr[32 * c + 2 * e], sr[32 * c + 2 * e + 1]);
+                                float2 v = fma2_ordered(make_float2(sr[2 * e], sr[2 * e + 1]), sc2, sub2);
                                 mx[e & 1] = fmaxf(mx[e & 1], v.x);
                                 mx[2 + (e & 1)] = fmaxf(mx[2 + (e & 1)], v.y);
-                                v = fma2(v, sc2, sub2);
                                 v.x = ex2(v.x);
                                 v.y = ex2(v.y);
                                 l2 = add2(l2, v);
                                 // the weight's rounding to bf16, the second product's operand type
                                 w[e] = pack_bf16x2(v.x, v.y);
                             }
-                            if (c == 0 && first && it > 1) {  // P(it - 2) has been multiplied
-                                if (!(ok = wait(&bar.pv_done[h][buf], ((it >> 1) & 1u) ^ 1u, 33))) break;
-                                tc_fence_after();
-                            }
-                            tmem_st_x16(tp + 32 * buf + 16 * c, w);
-                        }
-                        if (!ok) break;
-                        first = false;
-                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * P.scale_log2;
+                        };
+                        // the second scores are on their way beside the first ones' exponentials
+                        tmem_ld_wait_x32(ts + 64 * buf, sa);
+                        tmem_ld_x32(ts + 64 * buf + 32, sb);
+                        weights(sa, wa);
+                        tmem_ld_wait();
+                        weights(sb, wb);
+                        const float over = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));  // past m
                         // the first half also raises from below: its scores may be far under 0
-                        const bool far = top > m + kPRaise || (j == 0 && m == 0.f && top < -kPRaise);
-                        if (!__any_sync(0xffffffffu, far)) break;
-                        const float nm = j == 0 ? top : fmaxf(m, top);
+                        const bool far = over > (m == -INFINITY ? -INFINITY : kPRaise) ||
+                                         (j == 0 && m == 0.f && over < -kPRaise);
+                        // (scores past 2^26 round by more than that: m is near enough the second time)
+                        if (!__any_sync(0xffffffffu, far) || tries == 2) {
+                            tmem_st_x16(ts + 64 * buf, wa);  // P takes S's place
+                            tmem_st_x16(ts + 64 * buf + 16, wb);
+                            break;
+                        }
+                        const float top = over - sub, nm = j == 0 ? top : fmaxf(m, top);
                         const float c = j == 0 || m == -INFINITY ? 0.f : ex2(m - nm);
                         m = nm;
                         l2 = make_float2(l_old.x * c, l_old.y * c);
-                        tmem_st_wait();
                         if (j == 0) continue;
-                        if (!(ok = wait(&bar.pv_done[h][buf ^ 1u], ((it - 1) >> 1) & 1u, 25))) break;
+                        if (!(ok = multiplied(25))) break;
                         tc_fence_after();
 #pragma unroll 1
                         for (int q = 0; q < 64; q += 16) {
@@ -801,10 +810,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.p_full[h][buf]);
+                if (++buf == kPBufs) buf = 0, ph ^= 1;
             }
             if (!ok) break;
             // the last product, then this row's partial
-            if (!wait(&bar.pv_done[h][(it - 1) & 1u], ((it - 1) >> 1) & 1u, 26)) break;
+            if (!multiplied(26)) break;
             tc_fence_after();
             if (live) {
                 const size_t slot = b + (size_t)(pl.tile0[s.g] + s.kvh * pl.tiles[s.g] + s.tile);
