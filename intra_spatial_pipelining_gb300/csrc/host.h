@@ -1,7 +1,7 @@
 // What the C entry points outside runtime.cu share with it (all defined there).
 #pragma once
 
-#include "kernels.h"
+#include "serving.h"
 #include "sgp.h"
 
 namespace sgp {

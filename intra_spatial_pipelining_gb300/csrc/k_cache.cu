@@ -8,8 +8,7 @@
 //             below every number), in their order.
 #include <algorithm>
 
-#include "kernels.h"
-#include "mma.cuh"
+#include "serving.cuh"
 
 namespace sgp {
 

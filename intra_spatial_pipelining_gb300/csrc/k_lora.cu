@@ -13,8 +13,7 @@
 // bounds the kernel, with one adapter it is x and y.
 #include <algorithm>
 
-#include "kernels.h"
-#include "mma.cuh"
+#include "serving.cuh"
 
 namespace sgp {
 

@@ -18,8 +18,7 @@
 // loops is kept short: no unrolling, few divisions, one copy of what several warps need.
 #include <climits>
 
-#include "kernels.h"
-#include "mma.cuh"
+#include "serving.cuh"
 
 namespace sgp {
 
