@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kEThreads, 2)
     evict_kernel(const EvictProblem P, const int n_key, const int n_list, const KCtx ctx) {
     extern __shared__ uint32_t dyn[];  // [n_key] keys, [n_list] kept positions, SelectSmem
     SelectSmem& sm = *reinterpret_cast<SelectSmem*>(dyn + n_key + (MOVE ? n_list : 0));
-    griddep_launch();
+    if (!MOVE || P.kv_len == P.kv_len_out) griddep_launch();  // this call's second kernel
     griddep_wait();
     task_begin(ctx);
     const int tid = threadIdx.x;
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kMThreads) evict_move_kernel(const EvictProble
 int enqueue_weights(Launcher& L, const WeightsProblem& p, const KCtx& c, int sms) {
     void* args[] = {(void*)&p, (void*)&c};
     const void* f = p.G <= 8 ? (const void*)weights_kernel<1> : (const void*)weights_kernel<2>;
-    return L.launch(f, dim3(2 * sms), dim3(kWThreads), 0, args);
+    return L.launch(f, dim3(2 * sms), dim3(kWThreads), 0, args, true);
 }
 
 int enqueue_evict(Launcher& L, const EvictProblem& p, const KCtx& c) {
@@ -462,12 +462,12 @@ int enqueue_evict(Launcher& L, const EvictProblem& p, const KCtx& c) {
         const int pairs = p.T * p.nkv, rows = std::min(p.budget, p.cap);
         const int parts = std::max(1, std::min({16, 304 / pairs, rows / 64}));
         const int e = L.launch((const void*)evict_kernel<true>, dim3(parts, p.nkv, p.T), dim3(kEThreads),
-                               (size_t)(n_key + n_list) * 4 + sizeof(SelectSmem), args);
+                               (size_t)(n_key + n_list) * 4 + sizeof(SelectSmem), args, true);
         if (e || p.kv_len != p.kv_len_out) return e;
         return L.launch((const void*)evict_len_kernel, dim3(1), dim3(kEThreads), 0, args2, true);
     }
     const int e = L.launch((const void*)evict_kernel<false>, dim3(1, p.nkv, p.T), dim3(kEThreads),
-                           (size_t)n_key * 4 + sizeof(SelectSmem), args);
+                           (size_t)n_key * 4 + sizeof(SelectSmem), args, true);
     if (e) return e;
     return L.launch((const void*)evict_move_kernel, dim3(5, p.nkv, p.T), dim3(kMThreads), 0, args2, true);
 }

@@ -89,8 +89,6 @@ __global__ void __cluster_dims__(kLCluster, 1, 1) __launch_bounds__(kLThreads, R
     const uint32_t cr = cluster_rank();
     const int cluster = blockIdx.x / kLCluster, clusters = gridDim.x / kLCluster;
     const int blocks = (P.T + 31) >> 5;
-    griddep_wait();
-    task_begin(ctx);
 
     // The tiles.  Every CTA makes the same list, sequences in blocks of 32, a warp to a block: the
     // blocks' counts by group are added up by whoever needs them.
@@ -98,6 +96,8 @@ __global__ void __cluster_dims__(kLCluster, 1, 1) __launch_bounds__(kLThreads, R
     for (int i = tid; i <= P.n; i += kLThreads) first[i] = kLMaxT;
 #pragma unroll 1
     for (int i = tid; i < blocks * kLMaxT / 4; i += kLThreads) reinterpret_cast<uint32_t*>(count)[i] = 0;
+    griddep_wait();  // what is above may run beside the kernel before
+    task_begin(ctx);
     __syncthreads();
 #pragma unroll 1
     for (int t = tid; t < P.T; t += kLThreads) {
@@ -333,7 +333,7 @@ int enqueue_lora(Launcher& L, const LoraProblem& p, const KCtx& c) {
     // tiles at most: one of every sequence, or a started one per adapter and "none" beside full ones
     const int tiles = std::min(p.T, p.n + 1 + p.T / kLTile);
     return L.launch(f, dim3(kLCluster * std::min(tiles, kLClusters)), dim3(kLThreads),
-                    lora_smem_bytes(p.n, p.max_rank), args);
+                    lora_smem_bytes(p.n, p.max_rank), args, true);
 }
 
 }  // namespace sgp

@@ -516,7 +516,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
     Plan& pl = *reinterpret_cast<Plan*>(&bar + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     griddep_launch();
-    griddep_wait();
     if (tid == 0) {
         for (int s = 0; s < kPStages; ++s) {
             mbar_init(&bar.kv_full[s], 1);
@@ -542,6 +541,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         tmem_relinquish();
     }
     tc_fence_before();
+    griddep_wait();  // what is above may run beside the kernel before
     task_begin(ctx);
     static_assert(kPrefixMax / 32 * kPrefixMax * 4 <= 2 * 128 * 128 + kPStages * 2 * kPHalf, "scratch fits");
     build_plan(pl, reinterpret_cast<int*>(qs), P, ctx);  // ends with a barrier
@@ -919,7 +919,7 @@ int enqueue_prefix(Launcher& L, const PrefixProblem& p, const KCtx& c) {
     const size_t smem = 1024 + 2 * 128 * 128 + kPStages * 2 * kPHalf + sizeof(PrefixBars) + sizeof(Plan);
     void* args[] = {(void*)&p, (void*)&c};
     const void* f = p.G <= 8 ? (const void*)prefix_attn_kernel<1> : (const void*)prefix_attn_kernel<2>;
-    const int e = L.launch(f, dim3(kPrefixCtas), dim3(kPThreads), smem, args);
+    const int e = L.launch(f, dim3(kPrefixCtas), dim3(kPThreads), smem, args, true);
     if (e) return e;
     return L.launch((const void*)prefix_merge_kernel, dim3(p.T * p.nkv), dim3(32 * p.G), 0, args, true);
 }

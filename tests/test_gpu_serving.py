@@ -256,6 +256,67 @@ def test_prefix_attention_captured_and_beside_another_stream():
             x.check()
 
 
+def test_operators_behind_other_nodes_of_a_graph():
+    """Each operator directly behind a copy, a kernel of another stream that joins, and one another;
+    what they write is read by the next node."""
+    x = Prefix(31, 30, 16, 2, [400], [(t * 7) % 50 + 1 for t in range(30)], [0] * 30)
+    rng = np.random.default_rng(8)
+    a, b = bf16(rng, 2, 16, 1024), bf16(rng, 2, 1024, 16)
+    lora, of, ws = sgp.make_lora(a, b), ints([t % 2 for t in range(30)]), torch.zeros(64, dtype=torch.uint8, device="cuda")
+    cap, budget = x.cache.kv_cap, 20
+    acc, acc2 = torch.zeros(30, 2, cap, device="cuda"), torch.zeros(30, 2, budget, device="cuda")
+    to = [torch.zeros(30, 2, budget, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    ews = torch.zeros(sgp.sgp_kv_evict_workspace_bytes(x.dims, 30, budget), dtype=torch.uint8, device="cuda")
+    q_in, lens, n_out = torch.empty_like(x.q), x.kv_len.clone(), ints([0] * 30)
+    side = torch.cuda.Stream()
+
+    def step():
+        s = torch.cuda.current_stream()
+        side.wait_stream(s)
+        with torch.cuda.stream(side):
+            lens2 = lens.clone()                                 # a copy, on another branch
+            acc.zero_()
+        x.q.copy_(q_in)
+        s.wait_stream(side)
+        sgp.sgp_lora_apply(lora, of, x.q.view(30, -1), x.q.view(30, -1), xq.view(30, -1), 30, ws)
+        sgp.sgp_prefix_attention(x.dims, x.cache, x.prefix, lens2, xq, x.o, x.lse, 30, x.ws)
+        sgp.sgp_attention_weights(x.dims, x.cache, lens2, xq, x.lse, acc, 30, ws)
+        side.wait_stream(s)
+        with torch.cuda.stream(side):
+            summed = acc.sum()                                   # reads beside the eviction
+        sgp.sgp_kv_evict(x.dims, x.cache, sgp.make_cache(*to), sgp.make_evict(budget, 1, 4), lens2, n_out,
+                         acc, acc2, None, 30, ews)
+        s.wait_stream(side)
+        return [t.clone() for t in (x.o, x.lse, acc, acc2, n_out, to[0], summed)]
+
+    xq = torch.empty_like(x.q)
+    q_in.copy_(bf16(rng, 30, 16, D))
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for rep in range(4):
+        q_in.copy_(bf16(rng, 30, 16, D))
+        lens.copy_(ints([(t * 7 + rep) % 50 + 1 if (t * 7 + rep) % 50 < x.own[t] else x.own[t] for t in range(30)]))
+        for t in (x.o, acc, acc2, xq, *to):
+            t.fill_(0)
+        want = step()
+        torch.cuda.synchronize()
+        for t in (x.o, acc, acc2, xq, *to):
+            t.fill_(0)
+        graph.replay()
+        graph.replay()                                           # directly behind one another
+        torch.cuda.synchronize()
+        for status in (x.ws, ws, ews):
+            assert sgp.sgp_status_from_workspace(status) == sgp.SGP_OK
+        for got, ref in zip(outs, want):
+            assert torch.equal(got, ref)
+        x.q.copy_(xq)                                            # what the attention was given
+        x.own = lens.tolist()
+        x.check()
+
+
 def test_prefix_attention_far_into_long_caches():
     """Element offsets past 2^31 in the own cache and in the prefix: a window at their ends."""
     cap, W = (1 << 25) + 300, 200
