@@ -263,7 +263,8 @@ int sgp_router_topk_noalloc(const sgp_dims* dims, const void* h, const void* g_m
  *     and a stream) need a workspace each; calls ordered on the GPU may share one.
  *   - Device arrays of lengths and indices are checked on the device: what is out of range is
  *     recorded as SGP_ERR_DEVICE_BOUNDS and treated as each entry point says, never followed.
- *   - Every pointer must be accessible from the current device.
+ *   - Every pointer must be accessible from the current device, and 16-byte aligned where it is to
+ *     bf16 data (caches of the weights and the eviction: 32), else 4.
  *   - Of sgp_dims only n_q_heads, n_kv_heads and head_dim are read; of sgp_layer, here a cache,
  *     only k_cache, v_cache, kv_cap and window.                                             */
 
@@ -311,7 +312,7 @@ int sgp_prefix_attention(const sgp_dims* dims, const sgp_layer* cache, const sgp
  *   acc[b][j][p] += sum over the query heads h of KV head j of exp(q_h.k_p / sqrt(d) - lse_h)
  * for p < kv_len[b] (0 <= kv_len[b] <= kv_cap; out of range: nothing is added); acc behind kv_len
  * is left as it is.
- *   cache  only k_cache and kv_cap are read; window must be 0
+ *   cache  only k_cache (32-byte aligned) and kv_cap are read; window must be 0
  *   lse    device fp32 [n_tokens][n_q], as sgp_prefix_attention writes it (the prefix's share of
  *          the weight is then in it); a head with lse = -inf adds nothing
  *   acc    device fp32 [n_tokens][n_kv][kv_cap]
@@ -340,7 +341,8 @@ size_t sgp_kv_evict_workspace_bytes(const sgp_dims* dims, int n_tokens, int budg
  * own positions.  K and V rows of the target behind the new length are left as they are.  Cached
  * keys keep the rotation they were stored with.
  *   from, to   caches of n_tokens sequences; `to` may be the same cache (k, v, acc and kv_cap all
- *              the same: in place) or share no byte with `from`; its kv_cap >= budget
+ *              the same: in place) or share no byte with `from`; its kv_cap >= budget; k_cache and
+ *              v_cache are 32-byte aligned
  *   kv_len     device int32 [n_tokens], 0 <= kv_len[b] <= from->kv_cap (out of range: the
  *              sequence is left as it is); kv_len_out device int32 [n_tokens]: kv_len itself, or
  *              apart from it

@@ -14,14 +14,29 @@ namespace sgp {
 
 namespace {
 
+// 32 bytes that are read or written once: they leave L2 first.  (Attention weights, 295 MB: 45.6 us
+// so, 51 without; the eviction of 815 MB 137.5 and 140.)
+__device__ __forceinline__ void load_once(const void* p, uint4& a, uint4& b) {
+    asm volatile("ld.global.nc.L1::no_allocate.L2::evict_first.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                 : "l"(p));
+}
+
+__device__ __forceinline__ void store_once(void* p, const uint4& a, const uint4& b) {
+    asm volatile("st.global.L2::evict_first.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y),
+                 "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+}
+
 // ---------------------------------------------------------------------------------------
 // Accumulated attention weights.  One pass over K; the scores are S = K q^T on warp-level
 // matrix products (M = 16 positions, N = 8 heads, K = 64 dims) with K fragments loaded straight
-// from global memory: lane (g, c) loads 16 bytes of rows g and g + 8, and both operands read
+// from global memory: lane (g, c) loads 32 bytes of rows g and g + 8, and both operands read
 // the same permutation of the dims, so each product still sums matching pairs.  An item is 64
 // positions of one (sequence, KV head); the warps of the grid share the items in equal runs.
-// Bound by HBM: 64 sequences x 64 / 8 heads, up to 8192 positions, 295 MB, 51 us (5.8 TB/s, 0.85
-// of a copy's rate); 3 sequences of up to 577 positions 4.5 us, of which a launch is 2.
+// Bound by HBM: 64 sequences x 64 / 8 heads, up to 8192 positions, 295 MB, 45.6 us (6.5 TB/s, 0.95
+// of a copy's rate; the next item's loads issued beside this one's products made no difference);
+// 3 sequences of up to 577 positions 4.0 us, of which a launch is 2.
 // ---------------------------------------------------------------------------------------
 constexpr int kWThreads = 256;
 constexpr int kWPos = 64;
@@ -81,8 +96,7 @@ __global__ void __launch_bounds__(kWThreads, 2) weights_kernel(const WeightsProb
                 for (int h = 0; h < 2; ++h) {
                     const int p = m * 16 + h * 8 + g;
                     const uint4* src = reinterpret_cast<const uint4*>(k + (size_t)min(p, n - 1) * 64);
-                    kf[m][h][0] = src[cq];
-                    kf[m][h][1] = src[cq + 4];
+                    load_once(src + 2 * cq, kf[m][h][0], kf[m][h][1]);
                 }
             // lane (g, c) owns positions 16 c + g and 16 c + g + 8
             float* acc = P.acc + (size_t)pair * P.cap + p0 + cq * 16 + g;
@@ -97,7 +111,7 @@ __global__ void __launch_bounds__(kWThreads, 2) weights_kernel(const WeightsProb
                         P.q + (size_t)t * P.nq * 64 + (size_t)(kvh * P.G + min(h, P.G - 1)) * 64);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const uint4 v = src[cq + 4 * e];
+                        const uint4 v = src[2 * cq + e];
                         qf[nt][e][0] = v.x;
                         qf[nt][e][1] = v.y;
                         qf[nt][e][2] = v.z;
@@ -164,15 +178,15 @@ __global__ void __launch_bounds__(kWThreads, 2) weights_kernel(const WeightsProb
 // selection runs beside another's copies.  In place the selection is a kernel of its own, because
 // the move overwrites what it reads.
 //
-// Bound by the move: 64 sequences x 8 KV heads, 8192 -> 4096 positions, take 140 us for 815 MB
-// (5.8 TB/s), and 139 us with the rows 0, 2, 4 ... and no selection at all: every second 128-byte
+// Bound by the move: 64 sequences x 8 KV heads, 8192 -> 4096 positions, take 137.5 us for 815 MB
+// (5.9 TB/s), two or three more than the rows 0, 2, 4 ... without a selection: every second 128-byte
 // row of the source does not read at a plain copy's rate.  Four CTAs of 256 threads to an SM took
 // 221 us, one of 1024 146 us.  Two caches of 640 -> 512 take 9.6 us, latency: up to sixteen rounds
 // of counts with a barrier each, then loads of the rows.
 // ---------------------------------------------------------------------------------------
 constexpr int kEThreads = 512;
 constexpr int kEWarps = kEThreads / 32;
-constexpr int kEUnroll = 8;
+constexpr int kEUnroll = 4;  // 32-byte pieces in flight to a thread
 
 __device__ __forceinline__ uint32_t order_key(float v) {
     if (v != v) return 0u;             // NaN: below -inf
@@ -350,21 +364,21 @@ __global__ void __launch_bounds__(kEThreads, 2)
         const size_t so = (size_t)pair * P.cap, to = (size_t)pair * P.cap_out;
         // acc first: its few loads are under way while the rows' begin
         for (int r = r0 + tid; r < r1; r += kEThreads) P.acc_out[to + r] = P.acc[so + kept[r]];
-        const int c = tid & 7;  // 16-byte column of a row
-        constexpr int kRows = kEThreads / 8;
+        const int c = tid & 3;  // 32-byte column of a row
+        constexpr int kRows = kEThreads / 4;
 #pragma unroll 1
         for (int w = 0; w < 2; ++w) {
-            const uint4* src = reinterpret_cast<const uint4*>(w ? P.v : P.k) + so * 8 + c;
-            uint4* dst = reinterpret_cast<uint4*>(w ? P.v_out : P.k_out) + to * 8 + c;
+            const uint4* src = reinterpret_cast<const uint4*>(w ? P.v : P.k) + so * 8 + 2 * c;
+            uint4* dst = reinterpret_cast<uint4*>(w ? P.v_out : P.k_out) + to * 8 + 2 * c;
 #pragma unroll 1
-            for (int r = r0 + (tid >> 3); r < r1; r += kRows * kEUnroll) {
-                uint4 v[kEUnroll];
+            for (int r = r0 + (tid >> 2); r < r1; r += kRows * kEUnroll) {
+                uint4 v[kEUnroll][2];
 #pragma unroll
                 for (int u = 0; u < kEUnroll; ++u)
-                    if (r + u * kRows < r1) v[u] = __ldcs(src + (size_t)kept[r + u * kRows] * 8);
+                    if (r + u * kRows < r1) load_once(src + (size_t)kept[r + u * kRows] * 8, v[u][0], v[u][1]);
 #pragma unroll
                 for (int u = 0; u < kEUnroll; ++u)
-                    if (r + u * kRows < r1) __stcs(dst + (size_t)(r + u * kRows) * 8, v[u]);
+                    if (r + u * kRows < r1) store_once(dst + (size_t)(r + u * kRows) * 8, v[u][0], v[u][1]);
             }
         }
         // a new position starts at 0

@@ -51,11 +51,11 @@ int check_tokens(int T) {
     return T < 1 || T > kHostMaxTokens ? host_fail_arg("n_tokens must be in [1, 512]") : SGP_OK;
 }
 
-// The cache fields of a layer (the weights are not read).
-int check_cache(const sgp_dims* d, const sgp_layer* l, int T, bool values) {
+// The cache fields of a layer (the weights are not read).  align: of the loads of its rows.
+int check_cache(const sgp_dims* d, const sgp_layer* l, int T, bool values, size_t align) {
     if (!l) return host_fail_arg("cache is NULL");
-    if (bad16(l->k_cache) || (values && bad16(l->v_cache)))
-        return host_fail_arg("cache pointer NULL or not 16-byte aligned");
+    if (!l->k_cache || misaligned(l->k_cache, align) || (values && (!l->v_cache || misaligned(l->v_cache, align))))
+        return host_fail_arg("cache pointer NULL or not aligned (16 bytes for attention, 32 for weights and eviction)");
     if (l->kv_cap < 1) return host_fail_arg("kv_cap must be positive");
     if (l->window < 0) return host_fail_arg("window must be >= 0");
     if ((uint64_t)T * d->n_kv_heads * l->kv_cap >= (1ull << 31))
@@ -121,7 +121,7 @@ int prefix_attention(const sgp_dims* d, const sgp_layer* cache, const sgp_prefix
                      const int32_t* kv_len, const void* q, void* o, float* lse, int T, void* ws,
                      size_t ws_bytes, sgp_stream_t stream) {
     int r;
-    if ((r = check_heads(d, true)) || (r = check_tokens(T)) || (r = check_cache(d, cache, T, true)))
+    if ((r = check_heads(d, true)) || (r = check_tokens(T)) || (r = check_cache(d, cache, T, true, 16)))
         return r;
     if (bad4(kv_len)) return host_fail_arg("kv_len NULL or not aligned");
     if (bad16(q) || bad16(o)) return host_fail_arg("q or o NULL or not 16-byte aligned");
@@ -181,7 +181,7 @@ int attention_weights(const sgp_dims* d, const sgp_layer* cache, const int32_t* 
                       const void* q, const float* lse, float* acc, int T, void* ws,
                       size_t ws_bytes, sgp_stream_t stream) {
     int r;
-    if ((r = check_heads(d, true)) || (r = check_tokens(T)) || (r = check_cache(d, cache, T, false)))
+    if ((r = check_heads(d, true)) || (r = check_tokens(T)) || (r = check_cache(d, cache, T, false, 32)))
         return r;
     if (cache->window != 0) return host_fail_arg("attention weights of a sliding-window layer");
     if (bad4(kv_len) || bad4(lse) || bad4(acc)) return host_fail_arg("kv_len, lse or acc NULL or not aligned");
@@ -204,7 +204,7 @@ int kv_evict(const sgp_dims* d, const sgp_layer* from, const sgp_layer* to, cons
              int32_t* kept, int T, void* ws, size_t ws_bytes, sgp_stream_t stream) {
     int r;
     if ((r = check_heads(d, false)) || (r = check_tokens(T)) ||
-        (r = check_cache(d, from, T, true)) || (r = check_cache(d, to, T, true)))
+        (r = check_cache(d, from, T, true, 32)) || (r = check_cache(d, to, T, true, 32)))
         return r;
     if (!e) return host_fail_arg("policy is NULL");
     if (e->budget < 1 || e->budget > to->kv_cap)

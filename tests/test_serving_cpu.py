@@ -95,6 +95,7 @@ def test_attention_weights_refuses_bad_arguments(lib, mem):
         return lib.sgp_attention_weights(ctypes.byref(d), ctypes.byref(cache), kv_len, q, lse, acc, T,
                                          ws, nbytes, None)
     for kw in (dict(nq=15), dict(T=0), dict(T=513), dict(cache=_cache(base, window=5)),
+               dict(cache=_cache(base, k=16)),
                dict(cache=_cache(base, cap=0)), dict(cache=_cache(0)), dict(kv_len=None), dict(q=None),
                dict(q=base + 8), dict(lse=None), dict(acc=None), dict(acc=base + 2), dict(ws=None),
                dict(ws=base + 64), dict(nbytes=63)):
@@ -121,7 +122,8 @@ def test_kv_evict_refuses_bad_arguments(lib, mem):
                dict(b=far), dict(b=src, wo=acc_out),                    # overlap; in place without acc
                dict(b=_cache(base, cap=19, k=0, v=20480), wo=acc),      # in place, another capacity
                dict(b=_cache(base, cap=10, k=40960, v=45000 - 45000 % 16)),  # the target's k and v
-               dict(wo=acc + 4), dict(nkv=0), dict(kv_out=base + 4)):
+               dict(wo=acc + 4), dict(nkv=0), dict(kv_out=base + 4),
+               dict(a=_cache(base, cap=20, k=16, v=20480)), dict(b=_cache(base, cap=10, k=40960, v=51216))):
         assert call(**kw) == E, kw
     d = sgp.make_heads(2, 2)
     assert sgp.sgp_kv_evict_workspace_bytes(d, 4, 8) > 4 * 2 * 8 * 4
