@@ -94,13 +94,16 @@ __device__ __forceinline__ int chunks_of(int n, const PrefixProblem& P) {
     return (n + (1 << P.chunk_log2) - 1) >> P.chunk_log2;
 }
 
-// CTAs that take the own caches: what makes the slower part fastest, of the multiples of 5.  An own
-// CTA streams 85 GB/s, up to 6.6 TB/s together (measured: 77 on 8 CTAs with short chunks, 100 on
-// 40), a prefix CTA takes 1.3 us for a step; beginning and end cost 3 and 6 us.
-__device__ __forceinline__ int own_ctas(long long own_pos, int nkv, int steps, int lane) {
+// CTAs that take the own caches: what makes the slower part fastest, of the multiples of 5.  Measured
+// from the launch on: own CTAs begin after 5 us, each of their warps takes 1.8 us for 64 positions
+// of a chunk, all together at most 5 TB/s; prefix CTAs take 1.37 us for a step and 9.5 for all else.
+__device__ __forceinline__ int own_ctas(long long own_pos, int chunks, int nkv, int steps, int lane) {
     const int x = lane < 31 ? 5 * lane : kPrefixCtas, y = kPrefixCtas - x;
-    const float own = x > 0 ? 3000.f + __fdividef((float)own_pos * (float)(nkv * 256), fminf(85.f * x, 6600.f)) : 0.f;
-    const float pre = y > 0 ? 6000.f + 1300.f * (__fdividef((float)steps, (float)y) + 0.5f) : 0.f;
+    const float pos = (float)own_pos * (float)nkv;
+    const float rounds = ceilf(__fdividef((float)chunks, (float)(kOwnWarps * x)));
+    const float warp = rounds * __fdividef(pos, (float)chunks) * (1800.f / 64.f);
+    const float own = x > 0 ? 5000.f + fmaxf(pos * (256.f / 5000.f), warp) : 0.f;
+    const float pre = y > 0 ? 9500.f + 1370.f * (__fdividef((float)steps, (float)y) + 0.5f) : 0.f;
     float cost = fmaxf(own, pre);
     if ((x == 0 && own_pos > 0) || (y == 0 && steps > 0)) cost = INFINITY;
     int best = x;
@@ -212,7 +215,7 @@ __device__ void build_plan(Plan& pl, int* scratch, const PrefixProblem& P, const
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) pos += __shfl_xor_sync(0xffffffffu, pos, o);
         __syncwarp();
-        const int x = own_ctas(pos, P.nkv, pl.step0[n], lane);
+        const int x = own_ctas(pos, chunks, P.nkv, pl.step0[n], lane);
         if (lane == 0) {
             const int total = pl.step0[n], shares = min(kPrefixCtas - x, total);  // none empty
             pl.chunk0[P.T] = chunks;
@@ -250,7 +253,7 @@ __device__ __noinline__ Step step_at(const Plan& pl, int n, int x) {
 // layer's attention streams its caches.  S^T = K q^T and O^T += V^T P^T on warp-level products, the
 // heads of a group their N; a chunk's (m, l, a) go to its partial.
 struct OwnChunk {
-    int i, t, kvh, c, p0, p1;
+    int t, kvh, c, p0, p1;
 };
 __device__ __forceinline__ OwnChunk own_chunk(const Plan& pl, const PrefixProblem& P, int i) {
     int lo = 0, hi = P.T;  // the last sequence whose chunks begin at or before i
@@ -261,7 +264,22 @@ __device__ __forceinline__ OwnChunk own_chunk(const Plan& pl, const PrefixProble
     }
     const int per = (pl.chunk0[lo + 1] - pl.chunk0[lo]) / P.nkv, r = i - pl.chunk0[lo];
     const int kvh = r / per, c = r - kvh * per, p0 = pl.own_first[lo] + (c << P.chunk_log2);
-    return {i, lo, kvh, c, p0, min(pl.own_len[lo], p0 + (1 << P.chunk_log2))};
+    return {lo, kvh, c, p0, min(pl.own_len[lo], p0 + (1 << P.chunk_log2))};
+}
+// The chunk behind k, if there is one (the search and its divisions took 600 cycles a chunk).
+__device__ __forceinline__ void own_next(const Plan& pl, const PrefixProblem& P, OwnChunk& k) {
+    ++k.c;
+    k.p0 = k.p1;
+    if (k.p0 >= pl.own_len[k.t]) {
+        k.c = 0;
+        if (++k.kvh == P.nkv) {
+            k.kvh = 0;
+            do ++k.t;
+            while (pl.own_first[k.t] >= pl.own_len[k.t]);
+        }
+        k.p0 = pl.own_first[k.t];
+    }
+    k.p1 = min(pl.own_len[k.t], k.p0 + (1 << P.chunk_log2));
 }
 
 template <int NT>
@@ -278,19 +296,36 @@ __device__ void own_part(const PrefixProblem& P, const Plan& pl, uint8_t* ring_a
     const uint32_t ka = smem_u32(ring), va = ka + kOwnHalf;
     const uint64_t pol = policy_evict_first();
     OwnChunk cs = own_chunk(pl, P, i), ld = cs;
-    int ld_p = ld.p0, v_row = 0;
+    int ld_i = i, ld_p = ld.p0, v_row = 0;
+    // The query fragments of a new (sequence, KV head) are asked for with its first keys, which is
+    // after the last use of the ones before
+    uint32_t qf[NT][4][2];
+    int pair = -1;
     uint32_t n_k = 0, n_v = 0, c_k = 0, c_v = 0;  // halves issued and consumed
     auto issue_k = [&] {
-        v_row = (ld.t * P.nkv + ld.kvh) * P.kv_cap + ld_p;
+        const int ld_pair = ld.t * P.nkv + ld.kvh;
+        v_row = ld_pair * P.kv_cap + ld_p;
         if (lane == 0) {
             mbar_arrive_expect_tx(bar_k, kOwnHalf);
             tma_load_2d(ring, &P.tmK, bar_k, 0, v_row, pol);
         }
         ++n_k;
+        if (ld_pair != pair) {
+            pair = ld_pair;
+            const bf16* q = P.q + (size_t)pair * P.G * 64;  // [T][nkv][G][64]
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    const int h = nt * 8 + g;
+                    const uint32_t* src = reinterpret_cast<const uint32_t*>(q + h * 64 + kk * 16 + 2 * cq);
+                    qf[nt][kk][0] = h < P.G ? src[0] : 0u;
+                    qf[nt][kk][1] = h < P.G ? src[4] : 0u;
+                }
+        }
         ld_p += kOwnPos;
         if (ld_p >= ld.p1) {
-            if (ld.i + 1 < i1) ld = own_chunk(pl, P, ld.i + 1);
-            else ld.i = i1;
+            if (++ld_i < i1) own_next(pl, P, ld);
             ld_p = ld.p0;
         }
     };
@@ -303,25 +338,9 @@ __device__ void own_part(const PrefixProblem& P, const Plan& pl, uint8_t* ring_a
     };
     issue_k();
     issue_v();
-    uint32_t qf[NT][4][2];
     float m[NT][2], l[NT][2], o[4][NT][4];
-    int pair = -1;
     bool ok = true;
     for (; i < i1 && ok; ++i) {
-        if (i > cs.i) cs = own_chunk(pl, P, i);
-        if (cs.t * P.nkv + cs.kvh != pair) {  // query fragments of the new (sequence, KV head)
-            pair = cs.t * P.nkv + cs.kvh;
-            const bf16* q = P.q + (size_t)cs.t * P.nq * 64 + (size_t)cs.kvh * P.G * 64;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    const int h = nt * 8 + g;
-                    const uint32_t* src = reinterpret_cast<const uint32_t*>(q + h * 64 + kk * 16 + 2 * cq);
-                    qf[nt][kk][0] = h < P.G ? src[0] : 0u;
-                    qf[nt][kk][1] = h < P.G ? src[4] : 0u;
-                }
-        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             m[nt][0] = m[nt][1] = -INFINITY;
@@ -354,7 +373,7 @@ __device__ void own_part(const PrefixProblem& P, const Plan& pl, uint8_t* ring_a
             // K is consumed: the next keys load beside the softmax and the V product
             fence_proxy_async();
             __syncwarp();
-            if (ld.i < i1) issue_k();
+            if (ld_i < i1) issue_k();
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float mx[2] = {-INFINITY, -INFINITY};
@@ -425,7 +444,7 @@ __device__ void own_part(const PrefixProblem& P, const Plan& pl, uint8_t* ring_a
             if (n_v < n_k) issue_v();
         }
         if (!ok) break;
-        const size_t at = ((size_t)pair * P.S_max + cs.c) * 16;
+        const size_t at = ((size_t)(cs.t * P.nkv + cs.kvh) * P.S_max + cs.c) * 16;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -442,6 +461,7 @@ __device__ void own_part(const PrefixProblem& P, const Plan& pl, uint8_t* ring_a
                     acc[md * 16 + 8] = o[md][nt][2 + e];
                 }
             }
+        if (i + 1 < i1) own_next(pl, P, cs);
     }
     // loads in flight into this warp's stage, if it gave up (bounded)
     for (; c_k < n_k; ++c_k) (void)mbar_wait(bar_k, c_k & 1u, 10000000ull);
