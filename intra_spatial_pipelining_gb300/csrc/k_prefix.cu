@@ -34,6 +34,9 @@ constexpr int kOwnWarps = kPThreads / 32;
 constexpr int kOwnPos = 64;                  // positions of an own warp's stage
 constexpr int kOwnHalf = kOwnPos * 128;      // K (or V) bytes of it
 constexpr int kPHalf = kPrefixKeys * 128;     // K (or V) bytes of a step
+// The prefixes' work is cut into equal shares by units, a step each and these for the beginning of a
+// tile: what lies between two tiles (output, queries, first product: 2.7 us) is worth two steps.
+constexpr int kTileUnits = 2;
 
 // The groups of the batch, built by every CTA in shared memory.
 struct Plan {
@@ -42,7 +45,7 @@ struct Plan {
     int rank[kPrefixMax];        // its place in the group
     int base[kPrefixMax + 1];    // first entry of a group in mem
     int tile0[kPrefixMax + 1];   // first tile of a group
-    int step0[kPrefixMax + 1];   // first step of a group
+    int step0[kPrefixMax + 1];   // first unit of a group
     int tiles[kPrefixMax];       // tiles per KV head
     int steps[kPrefixMax];       // steps per tile
     int first[kPrefixMax];       // first step's place in the prefix (in steps)
@@ -53,7 +56,7 @@ struct Plan {
     int own_len[kPrefixMax];
     int block_chunks[kPrefixMax / 32], block_pos[kPrefixMax / 32];  // of 32 sequences: own chunks, positions
     int n_own;                   // CTAs that take the own caches; the others take the prefixes:
-    int shares, q, n_long;       // shares of q steps, the first n_long of one more
+    int shares, q, n_long;       // shares of q units, the first n_long of one more
 };
 
 // exclusive prefix sums over n <= kPrefixMax values of three arrays by one warp; x[n] = total
@@ -95,17 +98,17 @@ __device__ __forceinline__ int chunks_of(int n, const PrefixProblem& P) {
 }
 
 // CTAs that take the own caches: what makes the slower part fastest, of the multiples of 5.  Measured
-// from the launch on: own CTAs begin after 5 us, each of their warps takes 1.8 us for 64 positions
-// of a chunk, all together at most 5 TB/s; prefix CTAs take 1.37 us for a step and 9.5 for all else.
-__device__ __forceinline__ int own_ctas(long long own_pos, int chunks, int nkv, int steps, int lane) {
+// from the launch on: own CTAs begin after 5.5 us, each of their warps takes 1.8 us for 64 positions
+// of a chunk, all together at most 5 TB/s; prefix CTAs take 1.37 us for a unit and 7.5 for all else.
+__device__ __forceinline__ int own_ctas(long long own_pos, int chunks, int nkv, int units, int lane) {
     const int x = lane < 31 ? 5 * lane : kPrefixCtas, y = kPrefixCtas - x;
     const float pos = (float)own_pos * (float)nkv;
     const float rounds = ceilf(__fdividef((float)chunks, (float)(kOwnWarps * x)));
     const float warp = rounds * __fdividef(pos, (float)chunks) * (1800.f / 64.f);
-    const float own = x > 0 ? 5000.f + fmaxf(pos * (256.f / 5000.f), warp) : 0.f;
-    const float pre = y > 0 ? 9500.f + 1370.f * (__fdividef((float)steps, (float)y) + 0.5f) : 0.f;
+    const float own = x > 0 ? 5500.f + fmaxf(pos * (256.f / 5000.f), warp) : 0.f;
+    const float pre = y > 0 ? 7500.f + 1370.f * (__fdividef((float)units, (float)y) + 0.5f) : 0.f;
     float cost = fmaxf(own, pre);
-    if ((x == 0 && own_pos > 0) || (y == 0 && steps > 0)) cost = INFINITY;
+    if ((x == 0 && own_pos > 0) || (y == 0 && units > 0)) cost = INFINITY;
     int best = x;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -205,7 +208,7 @@ __device__ void build_plan(Plan& pl, int* scratch, const PrefixProblem& P, const
         pl.tiles[g] = some ? (int)((unsigned)(members + P.tile_seqs - 1) * P.tile_inv >> 22) : 0;
         pl.steps[g] = some ? (len + kPrefixKeys - 1) / kPrefixKeys - first : 0;
         pl.tile0[g] = pl.tiles[g] * P.nkv;
-        pl.step0[g] = pl.tile0[g] * pl.steps[g];
+        pl.step0[g] = pl.tile0[g] * (pl.steps[g] + kTileUnits);
     }
     __syncthreads();
     if (warp == 0) {
@@ -233,7 +236,7 @@ __device__ void build_plan(Plan& pl, int* scratch, const PrefixProblem& P, const
     __syncthreads();
 }
 
-// Step x of the call: group, KV head, tile of that pair, step within the tile.
+// Unit x of the call: group, KV head, tile of that pair, unit (then step) within the tile.
 struct Step {
     int g, kvh, tile, k;
 };
@@ -244,8 +247,15 @@ __device__ __noinline__ Step step_at(const Plan& pl, int n, int x) {
         if (pl.step0[mid] <= x) lo = mid;
         else hi = mid;
     }
-    const int r = x - pl.step0[lo], i = r / pl.steps[lo], kvh = i / pl.tiles[lo];
-    return {lo, kvh, i - kvh * pl.tiles[lo], r - i * pl.steps[lo]};
+    const int units = pl.steps[lo] + kTileUnits, r = x - pl.step0[lo], i = r / units, kvh = i / pl.tiles[lo];
+    return {lo, kvh, i - kvh * pl.tiles[lo], r - i * units};
+}
+// What the units [x, x1) hold of s's tile: its steps from s.k on, how many; x goes to the next tile.
+__device__ __forceinline__ int take_tile(const Plan& pl, int& x, int x1, Step& s) {
+    const int m = min(x1 - x, pl.steps[s.g] + kTileUnits - s.k), end = s.k + m - kTileUnits;
+    x += m;
+    s.k = max(0, s.k - kTileUnits);
+    return end - s.k;
 }
 
 // The own caches: independent warps, each with a private stage of 64 positions, K and V halves
@@ -510,7 +520,7 @@ __device__ __forceinline__ int halves_of(const Plan& pl, const Step& s, int step
     return (min(pl.len[s.g] - p0, steps * kPrefixKeys) + kPSub - 1) / kPSub;
 }
 
-// The share that holds step x: the first n_long have q + 1 steps, the others q.
+// The share that holds unit x: the first n_long have q + 1 steps, the others q.
 __device__ __forceinline__ int share_of(const Plan& pl, int x) {
     const int r = x - pl.n_long * (pl.q + 1);
     return r < 0 ? x / (pl.q + 1) : pl.n_long + r / pl.q;
@@ -523,7 +533,8 @@ __device__ void list_parts(const Plan& pl, const PrefixProblem& P, int i, int st
         PrefixParts p = {0, 0, 0, chunks_of(pl.own_len[t] - pl.own_first[t], P)};
         if (g >= 0 && pl.tiles[g] > 0) {
             const int rank = pl.rank[t], seq = (int)((unsigned)rank * P.tile_inv >> 22);
-            const int tile = kvh * pl.tiles[g] + seq, x = pl.step0[g] + tile * pl.steps[g];
+            const int tile = kvh * pl.tiles[g] + seq;
+            const int x = pl.step0[g] + tile * (pl.steps[g] + kTileUnits) + kTileUnits;  // its first step
             const int s0 = share_of(pl, x);
             p.slot = s0 + pl.tile0[g] + tile;
             p.row = (rank - seq * P.tile_seqs) * P.G;
@@ -594,10 +605,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
             const uint64_t pol = policy_evict_last();  // the other row tiles read it too
             uint32_t it = 0;
             for (int x = x0; x < x1 && !*err;) {
-                const Step s = step_at(pl, n, x);
-                const int steps = min(x1 - x, pl.steps[s.g] - s.k);
+                Step s = step_at(pl, n, x);
+                const int steps = take_tile(pl, x, x1, s);
                 int row = (s.g * P.nkv + s.kvh) * P.prefix.cap + (pl.first[s.g] + s.k) * kPrefixKeys;
-                x += steps;
 #pragma unroll 1
                 for (int i = 0; i < steps; ++i, ++it, row += kPrefixKeys) {
                     const uint32_t st = it % kPStages, use = it / kPStages;
@@ -643,10 +653,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 if ((j & 1) && ++st_s == kPStages) st_s = 0, ph_s ^= 1;
             };
             for (int x = x0; x < x1 && ok;) {
-                const Step s = step_at(pl, P.prefix.n, x);
-                const int steps = min(x1 - x, pl.steps[s.g] - s.k), halves = halves_of(pl, s, steps);
+                Step s = step_at(pl, P.prefix.n, x);
+                const int steps = take_tile(pl, x, x1, s);
+                if (steps <= 0) continue;
+                const int halves = halves_of(pl, s, steps);
                 const int rows = min(P.tile_seqs, pl.base[s.g + 1] - pl.base[s.g] - s.tile * P.tile_seqs) * P.G;
-                x += steps;
                 if (rows <= 128 * h) {  // no rows here: the stages are free for this group's part
                     for (int i = 0; i < steps && ok; ++i) {
                         if (!(ok = mbar_wait_near(&bar.kv_full[st_s], ph_s, ctx.timeout_ns))) gave_up(31);
@@ -702,6 +713,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const int row_of = (65536 + P.G - 1) / P.G;      // r / G = r * row_of >> 16 for r < 256
         const float2 sc2 = make_float2(P.scale_log2, P.scale_log2);
         uint32_t buf = 0, ph = 0;  // buffer and phase of the half
+        int done = 0;              // steps of earlier tiles
         bool ok = true;
         // every wait's outcome is the warp's: its tensor-memory accesses are warp-wide
         auto wait = [&](uint64_t* bar_, uint32_t parity, uint32_t where) {
@@ -713,12 +725,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
             return buf > 0 ? wait(&bar.pv_done[h][buf - 1], ph, where) : wait(&bar.pv_done[h][kPBufs - 1], ph ^ 1u, where);
         };
         for (int x = x0; x < x1 && ok;) {
-            const Step s = step_at(pl, n, x);
-            const int steps = min(x1 - x, pl.steps[s.g] - s.k), halves = halves_of(pl, s, steps);
+            Step s = step_at(pl, n, x);
+            const int steps = take_tile(pl, x, x1, s);
+            if (steps <= 0) continue;
+            const int halves = halves_of(pl, s, steps);
             const int seq0 = pl.base[s.g] + s.tile * P.tile_seqs;
             const int rows = min(P.tile_seqs, pl.base[s.g + 1] - seq0) * P.G;
-            const int i0 = x - x0;  // first step's place in the share
-            x += steps;
+            const int i0 = done;  // first step's place in the share
+            done += steps;
             if (rows <= 128 * h) continue;
             const int len = pl.len[s.g], seen = pl.low[s.g];
             // this warp's 32 query rows, 8 lanes to a row, into the swizzled tile (zeros past the

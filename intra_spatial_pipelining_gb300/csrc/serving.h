@@ -18,8 +18,9 @@ struct PrefixRef {
 //
 // Prefixes: sequences with the same prefix form a group; a row is one (sequence, query head) of
 // the group and KV head.  A tile is `tile_seqs` sequences' rows (at most kPrefixRows), a step is
-// one tile against kPrefixKeys positions.  The steps of all (group, KV head, tile) in order are
-// cut into equal shares, one per CTA; share s's part of tile i leaves its partial in slot s + i.
+// one tile against kPrefixKeys positions.  The steps of all (group, KV head, tile) in order, with
+// some units for the beginning of each tile, are cut into equal shares, one per CTA; share s's part
+// of tile i leaves its partial in slot s + i.
 // Own caches: chunks of 2^chunk_log2 positions of a (sequence, KV head), equal runs of them to a warp.
 constexpr int kPrefixRows = 256;
 constexpr int kPrefixKeys = 128;
