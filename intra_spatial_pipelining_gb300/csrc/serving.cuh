@@ -42,8 +42,10 @@ __device__ __forceinline__ uint32_t sw128(int r, int ch) {
 // ---------------------------------------------------------------------------------------
 // mbarrier and tcgen05
 // ---------------------------------------------------------------------------------------
-// mbar_wait for waits that stand in a chain of short steps: the first tries are a tight loop, and
-// the timer (whose read takes longer than such a wait) is read only when they are used up.
+// mbar_wait for waits that stand in a chain of short steps: one try in place, then tries in a tight
+// loop, and the timer (whose read takes longer than such a wait) only when they are used up.  What
+// follows the first try is a function, to keep the loops that wait small: the instructions of several
+// warps' loops compete for what a scheduler holds of them (0.96 of the time of a long prefix).
 __device__ __forceinline__ bool mbar_try_many(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -62,14 +64,17 @@ __device__ __forceinline__ bool mbar_try_many(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-__device__ __forceinline__ bool mbar_wait_near(uint64_t* bar, uint32_t parity, uint64_t timeout_ns) {
-    const uint32_t a = smem_u32(bar);
-    if (mbar_try_many(a, parity)) return true;
+__device__ __noinline__ inline bool mbar_wait_far(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
+    if (mbar_try_many(bar, parity)) return true;
     const uint64_t t0 = globaltimer();
     do {
-        if (mbar_try_many(a, parity)) return true;
+        if (mbar_try_many(bar, parity)) return true;
     } while (globaltimer() - t0 <= timeout_ns);
     return false;
+}
+__device__ __forceinline__ bool mbar_wait_near(uint64_t* bar, uint32_t parity, uint64_t timeout_ns) {
+    const uint32_t a = smem_u32(bar);
+    return mbar_try_wait(a, parity) || mbar_wait_far(a, parity, timeout_ns);
 }
 
 // tc_mma_bf16 with A in tensor memory: row r in lane r, elements 2c and 2c + 1 in column c.
