@@ -15,8 +15,8 @@
 // the other leaves idle.
 //
 // Measured (replayed): 64 sequences x 64 / 8 heads on a prefix of 8192 beside own caches of up to
-// 1024, 76 MB and 9.1 GFLOP, 30.5 us (2.5 TB/s); 512 sequences x 8 / 1 heads on 32,768, 34.6 GFLOP,
-// 57 us (607 TFLOP/s); two sequences on 500 positions 11 us.  Of these about 5.5 us pass before the
+// 1024, 76 MB and 9.1 GFLOP, 28.5 us (2.7 TB/s); 512 sequences x 8 / 1 heads on 32,768, 34.6 GFLOP,
+// 53 us (650 TFLOP/s); two sequences on 500 positions 11 us.  Of these about 5.5 us pass before the
 // first product (the plan of the groups 3.2, the query tile 2.4) and 5 us in the merge.
 //
 // Instructions that run once are met cold, about 300 cycles for eight of them, so what surrounds the
@@ -99,12 +99,13 @@ __device__ __forceinline__ int chunks_of(int n, const PrefixProblem& P) {
 
 // CTAs that take the own caches: what makes the slower part fastest, of the multiples of 5.  Measured
 // from the launch on: own CTAs begin after 5.5 us, each of their warps takes 1.8 us for 64 positions
-// of a chunk, all together at most 5 TB/s; prefix CTAs take 1.37 us for a unit and 7.5 for all else.
+// of a chunk or fewer (416 x 8 caches of up to 4 positions: 130 us on 5 CTAs, 23 on 75), all
+// together at most 5 TB/s; prefix CTAs take 1.37 us for a unit and 7.5 for all else.
 __device__ __forceinline__ int own_ctas(long long own_pos, int chunks, int nkv, int units, int lane) {
     const int x = lane < 31 ? 5 * lane : kPrefixCtas, y = kPrefixCtas - x;
     const float pos = (float)own_pos * (float)nkv;
     const float rounds = ceilf(__fdividef((float)chunks, (float)(kOwnWarps * x)));
-    const float warp = rounds * __fdividef(pos, (float)chunks) * (1800.f / 64.f);
+    const float warp = rounds * fmaxf(__fdividef(pos, (float)chunks), 64.f) * (1800.f / 64.f);
     const float own = x > 0 ? 5500.f + fmaxf(pos * (256.f / 5000.f), warp) : 0.f;
     const float pre = y > 0 ? 7500.f + 1370.f * (__fdividef((float)units, (float)y) + 0.5f) : 0.f;
     float cost = fmaxf(own, pre);
