@@ -170,8 +170,7 @@ __global__ void __launch_bounds__(kWThreads, 2) weights_kernel(const WeightsProb
 // The keys of the positions between the sinks and the recent ones are acc mapped to unsigned
 // integers of the same order, kept in shared memory (those that do not fit are read again).  The
 // threshold, the need-th largest key, is found two bits a round from counts, until exactly `need`
-// keys reach it; the positions above it stay, and of those equal to it the first ones.  Loops, not
-// registers: unrolled over registers, the code of a short selection was met cold, 5 us of it.
+// keys reach it; the positions above it stay, and of those equal to it the first ones.
 //
 // Into another cache one kernel does both: a few CTAs to a (sequence, KV head), each of which makes
 // the whole selection and moves its part of the rows, so that nothing is waited for and one CTA's
@@ -195,28 +194,41 @@ __device__ __forceinline__ uint32_t order_key(float v) {
     return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
-constexpr int kESeg = 32;  // blocks of kEThreads positions that are placed at a time
+constexpr int kESeg = 32;  // blocks of positions whose counts are summed at a time
 
 struct SelectSmem {
     int cnt[2][3][kEWarps];
-    int base[2][kESeg * kEWarps];  // larger and equal keys before 32 positions
+    int base[2][kESeg * kEWarps];  // larger and equal keys before a warp's positions of a block
     int total[2];
 };
 
 // Calls put(i, p) for the positions p that stay of `n` candidates from position `a` on, i = a ... in
-// their order.  key: shared memory for n_key of the candidates' keys.
-template <typename Put>
+// their order.  key: shared memory for n_key of the candidates' keys.  LONG: for thousands of
+// positions, with all loads at once, fewer keys in the later rounds and four positions of a block to
+// a thread (4 x 2 caches of up to 30,041 -> 16,809 positions: 41 us, 56 without; two of 640 -> 512
+// 10.7 us so, 9.6 without, since it is more code that is met cold).
+template <bool LONG, typename Put>
 __device__ void select_kept(SelectSmem& sm, uint32_t* key, int n_key, const float* acc, int a, int n, int need,
                             Put put) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int kPer = LONG ? 4 : 1, kEBlock = kPer * kEThreads;
     const int ns = min(n, n_key), n4 = (ns + 3) >> 2;
-    // (the last four are filled up with keys that no threshold of a count is below)
+    if constexpr (LONG) {
 #pragma unroll 4
-    for (int p = tid; p < 4 * n4; p += kEThreads) key[p] = p < ns ? order_key(acc[a + p]) : 0u;
+        for (int p = tid; p < ns; p += kEThreads)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(key + p)), "l"(acc + a + p) : "memory");
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+    // the last four are filled up with keys that no threshold of a count is below
+#pragma unroll 4
+    for (int p = tid; p < 4 * n4; p += kEThreads)
+        key[p] = p < ns ? order_key(LONG ? __uint_as_float(key[p]) : acc[a + p]) : 0u;
     __syncthreads();
-    auto key_at = [&](int p) { return p < ns ? key[p] : order_key(acc[a + p]); };
     uint32_t thr = 0;  // the largest value that at least `need` keys reach
     int reach = n;     // keys that reach it
+    int over = 0;      // keys past the values that are still in question, [thr, thr + 2^(bit + 2))
+    int m = 0, m_over = 0;                             // LONG: the keys in question once
+    uint32_t* few = reinterpret_cast<uint32_t*>(sm.base);  // they are 1024 at most, and `over` then
 #pragma unroll 1
     for (int bit = 30, ph = 0; bit >= 0 && reach != need; bit -= 2, ph ^= 1) {
         const uint32_t t1 = thr | 1u << bit, t2 = thr | 2u << bit, t3 = thr | 3u << bit;
@@ -226,16 +238,21 @@ __device__ void select_kept(SelectSmem& sm, uint32_t* key, int n_key, const floa
             c2 += k >= t2;
             c3 += k >= t3;
         };
-#pragma unroll 2
-        for (int p = tid; p < n4; p += kEThreads) {
-            const uint4 k = reinterpret_cast<const uint4*>(key)[p];
-            add(k.x);
-            add(k.y);
-            add(k.z);
-            add(k.w);
-        }
+        if (LONG && m > 0) {
 #pragma unroll 1
-        for (int p = ns + tid; p < n; p += kEThreads) add(order_key(acc[a + p]));
+            for (int p = tid; p < m; p += kEThreads) add(few[p]);
+        } else {
+#pragma unroll 4
+            for (int p = tid; p < n4; p += kEThreads) {
+                const uint4 k = reinterpret_cast<const uint4*>(key)[p];
+                add(k.x);
+                add(k.y);
+                add(k.z);
+                add(k.w);
+            }
+#pragma unroll 4
+            for (int p = ns + tid; p < n; p += kEThreads) add(order_key(acc[a + p]));
+        }
         c1 = __reduce_add_sync(0xffffffffu, c1);
         c2 = __reduce_add_sync(0xffffffffu, c2);
         c3 = __reduce_add_sync(0xffffffffu, c3);
@@ -245,40 +262,63 @@ __device__ void select_kept(SelectSmem& sm, uint32_t* key, int n_key, const floa
             sm.cnt[ph][2][warp] = c3;
         }
         __syncthreads();
-        c1 = __reduce_add_sync(0xffffffffu, lane < kEWarps ? sm.cnt[ph][0][lane] : 0);
-        c2 = __reduce_add_sync(0xffffffffu, lane < kEWarps ? sm.cnt[ph][1][lane] : 0);
-        c3 = __reduce_add_sync(0xffffffffu, lane < kEWarps ? sm.cnt[ph][2][lane] : 0);
+        c1 = m_over + __reduce_add_sync(0xffffffffu, lane < kEWarps ? sm.cnt[ph][0][lane] : 0);
+        c2 = m_over + __reduce_add_sync(0xffffffffu, lane < kEWarps ? sm.cnt[ph][1][lane] : 0);
+        c3 = m_over + __reduce_add_sync(0xffffffffu, lane < kEWarps ? sm.cnt[ph][2][lane] : 0);
         if (c3 >= need) thr = t3, reach = c3;
-        else if (c2 >= need) thr = t2, reach = c2;
-        else if (c1 >= need) thr = t1, reach = c1;
+        else if (c2 >= need) thr = t2, reach = c2, over = c3;
+        else if (c1 >= need) thr = t1, reach = c1, over = c2;
+        else over = c1;
+        if (LONG && m == 0 && n > 4096 && reach - over <= kESeg * kEWarps * 2 && reach != need && bit > 0) {
+            const uint32_t width = 1u << bit;  // the keys in question are thr and the width - 1 above it
+            if (tid == 0) sm.total[0] = 0;
+            __syncthreads();
+            auto keep = [&](uint32_t k) {
+                if (k - thr < width) few[atomicAdd(&sm.total[0], 1)] = k;  // (k < thr wraps)
+            };
+#pragma unroll 1
+            for (int p = tid; p < ns; p += kEThreads) keep(key[p]);
+#pragma unroll 1
+            for (int p = ns + tid; p < n; p += kEThreads) keep(order_key(acc[a + p]));
+            __syncthreads();
+            m = reach - over;
+            m_over = over;
+        }
     }
     // keys above `top` all stay, and of those equal to it the first need - (their number)
     const bool ties = reach != need;
     const uint32_t top = ties ? thr : thr - 1;  // (thr > 0 when reach == need < n)
-    int take_eq = 0;
-    if (ties) {
-        int c = 0;
-        for (int p = tid; p < n; p += kEThreads) c += key_at(p) > top;
-        c = __reduce_add_sync(0xffffffffu, c);
-        __syncthreads();
-        if (lane == 0) sm.cnt[0][0][warp] = c;
-        __syncthreads();
-        take_eq = need - __reduce_add_sync(0xffffffffu, lane < kEWarps ? sm.cnt[0][0][lane] : 0);
-    }
+    const int take_eq = ties ? need - over : 0;  // (with every bit settled, `over` are above thr)
+    // a thread's keys from candidate p on; what is past the end is 0 and not equal
+    auto keys = [&](int p, uint32_t (&k)[kPer]) {
+        if (LONG && p + 3 < ns) {
+            const uint4 v = *reinterpret_cast<const uint4*>(key + p);
+            k[0] = v.x, k[1 % kPer] = v.y, k[2 % kPer] = v.z, k[3 % kPer] = v.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) k[e] = p + e < ns ? key[p + e] : p + e < n ? order_key(acc[a + p + e]) : 0u;
+        }
+    };
+    auto count = [&](int p, const uint32_t (&k)[kPer]) {  // larger ones, and 65536 x equal ones
+        uint32_t c = 0;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) c += (k[e] > top ? 1u : 0u) + (ties && k[e] == top && p + e < n ? 65536u : 0u);
+        return c;
+    };
     int out0 = 0, eq0 = 0;  // taken / equal ones in earlier segments
 #pragma unroll 1
-    for (int p0 = 0; p0 < n; p0 += kESeg * kEThreads) {
-        const int blocks = min(kESeg, (n - p0 + kEThreads - 1) / kEThreads);
+    for (int p0 = 0; p0 < n; p0 += kESeg * kEBlock) {
+        const int blocks = min(kESeg, (n - p0 + kEBlock - 1) / kEBlock);
         __syncthreads();
 #pragma unroll 1
         for (int i = 0; i < blocks; ++i) {
-            const int p = p0 + i * kEThreads + tid;
-            const uint32_t k = p < n ? key_at(p) : 0u;
-            const int gt = __popc(__ballot_sync(0xffffffffu, k > top));
-            const int eq = __popc(__ballot_sync(0xffffffffu, ties && k == top && p < n));
+            const int p = p0 + i * kEBlock + kPer * tid;
+            uint32_t k[kPer];
+            keys(p, k);
+            const uint32_t c = __reduce_add_sync(0xffffffffu, count(p, k));
             if (lane == 0) {
-                sm.base[0][i * kEWarps + warp] = gt;
-                sm.base[1][i * kEWarps + warp] = eq;
+                sm.base[0][i * kEWarps + warp] = (int)(c & 0xffffu);
+                sm.base[1][i * kEWarps + warp] = (int)(c >> 16);
             }
         }
         __syncthreads();
@@ -299,19 +339,34 @@ __device__ void select_kept(SelectSmem& sm, uint32_t* key, int n_key, const floa
             if (lane == 0) sm.total[warp] = run;
         }
         __syncthreads();
-        const uint32_t below = (1u << lane) - 1u;
 #pragma unroll 1
         for (int i = 0; i < blocks; ++i) {
-            const int p = p0 + i * kEThreads + tid;
-            const uint32_t k = p < n ? key_at(p) : 0u;
-            const int eq_before = eq0 + sm.base[1][i * kEWarps + warp];
-            // taken before these 32: every larger key, and the first equal ones
-            const int out = out0 + sm.base[0][i * kEWarps + warp] + min(eq_before, take_eq) - min(eq0, take_eq);
-            const bool eq = ties && k == top && p < n;
-            const uint32_t meq = __ballot_sync(0xffffffffu, eq);
-            const bool take = k > top || (eq && eq_before + __popc(meq & below) < take_eq);
-            const uint32_t mt = __ballot_sync(0xffffffffu, take);
-            if (take) put(a + out + __popc(mt & below), a + p);
+            const int p = p0 + i * kEBlock + kPer * tid;
+            uint32_t k[kPer];
+            keys(p, k);
+            const uint32_t mine = count(p, k);
+            uint32_t before = mine;  // of the warp's lanes below this one
+            if constexpr (LONG) {
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t x = __shfl_up_sync(0xffffffffu, before, o);
+                    if (lane >= o) before += x;
+                }
+                before -= mine;
+            } else {
+                const uint32_t below = (1u << lane) - 1u;
+                before = __popc(__ballot_sync(0xffffffffu, (mine & 1u) != 0) & below) +
+                         (__popc(__ballot_sync(0xffffffffu, mine > 1u) & below) << 16);
+            }
+            int eq = eq0 + sm.base[1][i * kEWarps + warp] + (int)(before >> 16);
+            // taken before: every larger key, and the first equal ones
+            int out = out0 + sm.base[0][i * kEWarps + warp] + (int)(before & 0xffffu) + min(eq, take_eq) - min(eq0, take_eq);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+                const bool same = ties && k[e] == top && p + e < n;
+                if (k[e] > top || (same && eq < take_eq)) put(a + out++, a + p + e);
+                eq += same;
+            }
         }
         out0 += sm.total[0] + min(eq0 + sm.total[1], take_eq) - min(eq0, take_eq);
         eq0 += sm.total[1];
@@ -319,7 +374,7 @@ __device__ void select_kept(SelectSmem& sm, uint32_t* key, int n_key, const floa
 }
 
 // n_key, n_list: keys and kept positions that shared memory holds; with n_list = 0 the list is in P.kept.
-template <bool MOVE>
+template <bool MOVE, bool LONG>
 __global__ void __launch_bounds__(kEThreads, 2)
     evict_kernel(const EvictProblem P, const int n_key, const int n_list, const KCtx ctx) {
     extern __shared__ uint32_t dyn[];  // [n_key] keys, [n_list] kept positions, SelectSmem
@@ -355,7 +410,7 @@ __global__ void __launch_bounds__(kEThreads, 2)
             for (int i = tid; i < P.n_recent; i += kEThreads) put(a + need + i, L - P.n_recent + i);
         // need < candidates: L is past the budget
         if (need > 0)
-            select_kept(sm, dyn, n_key, P.acc + (size_t)pair * P.cap, a, L - P.n_recent - a, need, put);
+            select_kept<LONG>(sm, dyn, n_key, P.acc + (size_t)pair * P.cap, a, L - P.n_recent - a, need, put);
     }
     __syncthreads();
     if (MOVE && !bad) {
@@ -467,22 +522,27 @@ int enqueue_weights(Launcher& L, const WeightsProblem& p, const KCtx& c, int sms
 }
 
 int enqueue_evict(Launcher& L, const EvictProblem& p, const KCtx& c) {
-    // Shared memory for every key up to 8192 positions (two CTAs to an SM then), else for 24,576,
-    // and for the list where it is no longer than that.
-    const int n_key = p.cap <= 8192 ? (p.cap + 255) & ~255 : 24576;
-    const int n_list = p.budget <= n_key ? (p.budget + 255) & ~255 : 0;
+    // Shared memory for every key up to 49,152 of them, and for the list where it fits beside them
+    // (up to 8192 positions two CTAs to an SM, whatever the list).
+    constexpr int kWords = (227 * 1024 - (int)sizeof(SelectSmem)) / 4;
+    const int n_key = std::min((p.cap + 255) & ~255, 49152), list = (p.budget + 255) & ~255;
+    const int n_list = list <= kWords - n_key ? list : 0;
+    // The selection for long caches, unless so many (sequence, KV head) pairs are under way that their
+    // moves hide it: 32 pairs of 3000 positions 12.8 us without, 13.2 with it; of 6000 24.8 and 22.4;
+    // 512 pairs of up to 8192 135.7 and 138.2; 138 of up to 19,764 102 and 94.
+    const bool long_ = p.cap > 8192 || (p.cap > 4096 && p.T * p.nkv < 304);
     void* args[] = {(void*)&p, (void*)&n_key, (void*)&n_list, (void*)&c};
     void* args2[] = {(void*)&p, (void*)&c};
     if (!p.in_place) {
         // as many CTAs to a pair as give every SM two, at most 16, none with fewer than 64 rows
         const int pairs = p.T * p.nkv, rows = std::min(p.budget, p.cap);
         const int parts = std::max(1, std::min({16, 304 / pairs, rows / 64}));
-        const int e = L.launch((const void*)evict_kernel<true>, dim3(parts, p.nkv, p.T), dim3(kEThreads),
+        const int e = L.launch(long_ ? (const void*)evict_kernel<true, true> : (const void*)evict_kernel<true, false>, dim3(parts, p.nkv, p.T), dim3(kEThreads),
                                (size_t)(n_key + n_list) * 4 + sizeof(SelectSmem), args, true);
         if (e || p.kv_len != p.kv_len_out) return e;
         return L.launch((const void*)evict_len_kernel, dim3(1), dim3(kEThreads), 0, args2, true);
     }
-    const int e = L.launch((const void*)evict_kernel<false>, dim3(1, p.nkv, p.T), dim3(kEThreads),
+    const int e = L.launch(long_ ? (const void*)evict_kernel<false, true> : (const void*)evict_kernel<false, false>, dim3(1, p.nkv, p.T), dim3(kEThreads),
                            (size_t)n_key * 4 + sizeof(SelectSmem), args, true);
     if (e) return e;
     return L.launch((const void*)evict_move_kernel, dim3(5, p.nkv, p.T), dim3(kMThreads), 0, args2, true);

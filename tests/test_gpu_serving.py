@@ -432,7 +432,10 @@ EVICTIONS = [
     (2, 2, [1000, 999], 1000, 500, 1, 0, 0, "falling"), (1, 1, [8192], 8192, 8000, 8000, 3, 7, "plain"),
     (1, 2, [9000], 9001, 4100, 4097, 4, 100, "ties"), (1, 1, [32768], 32768, 20000, 20000, 0, 0, "plain"),
     (1, 1, [70001], 70005, 33000, 33000, 2, 2, "ties"), (1, 1, [70001], 70005, 69999, 69999, 0, 5, "odd"),
-    (512, 1, [t % 60 for t in range(512)], 60, 31, 30, 2, 8, "plain")]
+    (512, 1, [t % 60 for t in range(512)], 60, 31, 30, 2, 8, "plain"),
+    # both selections either side of where they take turns
+    (3, 2, [5000, 4097, 1], 5000, 4600, 4500, 7, 90, "odd"), (2, 1, [8193, 6000], 8193, 2000, 2000, 1, 0, "equal"),
+    (304, 1, [4100 - 13 * t for t in range(304)], 4100, 2100, 2049, 3, 100, "ties")]
 
 
 @pytest.mark.parametrize("in_place", [False, True])
