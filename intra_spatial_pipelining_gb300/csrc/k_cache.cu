@@ -14,8 +14,9 @@ namespace sgp {
 
 namespace {
 
-// 32 bytes that are read or written once: they leave L2 first.  (Attention weights, 295 MB: 45.6 us
-// so, 51 without; the eviction of 815 MB 137.5 and 140.)
+// 32 bytes that are read or written once: they leave L2 first.  (Attention weights, 295 MB, call
+// after call: 45.6 us so, since a part of K is still in L2 then, 51 without; the eviction of 815 MB
+// 137.5 and 140.)
 __device__ __forceinline__ void load_once(const void* p, uint4& a, uint4& b) {
     asm volatile("ld.global.nc.L1::no_allocate.L2::evict_first.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
@@ -34,9 +35,10 @@ __device__ __forceinline__ void store_once(void* p, const uint4& a, const uint4&
 // from global memory: lane (g, c) loads 32 bytes of rows g and g + 8, and both operands read
 // the same permutation of the dims, so each product still sums matching pairs.  An item is 64
 // positions of one (sequence, KV head); the warps of the grid share the items in equal runs.
-// Bound by HBM: 64 sequences x 64 / 8 heads, up to 8192 positions, 295 MB, 45.6 us (6.5 TB/s, 0.95
-// of a copy's rate; the next item's loads issued beside this one's products made no difference);
-// 3 sequences of up to 577 positions 4.0 us, of which a launch is 2.
+// Bound by HBM: 64 sequences x 64 / 8 heads, up to 8192 positions, 295 MB, 45.6 us call after call
+// and 52.5 with nothing in L2 (5.6 TB/s, 0.83 of a copy's rate; the next item's loads issued beside
+// this one's products made no difference to either); 3 sequences of up to 577 positions 4.0 us, of
+// which a launch is 2.
 // ---------------------------------------------------------------------------------------
 constexpr int kWThreads = 256;
 constexpr int kWPos = 64;
