@@ -283,7 +283,9 @@ typedef struct sgp_prefix {
     int cap;
 } sgp_prefix;
 
-/* Bytes of workspace sgp_prefix_attention needs.  Returns 0 on invalid arguments. */
+/* Bytes of workspace sgp_prefix_attention needs.  They never fall as n_tokens, kv_cap or n_prefixes
+ * grow, so one workspace of a server's largest call serves its smaller ones (same heads).
+ * Returns 0 on invalid arguments. */
 size_t sgp_prefix_attention_workspace_bytes(const sgp_dims* dims, int n_tokens, int kv_cap,
                                             int n_prefixes);
 

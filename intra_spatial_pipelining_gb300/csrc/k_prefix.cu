@@ -455,7 +455,7 @@ __device__ void own_part(const PrefixProblem& P, const Plan& pl, uint8_t* ring_a
             if (n_v < n_k) issue_v();
         }
         if (!ok) break;
-        const size_t at = ((size_t)(cs.t * P.nkv + cs.kvh) * P.S_max + cs.c) * 16;
+        const size_t at = ((size_t)(cs.t * P.nkv + cs.kvh) * P.S_max + cs.c) * P.G;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -904,7 +904,9 @@ __global__ void __launch_bounds__(512) prefix_merge_kernel(const __grid_constant
     const int pair = blockIdx.x, t = pair / P.nkv, kvh = pair - t * P.nkv;
     const PrefixParts q = P.parts[pair];
     const size_t row = (size_t)q.slot * kPrefixRows + q.row + h;
-    const size_t own = ((size_t)pair * P.S_max - q.n_pre) * 16 + h;  // part k >= n_pre at own + 16 k
+    const size_t own = ((size_t)pair * P.S_max - q.n_pre) * P.G + h;  // part k >= n_pre at own + G k
+    const unsigned own_step = P.G * 64;
+    const float *pre_acc = P.pre_acc + row * 64 + 2 * lane, *own_acc = P.own_acc + own * 64 + 2 * lane;
     const int parts = q.n_pre + q.n_own;
     float M = -INFINITY, L = 0.f;
     float2 a = make_float2(0.f, 0.f);
@@ -912,16 +914,16 @@ __global__ void __launch_bounds__(512) prefix_merge_kernel(const __grid_constant
     for (int k0 = 0; k0 < parts; k0 += 32) {
         const int nk = min(32, parts - k0);
         auto acc_of = [&](int k) {
-            const float* p = k < q.n_pre ? P.pre_acc + (row + (size_t)k * kPrefixRows) * 64
-                                         : P.own_acc + (own + (size_t)k * 16) * 64;
-            return __ldcg(reinterpret_cast<const float2*>(p) + lane);
+            const float* p = k < q.n_pre ? pre_acc + (size_t)k * (kPrefixRows * 64)
+                                         : own_acc + (size_t)(unsigned)k * own_step;
+            return __ldcg(reinterpret_cast<const float2*>(p));
         };
         float2 ml = make_float2(-INFINITY, 0.f);
         if (lane < nk) {
             const int k = k0 + lane;
-            const float* p = k < q.n_pre ? P.pre_ml + (row + (size_t)k * kPrefixRows) * 2
-                                         : P.own_ml + (own + (size_t)k * 16) * 2;
-            ml = __ldcg(reinterpret_cast<const float2*>(p));
+            const bool pre = k < q.n_pre;
+            ml = __ldcg(reinterpret_cast<const float2*>(pre ? P.pre_ml + row * 2 : P.own_ml + own * 2) +
+                        (size_t)(unsigned)k * (pre ? (unsigned)kPrefixRows : (unsigned)P.G));
         }
         float2 v[8];
 #pragma unroll

@@ -1,6 +1,7 @@
 // C entry points of the serving operators beside the decode layer: attention over shared
 // prefixes, accumulated attention weights, cache eviction and low-rank adapters.  Argument
 // checks, workspace layout and launches; nothing here keeps state between calls.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -85,10 +86,23 @@ struct PrefixLayout {
 // about four items each (a shorter one costs its partial, 2 KB written and read for 32 KB streamed
 // at 128 positions).  64 sequences x 8 KV heads of up to 1024 positions beside a prefix of 8192:
 // chunks of 1024 left the stream at half its rate.
+constexpr int kOwnLogMin = 7, kOwnLogMax = 10;
+constexpr size_t kOwnItems = 3000;
+
+size_t own_chunks(size_t pairs, int kv_cap, int log2) { return pairs * (size_t)(((kv_cap - 1) >> log2) + 1); }
+
 int own_chunk_log2(size_t pairs, int kv_cap) {
-    int b = 10;
-    while (b > 7 && pairs * (size_t)(((kv_cap - 1) >> b) + 1) < 3000) --b;
+    int b = kOwnLogMax;
+    while (b > kOwnLogMin && own_chunks(pairs, kv_cap, b) < kOwnItems) --b;
     return b;
+}
+
+// Room for the chunks of every call with at most so many pairs and positions.  A smaller call may cut
+// its caches finer, but a chunk is halved only while there are fewer than kOwnItems, which makes fewer
+// than twice as many of them.
+size_t own_slots(size_t pairs, int kv_cap) {
+    return std::max(own_chunks(pairs, kv_cap, kOwnLogMax),
+                    std::min(own_chunks(pairs, kv_cap, kOwnLogMin), 2 * (kOwnItems - 1)));
 }
 
 PrefixLayout prefix_layout(const sgp_dims& d, int T, int kv_cap, int n_prefixes) {
@@ -104,8 +118,10 @@ PrefixLayout prefix_layout(const sgp_dims& d, int T, int kv_cap, int n_prefixes)
         off = al256(off + bytes);
         return o;
     };
-    y.own_ml = take(pairs * y.S_max * 16 * 2 * 4);
-    y.own_acc = take(pairs * y.S_max * 16 * 64 * 4);
+    // (every size below grows with T, kv_cap and n_prefixes, so that a workspace serves smaller calls)
+    const size_t own_rows = own_slots(pairs, kv_cap) * G;
+    y.own_ml = take(own_rows * 2 * 4);
+    y.own_acc = take(own_rows * 64 * 4);
     // slots: one per share and tile; a group has a started tile at most beside its full ones
     const size_t groups = n_prefixes < T ? n_prefixes : T;
     const size_t tiles = d.n_kv_heads * (groups + T / y.tile_seqs);

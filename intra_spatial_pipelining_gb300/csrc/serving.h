@@ -42,8 +42,8 @@ struct PrefixProblem {
     PrefixRef prefix;       // n = 0: none
     float* pre_ml;          // [slot][kPrefixRows][2]  (max, sum)
     float* pre_acc;         // [slot][kPrefixRows][64]
-    float* own_ml;          // [T * nkv][S_max][16][2]
-    float* own_acc;         // [T * nkv][S_max][16][64]
+    float* own_ml;          // [T * nkv][S_max][G][2]
+    float* own_acc;         // [T * nkv][S_max][G][64]
     PrefixParts* parts;     // [T * nkv]
     bf16* o;                // [T][nq * 64]
     float* lse;             // [T][nq] or NULL
