@@ -18,11 +18,11 @@
 #include <cstring>
 #include <mutex>
 #include <string>
-#include <unordered_set>
 #include <vector>
 
 #include "host.h"
 #include "kernels.h"
+#include "once.h"
 #include "sgp.h"
 
 using namespace sgp;
@@ -108,16 +108,11 @@ Driver& drv() {
 }
 
 // Opt every kernel that asks for more than 48 KB of dynamic shared memory into the full
-// 227 KB, for the runtime's launches and (through its CUkernel) for every context.
-int ensure_smem_attr(const void* func, size_t smem) {
-    if (smem <= 48 * 1024) return 0;
-    static std::mutex mu;
-    static std::unordered_set<const void*> done;
-    std::lock_guard<std::mutex> lk(mu);
-    if (done.count(func)) return 0;
+// 227 KB, for the runtime's launches and (through its CUkernel) for every context.  Both
+// settings belong to one device, the current one.
+int set_smem_attr(const void* func, size_t smem, int dev) {
     // the opt-in limit covers static + dynamic shared memory of a block
-    int dev = 0, optin = 0;
-    cudaGetDevice(&dev);
+    int optin = 0;
     cudaError_t e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
     if (e != cudaSuccess) return (int)e;
     cudaFuncAttributes fa;
@@ -134,8 +129,15 @@ int ensure_smem_attr(const void* func, size_t smem) {
             d.kernelSetAttribute(CU_FUNC_ATTRIBUTE_MAX_DYNAMIC_SHARED_SIZE_BYTES, max_smem,
                                  (CUkernel)k, (CUdevice)dev);
     }
-    done.insert(func);
     return 0;
+}
+int ensure_smem_attr(const void* func, size_t smem) {
+    if (smem <= 48 * 1024) return 0;
+    static OncePerDevice once;
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return (int)e;
+    return once.run(dev, func, [&] { return set_smem_attr(func, smem, dev); });
 }
 
 // =======================================================================================
