@@ -299,7 +299,8 @@ size_t sgp_prefix_attention_workspace_bytes(const sgp_dims* dims, int n_tokens, 
  *   kv_len  device int32 [n_tokens], 0 <= kv_len[b] <= kv_cap (out of range: taken as 0)
  *   q, o    device bf16 [n_tokens][n_q d]; o may equal q
  *   lse     device fp32 [n_tokens][n_q] or NULL: log of the sum of exp(q.k / sqrt(d)) (natural)
- * Sums, maxima and lse are fp32; the weights are rounded to bf16 for their product with v.
+ * Sums, maxima and lse are fp32; the weights are rounded to bf16 for their product with v.  Scores
+ * (q.k / sqrt(d)) are below 2^30 in magnitude.
  * A sequence that sees no position gets o = 0 and lse = -inf.  A prefix index past n_prefixes
  * counts as none, a prefix length out of range as 0.  What caches hold behind their lengths, or
  * before every window, is not looked at (it may be NaN).  An infinity or NaN in v at a prefix

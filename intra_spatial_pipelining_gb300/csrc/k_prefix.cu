@@ -794,7 +794,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                         }
                         tmem_st_wait();
                     }
-                    const float2 l_old = l2;
+                    float2 l_old = l2;  // of the halves before, against m
                     for (int tries = 0;; ++tries) {
                         // a row that has seen nothing yet: every score is -inf, every weight 0
                         const float sub = m == -INFINITY ? 0.f : -m;
@@ -824,7 +824,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
                         // the first half also raises from below: its scores may be far under 0
                         const bool far = over > (m == -INFINITY ? -INFINITY : kPRaise) ||
                                          (j == 0 && m == 0.f && over < -kPRaise);
-                        // (scores past 2^26 round by more than that: m is near enough the second time)
+                        // (scaled scores past 2^28 round by more than that: m is near enough the second
+                        // time, and weights up to 2^64 below 2^31)
                         if (!__any_sync(0xffffffffu, far) || tries == 2) {
                             tmem_st_x16(ts + 64 * buf, wa);  // P takes S's place
                             tmem_st_x16(ts + 64 * buf + 16, wb);
@@ -833,7 +834,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
                         const float top = over - sub, nm = j == 0 ? top : fmaxf(m, top);
                         const float c = j == 0 || m == -INFINITY ? 0.f : ex2(m - nm);
                         m = nm;
-                        l2 = make_float2(l_old.x * c, l_old.y * c);
+                        l_old.x *= c;
+                        l_old.y *= c;
+                        l2 = l_old;
                         if (j == 0) continue;
                         if (!(ok = multiplied(25))) break;
                         tc_fence_after();
