@@ -8,6 +8,7 @@
 //             below every number), in their order.
 #include <algorithm>
 
+#include "evict_words.h"
 #include "serving.cuh"
 
 namespace sgp {
@@ -524,11 +525,8 @@ int enqueue_weights(Launcher& L, const WeightsProblem& p, const KCtx& c, int sms
 }
 
 int enqueue_evict(Launcher& L, const EvictProblem& p, const KCtx& c) {
-    // Shared memory for every key up to 49,152 of them, and for the list where it fits beside them
-    // (up to 8192 positions two CTAs to an SM, whatever the list).
-    constexpr int kWords = (227 * 1024 - (int)sizeof(SelectSmem)) / 4;
-    const int n_key = std::min((p.cap + 255) & ~255, 49152), list = (p.budget + 255) & ~255;
-    const int n_list = list <= kWords - n_key ? list : 0;
+    const EvictWords words = evict_words(p.cap, p.budget, (int)sizeof(SelectSmem));
+    const int n_key = words.key, n_list = words.list;
     // The selection for long caches, unless so many (sequence, KV head) pairs are under way that their
     // moves hide it: 32 pairs of 3000 positions 12.8 us without, 13.2 with it; of 6000 24.8 and 22.4;
     // 512 pairs of up to 8192 135.7 and 138.2; 138 of up to 19,764 102 and 94.

@@ -70,3 +70,33 @@ def test_prefix_attention_raises_a_maximum_twice_in_a_step():
         within("o", x.o[t], o, err)
         # the scale, its product with the score, m + log2(sum) and the factor ln 2 round once each
         within("lse", x.lse[t], lse, 5 * S.U32 * np.abs(lse))
+
+
+# ---------------------------------------------------------------------------------------
+# eviction
+# ---------------------------------------------------------------------------------------
+@pytest.mark.parametrize("cap,budget", [(300, 300), (300, 301), (1024, 33000), (9000, 60000), (30000, 40000)])
+def test_kv_evict_budget_past_the_capacity(cap, budget):
+    """A budget that no source cache can exceed: every position stays, the rest of the target is new."""
+    rng = np.random.default_rng(cap)
+    lens = [cap, cap - 1, 0]
+    k, v = bf16(rng, 3, 2, cap, D), bf16(rng, 3, 2, cap, D)
+    acc = torch.from_numpy(rng.random((3, 2, cap))).float().cuda()
+    for t, L in enumerate(lens):
+        k[t, :, L:], v[t, :, L:], acc[t, :, L:] = NAN, NAN, NAN
+    ko, vo = torch.full((2, 3, 2, budget + 1, D), 3.0, dtype=torch.bfloat16, device="cuda")
+    ao = torch.full((3, 2, budget + 1), NAN, device="cuda")
+    dims = sgp.make_heads(2, 2)
+    ws = torch.full((sgp.sgp_kv_evict_workspace_bytes(dims, 3, budget),), 255, dtype=torch.uint8, device="cuda")
+    ws[:64] = 0
+    n, n_out = ints(lens), ints([-1] * 3)
+    kept = torch.full((3, 2, budget), -9, dtype=torch.int32, device="cuda")
+    sgp.sgp_kv_evict(dims, sgp.make_cache(k, v), sgp.make_cache(ko, vo), sgp.make_evict(budget, 2, 9), n, n_out,
+                     acc, ao, kept, 3, ws)
+    assert sgp.sgp_status_from_workspace(ws) == sgp.SGP_OK
+    assert n_out.tolist() == lens
+    for t, L in enumerate(lens):
+        for out, src in ((ko, k), (vo, v)):
+            assert torch.equal(out[t, :, :L], src[t, :, :L]) and (out[t, :, L:] == 3.0).all()
+        assert torch.equal(ao[t, :, :L], acc[t, :, :L]) and not ao[t, :, L:].any()
+        assert (kept[t, :, :L] == torch.arange(L, device="cuda")).all() and (kept[t, :, L:] == -1).all()
