@@ -100,3 +100,30 @@ def test_kv_evict_budget_past_the_capacity(cap, budget):
             assert torch.equal(out[t, :, :L], src[t, :, :L]) and (out[t, :, L:] == 3.0).all()
         assert torch.equal(ao[t, :, :L], acc[t, :, :L]) and not ao[t, :, L:].any()
         assert (kept[t, :, :L] == torch.arange(L, device="cuda")).all() and (kept[t, :, L:] == -1).all()
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("lens,cap,budget", [([300, 129, 40, 0], 310, 128), ([6000, 4500], 6001, 4096),
+                                             ([9000, 64], 9100, 2000)])
+def test_kv_evict_values_behind_a_length_are_nan(lens, cap, budget, in_place):
+    """K, V and the weights behind a length hold NaN: none of it is moved or counted."""
+    T, rng = len(lens), np.random.default_rng(budget)
+    k, v = bf16(rng, T, 2, cap, D), bf16(rng, T, 2, cap, D)
+    acc = torch.from_numpy(rng.exponential(1.0, (T, 2, cap))).float().cuda()
+    for t, L in enumerate(lens):
+        k[t, :, L:], v[t, :, L:], acc[t, :, L:] = NAN, NAN, NAN
+    k0, v0, a0 = k.clone(), v.clone(), acc.cpu().numpy()
+    ko, vo, ao = (k, v, acc) if in_place else (torch.empty_like(k), torch.empty_like(v), torch.empty_like(acc))
+    dims = sgp.make_heads(2, 2)
+    ws = torch.zeros(sgp.sgp_kv_evict_workspace_bytes(dims, T, budget), dtype=torch.uint8, device="cuda")
+    n = ints(lens)
+    sgp.sgp_kv_evict(dims, sgp.make_cache(k, v), sgp.make_cache(ko, vo), sgp.make_evict(budget, 3, 20), n, n, acc,
+                     ao, None, T, ws)
+    assert sgp.sgp_status_from_workspace(ws) == sgp.SGP_OK
+    assert n.tolist() == [min(L, budget) for L in lens]
+    for t, L in enumerate(lens):
+        for j in range(2):
+            at = torch.from_numpy(S.evict(a0[t, j], L, budget, 3, 20)).cuda()
+            m = len(at)
+            assert torch.equal(ko[t, j, :m], k0[t, j, at]) and torch.equal(vo[t, j, :m], v0[t, j, at])
+            assert torch.isfinite(vo[t, j, :m]).all() and not ao[t, j, m:].any()
