@@ -248,11 +248,14 @@ def _rows(t, dev: int, n: int, width: int, what: str):
     return t.data_ptr(), stride[0] if shape[0] > 1 else width
 
 
-def _holds(c, dims, n: int, what: str):
-    """A cache or prefixes of the builders: as many sequences, KV heads and dims as the call reads."""
+def _holds(c, dims, dev: int, n: int, what: str):
+    """A cache or prefixes of the builders: as many sequences, KV heads and dims as the call reads,
+    and on the current device, which may have changed since."""
     t = getattr(c, "tensors", None)
     if t is not None:
         shape = t[0].shape
+        if t[0].get_device() != dev:
+            _bad(t[0], _BF16, dev, n, what)
         if shape[0] < n or shape[1] != dims.n_kv_heads or shape[3] != dims.head_dim:
             raise ValueError(f"{what}: expected [>= {n}][{dims.n_kv_heads}][cap][{dims.head_dim}], "
                              f"got {tuple(shape)}")
@@ -450,9 +453,9 @@ def sgp_prefix_attention(dims, cache: sgp_layer, prefix: Optional[sgp_prefix], k
                          n_tokens: int, workspace, stream=None) -> int:
     dev = _dev()
     rows = n_tokens * dims.n_q_heads
-    _holds(cache, dims, n_tokens, "cache")
+    _holds(cache, dims, dev, n_tokens, "cache")
     if prefix is not None and prefix.n_prefixes > 0:
-        _holds(prefix, dims, prefix.n_prefixes, "prefix")
+        _holds(prefix, dims, dev, prefix.n_prefixes, "prefix")
         t = getattr(prefix, "tensors", None)
         if t is not None and t[3].numel() < n_tokens:
             _bad(t[3], _I32, dev, n_tokens, "prefix_of")
@@ -469,7 +472,7 @@ def sgp_attention_weights(dims, cache: sgp_layer, kv_len, q, lse, acc, n_tokens:
                           stream=None) -> int:
     dev = _dev()
     rows = n_tokens * dims.n_q_heads
-    _holds(cache, dims, n_tokens, "cache")
+    _holds(cache, dims, dev, n_tokens, "cache")
     return check(lib().sgp_attention_weights(
         C.byref(dims), C.byref(cache), _arg(kv_len, _I32, dev, n_tokens, "kv_len"),
         _arg(q, _BF16, dev, rows * dims.head_dim, "q"), _arg(lse, _F32, dev, rows, "lse"),
@@ -486,8 +489,8 @@ def sgp_kv_evict(dims, source: sgp_layer, target: sgp_layer, policy: sgp_evict, 
                  kv_len_out, acc, acc_out, kept, n_tokens: int, workspace, stream=None) -> int:
     dev = _dev()
     pairs = n_tokens * dims.n_kv_heads
-    _holds(source, dims, n_tokens, "source")
-    _holds(target, dims, n_tokens, "target")
+    _holds(source, dims, dev, n_tokens, "source")
+    _holds(target, dims, dev, n_tokens, "target")
     return check(lib().sgp_kv_evict(
         C.byref(dims), C.byref(source), C.byref(target), C.byref(policy),
         _arg(kv_len, _I32, dev, n_tokens, "kv_len"),
@@ -502,6 +505,9 @@ def sgp_kv_evict(dims, source: sgp_layer, target: sgp_layer, policy: sgp_evict, 
 def sgp_lora_apply(lora: sgp_lora, adapter_of, x, y_in, y_out, n_tokens: int, workspace,
                    stream=None) -> int:
     dev = _dev()
+    t = getattr(lora, "tensors", None)
+    if t is not None and t[0].get_device() != dev:
+        _bad(t[0], _BF16, dev, t[0].numel(), "adapters")
     px, ld_x = _rows(x, dev, n_tokens, getattr(lora, "in"), "x")
     pi, ld_i = _rows(y_in, dev, n_tokens, lora.out, "y_in")
     po, ld_o = _rows(y_out, dev, n_tokens, lora.out, "y_out")
