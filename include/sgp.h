@@ -293,7 +293,8 @@ size_t sgp_prefix_attention_workspace_bytes(const sgp_dims* dims, int n_tokens, 
  * sequence b attends to the len[prefix_of[b]] positions of its prefix, then to the kv_len[b]
  * positions of its own cache, which the caller has filled (the current token's included).  A
  * prefix is read once for all its sequences.  With cache->window = W > 0 a sequence sees the
- * last W of its positions, own and prefix counted together.
+ * last W of its positions, own and prefix counted together.  Nothing is rotated here: q and all keys
+ * come with their rotation (sgp_workspace_views, RoPE).
  *   cache   own caches, bf16 [n_tokens][n_kv][kv_cap][d]; read only
  *   prefix  NULL: no sequence has a prefix
  *   kv_len  device int32 [n_tokens], 0 <= kv_len[b] <= kv_cap (out of range: taken as 0)
@@ -342,7 +343,8 @@ size_t sgp_kv_evict_workspace_bytes(const sgp_dims* dims, int n_tokens, int budg
  * order to the front of the target cache, writes the new length min(kv_len, budget), and clears
  * acc_out behind it (a new position starts at 0).  Every KV head keeps the same number, but its
  * own positions.  K and V rows of the target behind the new length are left as they are.  Cached
- * keys keep the rotation they were stored with.
+ * keys keep the rotation they were stored with, and slots are positions no longer: what that means
+ * for a layer that rotates stands at sgp_workspace_views (RoPE).
  *   from, to   caches of n_tokens sequences; `to` may be the same cache (k, v, acc and kv_cap all
  *              the same: in place) or share no byte with `from`; its kv_cap >= budget; k_cache and
  *              v_cache are 32-byte aligned
@@ -397,8 +399,24 @@ int sgp_lora_apply(const sgp_lora* lora, const int32_t* adapter_of, const void* 
  * view->a, q, o, h, u (bf16, as sgp_layer_dump documents them) and sets the other fields to
  * NULL.  With it the operators above take part in a layer run op by op: adapters on q between
  * SGP_OP_QKV and SGP_OP_ATTENTION (without RoPE: q is already rotated there) or on h after
- * SGP_OP_OPROJ, and sgp_prefix_attention in the place of SGP_OP_ATTENTION (q to o).  The
- * workspace's status word is the layer's.  Host only; arguments as sgp_workspace_bytes.
+ * SGP_OP_OPROJ, and sgp_prefix_attention in the place of SGP_OP_ATTENTION (q to o).  (SGP_OP_QKV
+ * writes k and v into the cache itself: adapters on those, or on a fused q/k/v projection, are for
+ * projections that the caller runs.)
+ *
+ * RoPE.  With rope_theta > 0 the layer rotates q and the new key for their cache slot, kv_len - 1.
+ * Only differences of positions count, and nothing checks them:
+ *   - Shared prefixes: own positions follow the prefix but are rotated for 0, 1, ...  So the keys of
+ *     a prefix of `len` positions are stored rotated for p - len (the last one for -1), which puts
+ *     every query at its distance.  Keys rotated for p are at the wrong one.
+ *   - Eviction: kept keys keep the rotation of the position that they had, so slots are positions no
+ *     longer, and the layer's next q and key would be rotated for one that lies before kept keys.
+ *     Run SGP_OP_QKV with rope_theta = 0 in its dims; then rotate view->q and the new row, slot
+ *     kv_len - 1 of k_cache, for the sequence's own count of positions, before the attention.  Keys of
+ *     a prefix may then be rotated for p, and own positions for len, len + 1, ...  A window counts
+ *     slots, not positions.
+ *   - Adapters on q: as after an eviction, between SGP_OP_QKV and the rotation.
+ *
+ * The workspace's status word is the layer's.  Host only; arguments as sgp_workspace_bytes.
  * Returns SGP_OK or SGP_ERR_INVALID_ARG. */
 int sgp_workspace_views(const sgp_dims* dims, int n_tokens, int max_kv_len, void* workspace,
                         size_t ws_bytes, sgp_layer_dump* view);

@@ -1,12 +1,16 @@
 """GPU tests of the serving operators where a call differs from the ordinary one: another call's
 workspace, scores at fp32's end, policies past a cache's capacity, layers that rotate.  Tolerances
 are the bounds of oracle/serving.py unless a test derives its own."""
+import dataclasses
+
 import numpy as np
 import pytest
 import torch
 
-from intra_spatial_pipelining_gb300 import sgp
+from intra_spatial_pipelining_gb300 import sgp, synth
+from oracle import layer as O
 from oracle import serving as S
+from tests import harness as H
 from tests.test_gpu_serving import D, NAN, Prefix, bf16, f64, ints, within
 
 pytestmark = pytest.mark.gpu
@@ -127,3 +131,146 @@ def test_kv_evict_values_behind_a_length_are_nan(lens, cap, budget, in_place):
             m = len(at)
             assert torch.equal(ko[t, j, :m], k0[t, j, at]) and torch.equal(vo[t, j, :m], v0[t, j, at])
             assert torch.isfinite(vo[t, j, :m]).all() and not ao[t, j, m:].any()
+
+
+# ---------------------------------------------------------------------------------------
+# layers that rotate queries and keys, run op by op
+# ---------------------------------------------------------------------------------------
+THETA = 150000.0
+
+
+class RopeLayer:
+    """A layer with 24 sequences on a shared prompt of 333 positions (every sixth without), run op by
+    op with its own rotation (base THETA) or without."""
+
+    def __init__(self, seed, own):
+        self.T, self.P, self.own = 24, 333, own
+        wl = synth.WORKLOADS["gptoss_layer"].with_(n_tokens=self.T, kv_len=max(own) + 4)
+        self.inp = H.make_inputs(wl, seed)
+        self.s = s = wl.shape
+        self.plain = H.dims(s)
+        self.rotating = H.dims(dataclasses.replace(s, rope_theta=THETA))
+        self.nq, self.nkv, self.G = s.n_q_heads, s.n_kv_heads, s.n_q_heads // s.n_kv_heads
+        self.k, self.v = (t.clone() for t in self.inp.caches[0])
+        self.cap = self.k.shape[2]
+        self.layer = sgp.make_layer(self.inp.weights[0], self.k, self.v, 0)
+        self.kv_len = ints(own)
+        rng = np.random.default_rng(seed)
+        # distances matter: keys as large as the layer's own scores allow
+        self.pk_raw = rng.standard_normal((self.nkv, self.P, D))
+        self.pv = bf16(rng, 1, self.nkv, self.P, D)
+        self.of = [-1 if t % 6 == 5 else 0 for t in range(self.T)]
+        self.pof = ints(self.of)
+        self.ws = H.workspace(self.plain, self.T, self.cap)
+        self.view = sgp.layer_views(self.plain, self.T, self.cap, self.ws)
+        n = sgp.sgp_prefix_attention_workspace_bytes(self.plain, self.T, self.cap, 1)
+        self.pws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+        self.lse = torch.empty(self.T, self.nq, device="cuda")
+        self.out = torch.empty_like(self.inp.x)
+
+    def prompt(self, first):
+        """The prompt with its keys rotated for first, first + 1, ..."""
+        k = np.stack([O.rope(self.pk_raw[:, p], first + p, THETA) for p in range(self.P)], 1)
+        self.pk = torch.from_numpy(k)[None].to(torch.bfloat16).cuda()
+        self.prefix = sgp.make_prefix(self.pk, self.pv, ints([self.P]), self.pof)
+
+    def qkv(self, dims):
+        for op in (0, 1):
+            sgp.sgp_layer_op(dims, self.layer, op, self.kv_len, self.inp.x, self.out, self.T, self.ws)
+        return f64(self.view["q"]).reshape(self.T, self.nq, D)
+
+    def attend(self):
+        sgp.sgp_prefix_attention(self.plain, self.layer, self.prefix, self.kv_len,
+                                 self.view["q"].view(self.T, self.nq, D),
+                                 self.view["o"].view(self.T, self.nq, D), self.lse, self.T, self.pws)
+        assert sgp.sgp_status_from_workspace(self.pws) == sgp.SGP_OK
+        assert sgp.sgp_status_from_workspace(self.ws) == sgp.SGP_OK
+
+    def check(self, q, keys):
+        """q[t] [nq][d] and keys(t, j) [n][d] in 64 bits, values as they are stored."""
+        for t in range(self.T):
+            L = int(self.kv_len[t])
+            for j in range(self.nkv):
+                v = f64(self.v[t, j, :L])
+                if self.of[t] >= 0:
+                    v = np.concatenate([f64(self.pv[0, j]), v])
+                h = slice(j * self.G, (j + 1) * self.G)
+                o, lse, eo, el = S.attention(q[t, h], keys(t, j), v, 0)
+                within("o", self.view["o"].view(self.T, self.nq, D)[t, h], o, eo)
+                within("lse", self.lse[t, h], lse, el)
+
+
+def pair_sum(x):
+    """|a| + |b| of every rotated pair, in both of its places."""
+    a = np.abs(x)
+    s = a[..., :D // 2] + a[..., D // 2:]
+    return np.concatenate([s, s], -1)
+
+
+def test_shared_prompt_in_a_layer_that_rotates_by_its_slots():
+    """The layer rotates for its own slots; the prompt's keys are stored for p - len.  Turned by the
+    prompt's length, every vector stands at its true position: the prompt's at 0 ... len - 1, the own
+    ones behind them."""
+    x = RopeLayer(51, [200 - 7 * t for t in range(24)])
+    x.prompt(-x.P)
+    raw = x.qkv(x.plain)                                   # what the projection gives, not rotated
+    for step in range(2):
+        q = x.qkv(x.rotating)
+        for t in range(x.T):
+            # two roundings to bf16 (of a pair's elements before, of the result after); the angle
+            want = O.rope(raw[t], int(x.kv_len[t]) - 1, THETA)
+            bound = S.UBF * (np.abs(want) * (1 + S.UBF) + pair_sum(raw[t]) * (1 + S.UBF)) + 2.0 ** -16 * pair_sum(raw[t])
+            assert (np.abs(q[t] - want) <= bound).all()
+        x.attend()
+        turn = [x.P if g >= 0 else 0 for g in x.of]
+        pk = [np.stack([O.rope(k, x.P, THETA) for k in f64(x.pk[0, j])]) for j in range(x.nkv)]
+        for j in range(x.nkv):                             # the stored prompt, turned: its true rotation
+            want = np.stack([O.rope(x.pk_raw[j, p], p, THETA) for p in range(x.P)])
+            assert (np.abs(pk[j] - want) <= S.UBF * pair_sum(f64(x.pk[0, j])) * (1 + S.UBF) * 2).all()
+
+        def keys(t, j):
+            own = O.rope(f64(x.k[t, j, :int(x.kv_len[t])]), turn[t], THETA)
+            return np.concatenate([pk[j], own]) if x.of[t] >= 0 else own
+        x.check(np.stack([O.rope(q[t], turn[t], THETA) for t in range(x.T)]), keys)
+        x.kv_len += 1
+
+
+def test_eviction_in_a_layer_whose_caller_rotates():
+    """Own caches at positions 0 ... 199 are cut to 96; the layer projects without rotation, and q and
+    the new key are rotated for the positions that the sequences really have, behind the prompt."""
+    n, budget = 200, 96
+    x = RopeLayer(52, [n] * 24)
+    x.prompt(0)
+    start = [x.P if g >= 0 else 0 for g in x.of]           # position of a sequence's first own token
+    rng = np.random.default_rng(9)
+    raw = rng.standard_normal((x.T, x.nkv, n, D))
+    own = np.stack([np.stack([O.rope(raw[t, :, i], start[t] + i, THETA) for i in range(n)], 1) for t in range(x.T)])
+    x.k[:, :, :n] = torch.from_numpy(own).to(torch.bfloat16)
+    acc = torch.from_numpy(rng.exponential(1.0, (x.T, x.nkv, x.cap))).float().cuda()
+    kept = torch.empty(x.T, x.nkv, budget, dtype=torch.int32, device="cuda")
+    ews = torch.zeros(sgp.sgp_kv_evict_workspace_bytes(x.plain, x.T, budget), dtype=torch.uint8, device="cuda")
+    sgp.sgp_kv_evict(x.plain, x.layer, x.layer, sgp.make_evict(budget, 4, 16), x.kv_len, x.kv_len, acc, acc, kept,
+                     x.T, ews)
+    assert sgp.sgp_status_from_workspace(ews) == sgp.SGP_OK
+    stored = [[torch.from_numpy(own[t, j, kept[t, j].cpu().numpy()]).to(torch.bfloat16) for j in range(x.nkv)]
+              for t in range(x.T)]
+    for step in range(2):
+        x.kv_len += 1
+        slot = budget + step
+        q = x.qkv(x.plain)
+        new = f64(x.k[:, :, slot])
+        # the caller's rotation, of the queries and of the row that the projection appended
+        q = np.stack([O.rope(q[t], start[t] + n + step, THETA) for t in range(x.T)])
+        new = np.stack([O.rope(new[t], start[t] + n + step, THETA) for t in range(x.T)])
+        q, new = torch.from_numpy(q).to(torch.bfloat16), torch.from_numpy(new).to(torch.bfloat16)
+        x.view["q"].copy_(q.reshape(x.T, -1))
+        x.k[:, :, slot] = new.cuda()
+        x.attend()
+        for t in range(x.T):
+            for j in range(x.nkv):
+                stored[t][j] = torch.cat([stored[t][j], new[t, j][None]])
+
+        def keys(t, j):
+            k = f64(stored[t][j])
+            return np.concatenate([f64(x.pk[0, j]), k]) if x.of[t] >= 0 else k
+        x.check(f64(q), keys)
