@@ -527,10 +527,13 @@ int enqueue_weights(Launcher& L, const WeightsProblem& p, const KCtx& c, int sms
 int enqueue_evict(Launcher& L, const EvictProblem& p, const KCtx& c) {
     const EvictWords words = evict_words(p.cap, p.budget, (int)sizeof(SelectSmem));
     const int n_key = words.key, n_list = words.list;
-    // The selection for long caches, unless so many (sequence, KV head) pairs are under way that their
-    // moves hide it: 32 pairs of 3000 positions 12.8 us without, 13.2 with it; of 6000 24.8 and 22.4;
-    // 512 pairs of up to 8192 135.7 and 138.2; 138 of up to 19,764 102 and 94.
-    const bool long_ = p.cap > 8192 || (p.cap > 4096 && p.T * p.nkv < 304);
+    // The selection for long caches, by capacity (lengths are on the device).  Without and with it,
+    // half of the positions kept: 32 pairs of (sequence, KV head) of up to 3000 positions 15.7 and
+    // 16.1 us, 4000 18.0 and 18.5, 6000 22.3 and 21.3, 9000 30.2 and 26.4, 30,000 112 and 90.  512 pairs
+    // of 5000 83 and 82.7, 8192 131 and 130, 9000 140 and 142.7, 12,288 193 and 196, 16,384 342 and 340,
+    // 16,384 -> 1000 79 and 70; in place 8192 116 and 110, 16,384 222 and 212.  What it loses most on
+    // are short caches with much room: 512 of 600 positions in 16,384 20.4 and 22.5.
+    const bool long_ = p.cap > 4096;
     void* args[] = {(void*)&p, (void*)&n_key, (void*)&n_list, (void*)&c};
     void* args2[] = {(void*)&p, (void*)&c};
     if (!p.in_place) {

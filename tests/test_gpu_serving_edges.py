@@ -11,6 +11,7 @@ from intra_spatial_pipelining_gb300 import sgp, synth
 from oracle import layer as O
 from oracle import serving as S
 from tests import harness as H
+from tests import test_gpu_serving as base
 from tests.test_gpu_serving import D, NAN, Prefix, bf16, f64, ints, within
 
 pytestmark = pytest.mark.gpu
@@ -131,6 +132,14 @@ def test_kv_evict_values_behind_a_length_are_nan(lens, cap, budget, in_place):
             m = len(at)
             assert torch.equal(ko[t, j, :m], k0[t, j, at]) and torch.equal(vo[t, j, :m], v0[t, j, at])
             assert torch.isfinite(vo[t, j, :m]).all() and not ao[t, j, m:].any()
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("T,nkv,cap", [(2, 1, 4096), (2, 1, 4097), (40, 8, 4096), (40, 8, 4097)])
+def test_kv_evict_where_the_selections_take_turns(T, nkv, cap, in_place):
+    """Capacities on both sides of the border, few and many caches, lengths from none to all of it."""
+    lens = [cap - (t * 611) % (cap + 1) for t in range(T)]
+    base.test_kv_evict(T, nkv, lens, cap, 1000, 900, 3, 50, "ties", in_place)
 
 
 # ---------------------------------------------------------------------------------------
