@@ -143,6 +143,90 @@ def test_kv_evict_where_the_selections_take_turns(T, nkv, cap, in_place):
 
 
 # ---------------------------------------------------------------------------------------
+# padded batches, and the ends of what the arguments may be
+# ---------------------------------------------------------------------------------------
+def test_rows_behind_the_last_sequence_are_left_as_they_were():
+    """Every operator called for 5 sequences on tensors of 8; what lies behind is as it was, and what is
+    only read there is NaN or out of range."""
+    T, N = 5, 8
+    own = [70, 0, 3, 129, 64]
+    x = Prefix(61, N, 16, 2, [200], own + [1, 1, 1], [0, -1, 0, 0, -1, 0, 0, 0])
+    x.q[T:], x.k[T:], x.v[T:] = NAN, NAN, NAN
+    x.kv_len[T:], x.pof[T:] = 1 << 30, 1 << 30
+    x.o.fill_(5.0)
+    x.lse.fill_(5.0)
+    sgp.sgp_prefix_attention(x.dims, x.cache, x.prefix, x.kv_len, x.q, x.o, x.lse, T, x.ws)
+    assert x.status() == sgp.SGP_OK
+    assert (x.o[T:] == 5.0).all() and (x.lse[T:] == 5.0).all()
+    z = lambda t: np.nan_to_num(f64(t))
+    o, lse, eo, el = S.prefix_attention(f64(x.q[:T]), z(x.k[:T]), z(x.v[:T]), own, z(x.pk), z(x.pv), [200],
+                                        x.of[:T], 0)
+    within("o", x.o[:T], o, eo)
+    within("lse", x.lse[:T], lse, el)
+    cap = x.cache.kv_cap
+    acc = torch.full((N, 2, cap), 7.0, device="cuda")
+    sgp.sgp_attention_weights(x.dims, x.cache, x.kv_len, x.q, x.lse, acc, T, x.ws)
+    assert x.status() == sgp.SGP_OK and (acc[T:] == 7.0).all()
+    add, err = S.attention_weights(f64(x.q[:T]), z(x.k[:T]), own, f64(x.lse[:T]))
+    within("acc", acc[:T], 7.0 + add, err + S.U32 * (7.0 + add))
+    ws = torch.zeros(sgp.sgp_kv_evict_workspace_bytes(x.dims, T, 32), dtype=torch.uint8, device="cuda")
+    kept, a0, k0 = torch.full((N, 2, 32), -7, dtype=torch.int32, device="cuda"), f64(acc), x.k.clone()
+    for to in (40, None):                                     # into another cache, then in place
+        ko, vo = (x.k, x.v) if to is None else torch.full((2, N, 2, to, D), 3.0, dtype=torch.bfloat16, device="cuda")
+        ao = acc if to is None else torch.full((N, 2, to), 3.0, device="cuda")
+        behind = [t[T:].clone() for t in (ko, vo, ao, x.kv_len)]
+        n_out = x.kv_len if to is None else torch.full_like(x.kv_len, -3)
+        sgp.sgp_kv_evict(x.dims, x.cache, sgp.make_cache(ko, vo), sgp.make_evict(32, 2, 5), x.kv_len, n_out, acc,
+                         ao, kept, T, ws)
+        assert sgp.sgp_status_from_workspace(ws) == sgp.SGP_OK
+        assert n_out[:T].tolist() == [min(n, 32) for n in own] and (kept[T:] == -7).all()
+        for t, was in zip((ko, vo, ao), behind):
+            assert torch.equal(t[T:].view(torch.uint8), was.view(torch.uint8))
+        assert torch.equal(n_out[T:], behind[3] if to is None else torch.full_like(behind[3], -3))
+        for t in range(T):
+            for j in range(2):
+                want = S.evict(a0[t, j], own[t], 32, 2, 5)
+                assert kept[t, j, :len(want)].tolist() == want.tolist()
+                assert torch.equal(ko[t, j, :len(want)], k0[t, j, torch.from_numpy(want).cuda()])
+    rng = np.random.default_rng(3)
+    a, b, xx, y = bf16(rng, 2, 8, 64), bf16(rng, 2, 96, 8), bf16(rng, N, 64), bf16(rng, N, 96)
+    out, of = torch.full_like(y, 3.0), ints([0, 1, -1, 0, 1, 1 << 30, 0, -9])
+    xx[T:], y[T:] = NAN, NAN
+    sgp.sgp_lora_apply(sgp.make_lora(a, b), of, xx, y, out, T, x.ws)
+    assert x.status() == sgp.SGP_OK and (out[T:] == 3.0).all()
+    want, err = S.lora(f64(xx[:T]), f64(y[:T]), f64(a), f64(b), [1.0] * 2, [8] * 2, of[:T].tolist())
+    within("y", out[:T], want, err)
+
+
+@pytest.mark.parametrize("nq,nkv", [(1024, 1024), (2048, 512), (256, 16)])
+def test_many_heads(nq, nkv):
+    """As many KV heads as there may be, and as many query heads to one."""
+    own = [65, 1, 0]
+    x = Prefix(nq, 3, nq, nkv, [130, 3], own, [0, 1, -1])
+    x.run()
+    x.check()
+    acc = torch.zeros(3, nkv, x.cache.kv_cap, device="cuda")
+    sgp.sgp_attention_weights(x.dims, x.cache, x.kv_len, x.q, x.lse, acc, 3, x.ws)
+    assert x.status() == sgp.SGP_OK
+    add, err = S.attention_weights(f64(x.q), np.nan_to_num(f64(x.k)), own, f64(x.lse))
+    within("acc", acc, add, err + S.U32 * add)
+    assert not acc[1, :, 1:].any() and not acc[2].any()
+
+
+@pytest.mark.parametrize("i,o,r", [(1 << 20, 32, 8), (32, 1 << 20, 8), (65536, 65568, 128)])
+def test_lora_apply_wide(i, o, r):
+    """The widest rows."""
+    rng = np.random.default_rng(r + o)
+    x, y = bf16(rng, 3, i), bf16(rng, 3, o)
+    a, b = bf16(rng, 2, r, i, scale=i ** -0.5), bf16(rng, 2, o, r, scale=r ** -0.5)
+    ws, of = torch.zeros(64, dtype=torch.uint8, device="cuda"), [1, -1, 1]
+    want, err = S.lora(f64(x), f64(y), f64(a), f64(b), [1.0] * 2, [r] * 2, of)
+    sgp.sgp_lora_apply(sgp.make_lora(a, b), ints(of), x, y, y, 3, ws)
+    assert sgp.sgp_status_from_workspace(ws) == sgp.SGP_OK
+    within("y", y, want, err)
+
+
+# ---------------------------------------------------------------------------------------
 # layers that rotate queries and keys, run op by op
 # ---------------------------------------------------------------------------------------
 THETA = 150000.0
