@@ -263,6 +263,7 @@ int sgp_router_topk_noalloc(const sgp_dims* dims, const void* h, const void* g_m
  *     and a stream) need a workspace each; calls ordered on the GPU may share one.
  *   - Device arrays of lengths and indices are checked on the device: what is out of range is
  *     recorded as SGP_ERR_DEVICE_BOUNDS and treated as each entry point says, never followed.
+ *   - Host memory that cannot be had is SGP_ERR_OOM, from any of them.
  *   - Every pointer must be accessible from the current device, and 16-byte aligned where it is to
  *     bf16 data (caches of the weights and the eviction: 32), else 4.
  *   - Of sgp_dims only n_q_heads, n_kv_heads and head_dim are read; of sgp_layer, here a cache,

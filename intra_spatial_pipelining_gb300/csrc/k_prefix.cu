@@ -15,7 +15,7 @@
 // the other leaves idle.
 //
 // Measured (replayed): 64 sequences x 64 / 8 heads on a prefix of 8192 beside own caches of up to
-// 1024, 76 MB and 9.1 GFLOP, 28.5 us (2.7 TB/s); 512 sequences x 8 / 1 heads on 32,768, 34.6 GFLOP,
+// 1024, 76 MB and 9.1 GFLOP, 28.4 us (2.7 TB/s); 512 sequences x 8 / 1 heads on 32,768, 34.6 GFLOP,
 // 53 us (650 TFLOP/s); two sequences on 500 positions 11 us.  Of these about 5.5 us pass before the
 // first product (the plan of the groups 3.2, the query tile 2.4) and 5 us in the merge.
 //
@@ -437,7 +437,7 @@ __device__ void own_part(const PrefixProblem& P, const Plan& pl, uint8_t* ring_a
             for (int ks = 0; ks < 4; ++ks) {
                 uint32_t b0[NT], b1[NT];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
+                for (int nt = 0; nt < NT; ++nt) {  // rounded to bf16, V's type, as for the prefixes
                     b0[nt] = movmatrix_t(pack_bf16x2(s[ks][nt][0], s[ks][nt][1]));
                     b1[nt] = movmatrix_t(pack_bf16x2(s[ks][nt][2], s[ks][nt][3]));
                 }
@@ -521,7 +521,7 @@ __device__ __forceinline__ int halves_of(const Plan& pl, const Step& s, int step
     return (min(pl.len[s.g] - p0, steps * kPrefixKeys) + kPSub - 1) / kPSub;
 }
 
-// The share that holds unit x: the first n_long have q + 1 steps, the others q.
+// The share that holds unit x: the first n_long have q + 1 units, the others q.
 __device__ __forceinline__ int share_of(const Plan& pl, int x) {
     const int r = x - pl.n_long * (pl.q + 1);
     return r < 0 ? x / (pl.q + 1) : pl.n_long + r / pl.q;
@@ -810,7 +810,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
                                 v.x = ex2(v.x);
                                 v.y = ex2(v.y);
                                 l2 = add2(l2, v);
-                                // the weight's rounding to bf16, the second product's operand type
+                                // The weight's rounding to bf16: a product's operands have one
+                                // type, V's.  It makes o's error 1.2 to 1.5 times that of one
+                                // rounding; a second product with the rest would double the
+                                // tensor work and lengthen the softmax, which bounds the kernel.
                                 w[e] = pack_bf16x2(v.x, v.y);
                             }
                         };

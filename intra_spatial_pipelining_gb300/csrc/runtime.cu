@@ -143,12 +143,15 @@ int ensure_smem_attr(const void* func, size_t smem) {
 // =======================================================================================
 // launchers
 // =======================================================================================
-// Every kernel of this library starts with griddepcontrol.launch_dependents and calls
-// griddepcontrol.wait before it touches memory a predecessor wrote (or may still read), so
-// consecutive launches may overlap their launch latency and prologue with the tail of the
-// previous kernel (programmatic dependent launch).  Only launches that declare overlap_ok
-// (the projection kernels and their finishing passes) use it by default: measured on the
-// 36-layer slice, overlapping every kernel is slower than overlapping none.
+// Every kernel of this library calls griddepcontrol.wait before it touches memory a
+// predecessor wrote (or may still read), and the layer's kernels start with
+// griddepcontrol.launch_dependents, so consecutive launches may overlap their launch latency
+// and prologue with the tail of the previous kernel (programmatic dependent launch).  Only
+// launches that declare overlap_ok use it by default: of the layer the projection kernels and
+// their finishing passes (measured on the 36-layer slice, overlapping every kernel is slower
+// than overlapping none), and all serving operators.  Of those only a first kernel with a
+// second one behind it in the same call signals early; what follows an operator starts when
+// its last kernel has ended.
 struct StreamLauncher : Launcher {
     cudaStream_t s;
     bool pdl;
