@@ -180,10 +180,10 @@ __global__ void __launch_bounds__(kWThreads, 2) weights_kernel(const WeightsProb
 // selection runs beside another's copies.  In place the selection is a kernel of its own, because
 // the move overwrites what it reads.
 //
-// Bound by the move: 64 sequences x 8 KV heads, 8192 -> 4096 positions, take 137.5 us for 815 MB
-// (5.9 TB/s), two or three more than the rows 0, 2, 4 ... without a selection: every second 128-byte
-// row of the source does not read at a plain copy's rate.  Four CTAs of 256 threads to an SM took
-// 221 us, one of 1024 146 us.  Two caches of 640 -> 512 take 9.6 us, latency: up to sixteen rounds
+// Bound by the move: 64 sequences x 8 KV heads, 8192 -> 4096 positions, take 135.5 us for 815 MB
+// (6.0 TB/s), within three of the rows 0, 2, 4 ... without a selection: every second 128-byte row of
+// the source does not read at a plain copy's rate.  Four CTAs of 256 threads to an SM took
+// 221 us, one of 1024 146 us.  Two caches of 640 -> 512 take 9.3 us, latency: up to sixteen rounds
 // of counts with a barrier each, then loads of the rows.
 // ---------------------------------------------------------------------------------------
 constexpr int kEThreads = 512;

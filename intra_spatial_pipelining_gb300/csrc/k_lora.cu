@@ -13,8 +13,8 @@
 // bytes, with one adapter x and y are.
 //
 // Bound by the chain of dependent steps, not by bytes: 64 sequences of 24 adapters of rank 64, 4096
-// -> 2880, 16.4 MB, 10.7 us (1.5 TB/s), of which a launch is 2, the list of tiles 2.5, A x 2.5, its
-// join through distributed shared memory 1.5 and the second product 2; one sequence, rank 16, 5.0
+// -> 2880, 16.4 MB, 10.4 us (1.6 TB/s), of which a launch is 2, the list of tiles 2.5, A x 2.5, its
+// join through distributed shared memory 1.5 and the second product 2; one sequence, rank 16, 4.6
 // us.  A cluster to a tile, not a kernel to a product: a second launch costs more than the join.
 #include <algorithm>
 

@@ -15,7 +15,7 @@
 // the other leaves idle.
 //
 // Measured (replayed): 64 sequences x 64 / 8 heads on a prefix of 8192 beside own caches of up to
-// 1024, 76 MB and 9.1 GFLOP, 28.4 us (2.7 TB/s); 512 sequences x 8 / 1 heads on 32,768, 34.6 GFLOP,
+// 1024, 76 MB and 9.1 GFLOP, 27.6 us (2.8 TB/s); 512 sequences x 8 / 1 heads on 32,768, 34.6 GFLOP,
 // 53 us (650 TFLOP/s); two sequences on 500 positions 11 us.  Of these about 5.5 us pass before the
 // first product (the plan of the groups 3.2, the query tile 2.4) and 5 us in the merge.
 //
