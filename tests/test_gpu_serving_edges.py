@@ -48,19 +48,21 @@ def test_prefix_attention_in_the_workspace_of_a_larger_call(nq, nkv, cap, sizes)
                 assert (buf[need:] == 165).all()
 
 
-def test_prefix_attention_raises_a_maximum_twice_in_a_step():
-    """Scaled scores past 2^28, where fp32 steps by 32: the first raise of a row's maximum can miss the
-    scores by more than a weight may exceed it, and the half is done a third time.
+@pytest.mark.parametrize("size", [1, 2, 4])
+def test_prefix_attention_raises_a_maximum_twice_in_a_step(size):
+    """Scaled scores past 2^28, where fp32 steps by 32, and up to the largest that a call may have: the
+    first raise of a row's maximum can miss the scores by more than a weight may exceed it, and the half
+    is done a third time.
 
-    One KV head to a pair (a, d): q = (2^15, 2^7, 0 ...), keys (191 2^8, a) on the first 64 positions
-    and (191 2^8, a + d) on the next, so q.k = 191 2^23 + 128 a, exact in fp32, and 128 d more.  All
-    weight is on the second half, in equal parts: o is the mean of its values.  The equal weights'
-    rounding to bf16 and the result's are one half step each; the sums are of 64 terms."""
+    One KV head to a pair (a, d): q = size (2^15, 2^7, 0 ...), keys (191 2^8, a) on the first 64
+    positions and (191 2^8, a + d) on the next, so q.k = size (191 2^23 + 128 a), exact in fp32, and
+    size 128 d more.  All weight is on the second half, in equal parts: o is the mean of its values.  The
+    equal weights' rounding to bf16 and the result's are one half step each; the sums are of 64 terms."""
     pairs = [(2, 4), (2, 15), (2, 22), (2, 33), (2, 51), (2, 58), (13, 4), (13, 22), (20, 15), (24, 11),
              (24, 43), (6, 29), (17, 36), (20, 58), (0, 1), (100, 7)]
     x = Prefix(41, 3, len(pairs), len(pairs), [128], [0, 0, 0], [0, 0, 0])
     x.q.zero_()
-    x.q[..., 0], x.q[..., 1] = 2.0 ** 15, 2.0 ** 7
+    x.q[..., 0], x.q[..., 1] = size * 2.0 ** 15, size * 2.0 ** 7
     x.pk[0, :, :128] = 0.0
     x.pk[0, :, :128, 0] = 191.0 * 2 ** 8
     for j, (a, d) in enumerate(pairs):
@@ -70,7 +72,7 @@ def test_prefix_attention_raises_a_maximum_twice_in_a_step():
     v = f64(x.pv[0, :, 64:128])
     o, mag = v.mean(1), np.abs(v).mean(1)
     err = S.UBF * mag + S.UBF * np.abs(o) * (1 + S.UBF) + 256 * S.U32 * mag
-    lse = np.array([(191 * 2 ** 23 + 128 * (a + d)) / 8 + np.log(64) for a, d in pairs])
+    lse = np.array([size * (191 * 2 ** 23 + 128 * (a + d)) / 8 + np.log(64) for a, d in pairs])
     for t in range(3):
         within("o", x.o[t], o, err)
         # the scale, its product with the score, m + log2(sum) and the factor ln 2 round once each
