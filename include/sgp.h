@@ -422,6 +422,134 @@ int sgp_lora_apply(const sgp_lora* lora, const int32_t* adapter_of, const void* 
 int sgp_workspace_views(const sgp_dims* dims, int n_tokens, int max_kv_len, void* workspace,
                         size_t ws_bytes, sgp_layer_dump* view);
 
+/* ---- a cache in 8 bits, and what fills it ----------------------------------------------
+ * A cache of 8-bit codes beside a bf16 one that holds a sequence's newest positions (the layer's own
+ * k_cache and v_cache, which then need no more room than a few blocks).  A decode step:
+ * SGP_OP_QKV with rope_theta = 0 writes the new key and value into the bf16 cache,
+ * sgp_qk_rope_append norms and rotates q and that key, sgp_kvq_attention attends to both caches in the
+ * place of SGP_OP_ATTENTION, and sgp_kvq_fold takes full blocks over into the codes (a prompt's cache in
+ * the same way).  What is common to the operators above holds for these (op 20 norms and rotation,
+ * 21 fold, 22 attention), but that the norms and rotation take up to 2^20 tokens. */
+
+/* How positions rotate a head: pairs of its first rot_dim elements by freq[i] radians per position, with
+ * the result times `amplitude`; the other elements are left as they are.  Fill it with sgp_rope_init, or
+ * by hand. */
+enum { SGP_ROPE_HALF = 0, SGP_ROPE_INTERLEAVED = 1 };  /* pairs (i, i + rot_dim / 2), or (2 i, 2 i + 1) */
+enum {
+    SGP_ROPE_PLAIN = 0,     /* f_i = theta^(-2 i / rot_dim)                                           */
+    SGP_ROPE_LINEAR = 1,    /* f_i / factor                                                           */
+    SGP_ROPE_BY_TURNS = 2,  /* f_i (w + (1 - w) / factor), w in [0, 1] rising linearly with the turns
+                               that pair i makes in `context` positions, from turns_low to turns_high */
+    SGP_ROPE_BY_INDEX = 3   /* the same between the same bounds, but linearly with the index i (as a
+                               real number) at which a pair would make so many turns                  */
+};
+typedef struct sgp_rope {
+    int rot_dim;            /* 16, 32, 48 or 64                                             */
+    int layout;             /* SGP_ROPE_HALF or SGP_ROPE_INTERLEAVED                        */
+    float amplitude;
+    double freq[32];        /* the first rot_dim / 2 are read; finite                       */
+} sgp_rope;
+
+/* Fills *rope (its amplitude too).  theta > 1; factor > 0 where scaled; by turns and by index
+ * context > 0 and 0 < turns_low < turns_high (what a scaling does not use is not read).  Host only.
+ * Returns SGP_OK or SGP_ERR_INVALID_ARG. */
+int sgp_rope_init(sgp_rope* rope, int rot_dim, int layout, double theta, int scaling, double factor,
+                  double context, double turns_low, double turns_high, float amplitude);
+
+/* Norms every head of q and k, then rotates it for its token's position:
+ *   x' = x / sqrt(mean(x^2) + eps) * g, then the rotation; sums and products fp32, rounded once.
+ *   g_q, g_k   device bf16 [d] or NULL: that side is not normed; eps >= 0
+ *   pos        device int32 [n_tokens], any value (negative ones too): angles are exact to 2^-25 turns
+ *   q, k       device bf16 rows of n_q d and n_kv d, ld_q and ld_k elements apart (parts of one fused
+ *              projection's rows, for example); one of them may be NULL, with its result
+ *   q_out,k_out  rows for the result, ld_q_out and ld_k_out apart: the input itself (same stride), or
+ *              apart from every input; strides are multiples of 8 elements
+ *   workspace  64 bytes (the status word); any other operator's workspace serves
+ * 1 <= n_tokens <= 2^20.  Returns SGP_OK, SGP_ERR_INVALID_ARG or SGP_ERR_CUDA. */
+int sgp_qk_rope(const sgp_dims* dims, const sgp_rope* rope, const void* g_q, const void* g_k, float eps,
+                const int32_t* pos, const void* q, int64_t ld_q, void* q_out, int64_t ld_q_out,
+                const void* k, int64_t ld_k, void* k_out, int64_t ld_k_out, int n_tokens,
+                void* workspace, size_t ws_bytes, sgp_stream_t stream);
+
+/* The same with keys, and values, that go into a cache: token t's key to k_cache[seq[t]][j][slot[t]] and
+ * its value, as it is, to v_cache there.
+ *   q          rows and result as above, or NULL
+ *   k          rows, or NULL: the key stands in its slot already and is rotated there
+ *   v          rows of n_kv d, ld_v elements apart, or NULL: v_cache is left as it is
+ *   cache      of n_seqs sequences; only k_cache, v_cache (NULL without v) and kv_cap are read
+ *   seq        device int32 [n_tokens] or NULL (t); negative: the token has no slot (only its q is
+ *              rotated)
+ *   slot       device int32 [n_tokens], 0 <= slot[t] < kv_cap; no two tokens have the same place.  A
+ *              sequence or slot out of range is recorded and counts as none
+ * The caches must be apart from every row.  Returns as sgp_qk_rope. */
+int sgp_qk_rope_append(const sgp_dims* dims, const sgp_rope* rope, const void* g_q, const void* g_k,
+                       float eps, const int32_t* pos, const void* q, int64_t ld_q, void* q_out,
+                       int64_t ld_q_out, const void* k, int64_t ld_k, const void* v, int64_t ld_v,
+                       const sgp_layer* cache, int n_seqs, const int32_t* seq, const int32_t* slot,
+                       int n_tokens, void* workspace, size_t ws_bytes, sgp_stream_t stream);
+
+/* A cache in 8 bits (device pointers, caller-owned): a position's element is code * scale, with one scale
+ * for `block` positions of a sequence and KV head.
+ *   k, v              codes [n][n_kv][cap][d], a byte each, 16-byte aligned: e4m3 numbers
+ *                     (SGP_KVQ_E4M3) or two's-complement integers (SGP_KVQ_INT8)
+ *   k_scale, v_scale  fp32 [n][n_kv][cap / block], not negative
+ *   cap               a multiple of block; n * n_kv * cap < 2^31
+ *   block             16, 32, 64 or 128 */
+enum { SGP_KVQ_E4M3 = 0, SGP_KVQ_INT8 = 1 };
+typedef struct sgp_kvq {
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    int cap;
+    int block;
+    int format;
+} sgp_kvq;
+
+/* Takes the full blocks at the front of every sequence's bf16 cache over into its codes, behind those it
+ * has, and moves the positions that are left (fewer than block) to the front of `rest`:
+ *   kv_len_out = kv_len mod block, kvq_len_out = kvq_len + kv_len - kv_len_out.
+ * A block's scale goes by its largest magnitude a (at least 2^-110): for e4m3 the least power of two
+ * with a <= 448 scale; for integers a / 127 in fp32, codes being the fp32 quotients x / scale rounded
+ * to the nearest (halves to even, as for e4m3).  A block with an infinity or a NaN gets NaN for its scale
+ * and codes of 0, which shows in whatever attends to it.
+ *   from       bf16 caches of n_tokens sequences, 32-byte aligned; left as they are unless in place
+ *   rest       the same caches (in place) or others that share no byte with them, with room for
+ *              min(block - 1, from->kv_cap) positions; rows behind those moved are left as they are
+ *   kv_len     device int32 [n_tokens], 0 <= kv_len[b] <= from->kv_cap
+ *   kvq_len    device int32 [n_tokens], a multiple of block, with room for the new blocks behind it
+ *              (where either is out of range the sequence and its lengths are left as they are)
+ *   kv_len_out, kvq_len_out   kv_len and kvq_len themselves (both), or apart from them
+ *   workspace  64 bytes (the status word); any other operator's workspace serves
+ * Only n_kv_heads and head_dim of dims are read.  Returns SGP_OK, SGP_ERR_INVALID_ARG or SGP_ERR_CUDA. */
+int sgp_kvq_fold(const sgp_dims* dims, const sgp_layer* from, const sgp_kvq* to, const sgp_layer* rest,
+                 const int32_t* kv_len, const int32_t* kvq_len, int32_t* kv_len_out,
+                 int32_t* kvq_len_out, int n_tokens, void* workspace, size_t ws_bytes,
+                 sgp_stream_t stream);
+
+/* Bytes of workspace sgp_kvq_attention needs; they never fall as n_tokens grows.  Returns 0 on invalid
+ * arguments. */
+size_t sgp_kvq_attention_workspace_bytes(const sgp_dims* dims, int n_tokens);
+
+/* Decode attention (as SGP_OP_ATTENTION) over a cache in 8 bits and the bf16 positions behind it:
+ * sequence b attends to its kvq_len[b] coded positions, then to the kv_len[b] positions of `cache`.  With
+ * cache->window = W > 0 it sees the last W of both together.  Nothing is rotated here.
+ *   kvq        codes and scales of n_tokens sequences; read only
+ *   kvq_len    device int32 [n_tokens], a multiple of block, 0 <= kvq_len[b] <= kvq->cap
+ *   cache      bf16 caches [n_tokens][n_kv][kv_cap][d], or NULL: no bf16 positions, no window
+ *   kv_len     device int32 [n_tokens], 0 <= kv_len[b] <= kv_cap (not read without cache); where either
+ *              length is out of range the sequence counts as empty
+ *   q, o       device bf16 [n_tokens][n_q d]; o may equal q
+ *   lse        device fp32 [n_tokens][n_q] or NULL, as sgp_prefix_attention writes it
+ * Sums, maxima and lse are fp32; for their product with v the weights, times v's scale, are rounded to
+ * fp16 over coded positions (relative to the largest of them, down to 2^-28 of it) and to bf16 over the
+ * others.  A sequence that sees no position gets o = 0 and lse = -inf.  What caches, codes and scales
+ * hold behind their lengths, or before the window, is not looked at (it may be NaN).
+ * Returns SGP_OK, SGP_ERR_INVALID_ARG or SGP_ERR_CUDA. */
+int sgp_kvq_attention(const sgp_dims* dims, const sgp_kvq* kvq, const int32_t* kvq_len,
+                      const sgp_layer* cache, const int32_t* kv_len, const void* q, void* o, float* lse,
+                      int n_tokens, void* workspace, size_t ws_bytes, sgp_stream_t stream);
+
 /* ---- spatial pipeline (Section 3: cut, binding, SM allocation, microbatches) -------- */
 typedef struct sgp_pipeline sgp_pipeline;
 

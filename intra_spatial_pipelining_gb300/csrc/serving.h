@@ -94,6 +94,72 @@ struct LoraProblem {
     int T, n, in, out, max_rank;
 };
 
+// Norms and rotation of queries and keys (see k_rope.cu); NULL where a part is not wanted.
+struct RopeProblem {
+    unsigned long long turns[32];   // frequency / 2 pi of every pair, in 2^-64 turns per position
+    const int* pos;         // [T]
+    const bf16* q;          // [T] rows, ld_q apart
+    bf16* q_out;
+    const bf16* k;          // [T] rows; NULL with caches: the key stands in its slot
+    bf16* k_out;            // without caches
+    const bf16* v;          // [T] rows that go to the cache as they are
+    const bf16* g_q;        // [64] or NULL: no norm
+    const bf16* g_k;
+    bf16* k_cache;          // [n_seqs][nkv][cap][64] or NULL
+    bf16* v_cache;
+    const int* seq;         // [T] or NULL (t), negative: none
+    const int* slot;        // [T]
+    long long ld_q, ld_q_out, ld_k, ld_k_out, ld_v;
+    int T, nq, nkv, n_seqs, cap, rot, interleaved;
+    float eps, amplitude;
+};
+
+// A cache in 8 bits (see k_kvq.cu).  The attention's tiles are cut into kKvqShares equal shares (or one
+// tile each), one to a warp; the part of pair i ((sequence, KV head)) that share w has worked on is in
+// slot w + i.  Fixed, so that results never depend on the SM count.
+enum { KVQ_E4M3 = 0, KVQ_INT8 = 1 };
+constexpr int kKvqWarps = 12, kKvqCtas = 152, kKvqShares = kKvqWarps * kKvqCtas;
+constexpr float kKvqSmallest = 0x1p-110f;   // a block's largest magnitude counts as at least this
+
+struct KvqProblem {
+    const uint8_t* k;       // [T][nkv][cap][64] codes
+    const uint8_t* v;
+    const float* ks;        // [T][nkv][cap / block]
+    const float* vs;
+    const int* held;        // [T] coded positions
+    const bf16* tk;         // [T][nkv][tail_cap][64]
+    const bf16* tv;
+    const int* kv_len;      // [T] bf16 positions, or NULL: none
+    const bf16* q;          // [T][nq * 64]
+    bf16* o;
+    float* lse;             // [T][nq] or NULL
+    float* ml;              // [slot][G][2]  (max, sum)
+    float* acc;             // [slot][G][64]
+    int2* parts;            // [T * nkv] first slot, slots (1: written already)
+    int T, nq, nkv, G, cap, tail_cap, window, block, block_log2, format;
+    float scale_log2;
+};
+
+struct FoldProblem {
+    const bf16* k;          // [T][nkv][cap][64]
+    const bf16* v;
+    uint8_t* kq;            // [T][nkv][cap_q][64]
+    uint8_t* vq;
+    float* ks;              // [T][nkv][cap_q / block]
+    float* vs;
+    bf16* k_rest;           // [T][nkv][cap_rest][64]
+    bf16* v_rest;
+    const int* kv_len;      // [T]
+    const int* held;
+    int* len_out;
+    int* held_out;
+    int T, nkv, cap, cap_q, cap_rest, block, format;
+    int moved;              // the rest goes to another cache
+};
+
+int enqueue_qk_rope(Launcher& L, const RopeProblem& p, const KCtx& c, int sms);
+int enqueue_kvq_attention(Launcher& L, const KvqProblem& p, const KCtx& c);
+int enqueue_kvq_fold(Launcher& L, const FoldProblem& p, const KCtx& c);
 int enqueue_prefix(Launcher& L, const PrefixProblem& p, const KCtx& c);
 int enqueue_weights(Launcher& L, const WeightsProblem& p, const KCtx& c, int sms);
 int enqueue_evict(Launcher& L, const EvictProblem& p, const KCtx& c);

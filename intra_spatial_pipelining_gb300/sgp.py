@@ -80,6 +80,19 @@ class sgp_lora(C.Structure):
                 ("max_rank", C.c_int)]
 
 
+class sgp_rope(C.Structure):
+    _fields_ = [("rot_dim", C.c_int), ("layout", C.c_int), ("amplitude", C.c_float),
+                ("freq", C.c_double * 32)]
+
+
+class sgp_kvq(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p),
+                ("v_scale", C.c_void_p), ("cap", C.c_int), ("block", C.c_int), ("format", C.c_int)]
+
+
+ROPE_LAYOUTS = ("half", "interleaved")
+ROPE_SCALINGS = ("none", "linear", "turns", "index")
+
 _lib = None
 
 _SIGS = {
@@ -162,6 +175,24 @@ _SIGS["sgp_kv_evict"] = (C.c_int, [C.POINTER(sgp_dims), C.POINTER(sgp_layer),
 _SIGS["sgp_lora_apply"] = (C.c_int, [C.POINTER(sgp_lora), C.c_void_p, C.c_void_p, C.c_int64,
                                      C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int,
                                      C.c_void_p, C.c_size_t, C.c_void_p])
+_SIGS["sgp_rope_init"] = (C.c_int, [C.POINTER(sgp_rope), C.c_int, C.c_int, C.c_double, C.c_int,
+                                    C.c_double, C.c_double, C.c_double, C.c_double, C.c_float])
+_SIGS["sgp_qk_rope"] = (C.c_int, [C.POINTER(sgp_dims), C.POINTER(sgp_rope), C.c_void_p, C.c_void_p,
+                                  C.c_float, C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p,
+                                  C.c_int64, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int,
+                                  C.c_void_p, C.c_size_t, C.c_void_p])
+_SIGS["sgp_qk_rope_append"] = (C.c_int, [C.POINTER(sgp_dims), C.POINTER(sgp_rope), C.c_void_p,
+                                         C.c_void_p, C.c_float, C.c_void_p, C.c_void_p, C.c_int64,
+                                         C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p,
+                                         C.c_int64, C.POINTER(sgp_layer), C.c_int, C.c_void_p,
+                                         C.c_void_p, C.c_int, C.c_void_p, C.c_size_t, C.c_void_p])
+_SIGS["sgp_kvq_fold"] = (C.c_int, [C.POINTER(sgp_dims), C.POINTER(sgp_layer), C.POINTER(sgp_kvq),
+                                   C.POINTER(sgp_layer), C.c_void_p, C.c_void_p, C.c_void_p,
+                                   C.c_void_p, C.c_int, C.c_void_p, C.c_size_t, C.c_void_p])
+_SIGS["sgp_kvq_attention_workspace_bytes"] = (C.c_size_t, [C.POINTER(sgp_dims), C.c_int])
+_SIGS["sgp_kvq_attention"] = (C.c_int, [C.POINTER(sgp_dims), C.POINTER(sgp_kvq), C.c_void_p,
+                                        C.POINTER(sgp_layer), C.c_void_p, C.c_void_p, C.c_void_p,
+                                        C.c_void_p, C.c_int, C.c_void_p, C.c_size_t, C.c_void_p])
 
 ABI_FUNCTIONS = tuple(_SIGS)
 
@@ -336,6 +367,46 @@ def make_lora(a, b, scale=None, rank=None) -> sgp_lora:
                  None if rank is None else _arg(rank, _I32, dev, n, "rank"), n, n_in, b.shape[1], r)
     p.tensors = (a, b, scale, rank)
     return p
+
+
+def make_rope(rot_dim: int = 64, theta: float = 10000.0, layout: str = "half",
+              scaling: str = "none", factor: float = 1.0, context: float = 0.0,
+              turns_low: float = 1.0, turns_high: float = 32.0, amplitude: float = 1.0) -> sgp_rope:
+    """Rotary positions.  layout: "half" or "interleaved"; scaling: "none", "linear", "turns" or
+    "index" (see sgp_rope_init in include/sgp.h)."""
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout: expected one of {ROPE_LAYOUTS}, got {layout!r}")
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling: expected one of {ROPE_SCALINGS}, got {scaling!r}")
+    r = sgp_rope()
+    check(lib().sgp_rope_init(C.byref(r), rot_dim, ROPE_LAYOUTS.index(layout), theta,
+                              ROPE_SCALINGS.index(scaling), factor, context, turns_low, turns_high,
+                              amplitude), "sgp_rope_init")
+    return r
+
+
+def make_kvq(k, v, k_scale, v_scale) -> sgp_kvq:
+    """A cache in 8 bits: codes [n][n_kv][cap][d] of torch.float8_e4m3fn or torch.int8 and their
+    scales [n][n_kv][cap / block].  Keeps the tensors alive."""
+    dev = _dev()
+    if k.dtype is torch.float8_e4m3fn:
+        fmt = 0
+    elif k.dtype is torch.int8:
+        fmt = 1
+    else:
+        raise ValueError(f"codes: expected torch.float8_e4m3fn or torch.int8, got {k.dtype}")
+    if k.dim() != 4 or k.shape != v.shape or k_scale.dim() != 3 or k_scale.shape != v_scale.shape:
+        raise ValueError(f"codes {tuple(k.shape)} and {tuple(v.shape)}, scales {tuple(k_scale.shape)} "
+                         f"and {tuple(v_scale.shape)}: expected [n][n_kv][cap][d] and [n][n_kv][blocks]")
+    cap, blocks = int(k.shape[2]), int(k_scale.shape[2])
+    if k_scale.shape[:2] != k.shape[:2] or blocks < 1 or cap % blocks:
+        raise ValueError(f"scales {tuple(k_scale.shape)} do not cut codes {tuple(k.shape)} into blocks")
+    n, m = k.numel(), k_scale.numel()
+    c = sgp_kvq(_arg(k, k.dtype, dev, n, "k"), _arg(v, k.dtype, dev, n, "v"),
+                _arg(k_scale, _F32, dev, m, "k_scale"), _arg(v_scale, _F32, dev, m, "v_scale"), cap,
+                cap // blocks, fmt)
+    c.tensors = (k, v, k_scale, v_scale)
+    return c
 
 
 def layer_array(layers: Sequence[sgp_layer]):
@@ -515,6 +586,91 @@ def sgp_lora_apply(lora: sgp_lora, adapter_of, x, y_in, y_out, n_tokens: int, wo
         C.byref(lora), _arg(adapter_of, _I32, dev, n_tokens, "adapter_of"), px, ld_x, pi, ld_i, po,
         ld_o, n_tokens, _arg(workspace, _U8, dev, 64, "workspace"), workspace.numel(),
         _on(stream, dev)), "sgp_lora_apply")
+
+
+def sgp_qk_rope(dims, rope: sgp_rope, g_q, g_k, eps: float, pos, q, q_out, k, k_out, n_tokens: int,
+                workspace, stream=None) -> int:
+    dev = _dev()
+    d, wq, wk = dims.head_dim, dims.n_q_heads * dims.head_dim, dims.n_kv_heads * dims.head_dim
+    pq, ld_q = (None, 0) if q is None else _rows(q, dev, n_tokens, wq, "q")
+    po, ld_o = (None, 0) if q_out is None else _rows(q_out, dev, n_tokens, wq, "q_out")
+    pk, ld_k = (None, 0) if k is None else _rows(k, dev, n_tokens, wk, "k")
+    pz, ld_z = (None, 0) if k_out is None else _rows(k_out, dev, n_tokens, wk, "k_out")
+    return check(lib().sgp_qk_rope(
+        C.byref(dims), C.byref(rope), None if g_q is None else _arg(g_q, _BF16, dev, d, "g_q"),
+        None if g_k is None else _arg(g_k, _BF16, dev, d, "g_k"), eps,
+        _arg(pos, _I32, dev, n_tokens, "pos"), pq, ld_q, po, ld_o, pk, ld_k, pz, ld_z, n_tokens,
+        _arg(workspace, _U8, dev, 64, "workspace"), workspace.numel(), _on(stream, dev)),
+        "sgp_qk_rope")
+
+
+def sgp_qk_rope_append(dims, rope: sgp_rope, g_q, g_k, eps: float, pos, q, q_out, k, v,
+                       cache: sgp_layer, n_seqs: int, seq, slot, n_tokens: int, workspace,
+                       stream=None) -> int:
+    dev = _dev()
+    d, wq, wk = dims.head_dim, dims.n_q_heads * dims.head_dim, dims.n_kv_heads * dims.head_dim
+    _holds(cache, dims, dev, n_seqs, "cache")
+    pq, ld_q = (None, 0) if q is None else _rows(q, dev, n_tokens, wq, "q")
+    po, ld_o = (None, 0) if q_out is None else _rows(q_out, dev, n_tokens, wq, "q_out")
+    pk, ld_k = (None, 0) if k is None else _rows(k, dev, n_tokens, wk, "k")
+    pv, ld_v = (None, 0) if v is None else _rows(v, dev, n_tokens, wk, "v")
+    return check(lib().sgp_qk_rope_append(
+        C.byref(dims), C.byref(rope), None if g_q is None else _arg(g_q, _BF16, dev, d, "g_q"),
+        None if g_k is None else _arg(g_k, _BF16, dev, d, "g_k"), eps,
+        _arg(pos, _I32, dev, n_tokens, "pos"), pq, ld_q, po, ld_o, pk, ld_k, pv, ld_v,
+        C.byref(cache), n_seqs, None if seq is None else _arg(seq, _I32, dev, n_tokens, "seq"),
+        _arg(slot, _I32, dev, n_tokens, "slot"), n_tokens,
+        _arg(workspace, _U8, dev, 64, "workspace"), workspace.numel(), _on(stream, dev)),
+        "sgp_qk_rope_append")
+
+
+def _holds_codes(c, dims, dev: int, n: int):
+    """_holds of a cache in 8 bits."""
+    t = getattr(c, "tensors", None)
+    if t is not None:
+        shape = t[0].shape
+        if t[0].get_device() != dev:
+            _bad(t[0], t[0].dtype, dev, n, "codes")
+        if shape[0] < n or shape[1] != dims.n_kv_heads or shape[3] != dims.head_dim:
+            raise ValueError(f"codes: expected [>= {n}][{dims.n_kv_heads}][cap][{dims.head_dim}], "
+                             f"got {tuple(shape)}")
+
+
+def sgp_kvq_fold(dims, source: sgp_layer, target: sgp_kvq, rest: sgp_layer, kv_len, kvq_len,
+                 kv_len_out, kvq_len_out, n_tokens: int, workspace, stream=None) -> int:
+    dev = _dev()
+    _holds(source, dims, dev, n_tokens, "source")
+    _holds_codes(target, dims, dev, n_tokens)
+    _holds(rest, dims, dev, n_tokens, "rest")
+    return check(lib().sgp_kvq_fold(
+        C.byref(dims), C.byref(source), C.byref(target), C.byref(rest),
+        _arg(kv_len, _I32, dev, n_tokens, "kv_len"), _arg(kvq_len, _I32, dev, n_tokens, "kvq_len"),
+        _arg(kv_len_out, _I32, dev, n_tokens, "kv_len_out"),
+        _arg(kvq_len_out, _I32, dev, n_tokens, "kvq_len_out"), n_tokens,
+        _arg(workspace, _U8, dev, 64, "workspace"), workspace.numel(), _on(stream, dev)),
+        "sgp_kvq_fold")
+
+
+def sgp_kvq_attention_workspace_bytes(dims, n_tokens: int) -> int:
+    return int(lib().sgp_kvq_attention_workspace_bytes(C.byref(dims), n_tokens))
+
+
+def sgp_kvq_attention(dims, kvq: sgp_kvq, kvq_len, cache: Optional[sgp_layer], kv_len, q, o, lse,
+                      n_tokens: int, workspace, stream=None) -> int:
+    dev = _dev()
+    rows = n_tokens * dims.n_q_heads
+    _holds_codes(kvq, dims, dev, n_tokens)
+    if cache is not None:
+        _holds(cache, dims, dev, n_tokens, "cache")
+    return check(lib().sgp_kvq_attention(
+        C.byref(dims), C.byref(kvq), _arg(kvq_len, _I32, dev, n_tokens, "kvq_len"),
+        None if cache is None else C.byref(cache),
+        None if cache is None else _arg(kv_len, _I32, dev, n_tokens, "kv_len"),
+        _arg(q, _BF16, dev, rows * dims.head_dim, "q"),
+        _arg(o, _BF16, dev, rows * dims.head_dim, "o"),
+        None if lse is None else _arg(lse, _F32, dev, rows, "lse"), n_tokens,
+        _arg(workspace, _U8, dev, 64, "workspace"), workspace.numel(), _on(stream, dev)),
+        "sgp_kvq_attention")
 
 
 def sgp_status_from_workspace(workspace, stream=None) -> int:
