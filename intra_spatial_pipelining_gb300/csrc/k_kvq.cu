@@ -77,12 +77,25 @@ constexpr int kQTail = 32;                      // bf16 positions of a tile: as 
 constexpr int kQHalf = 4096;                    // K (or V) bytes of a tile
 constexpr int kQStages = 2;
 constexpr int kQMax = 512;                      // sequences
+constexpr int kWholeTiles = 24;
 constexpr float kPShift = 14.f;                 // weights of V are below 2^14: fp16 down to 2^-28 of the largest
 
-struct KvqSmem {
+// n things cut into `parts` runs, the longer ones first.
+struct Cuts {
+    int each, more;                             // `more` runs have one thing more
+    __device__ __forceinline__ Cuts(int n, int parts) : each(n / parts), more(n - n / parts * parts) {}
+    __device__ __forceinline__ int begin(int run) const { return run * each + min(run, more); }
+    __device__ __forceinline__ int of(int i) const {
+        const int edge = more * (each + 1);
+        return i < edge ? i / (each + 1) : more + (i - edge) / max(each, 1);
+    }
+};
+
+struct alignas(16) KvqSmem {
     uint64_t full[kKvqWarps][kQStages];
     int pre[kQMax + 1];                         // tiles before each sequence
     int held[kQMax], len[kQMax];                // lengths, 0 where out of range
+    int sums[kKvqWarps];
 };
 
 // A sequence's tiles for one KV head: coded ones from `q0` on (a multiple of the tile), then the
@@ -116,7 +129,63 @@ struct Place {
     Span s;
 };
 
-template <int NT, int FMT>
+// The joined parts of one query head: maximum, sum, and four dims to a thread of sixteen.
+struct Join {
+    float M = -INFINITY, L = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+
+    // raises the maximum; then takes parts whose maxima are not above it
+    __device__ __forceinline__ void raise(float top) {
+        const float f = ex2(M - (top == -INFINITY ? 0.f : top));
+        M = top;
+        L *= f;
+        a.x *= f;
+        a.y *= f;
+        a.z *= f;
+        a.w *= f;
+    }
+    __device__ __forceinline__ void take(float2 ml, const float4& v) {
+        const float f = ex2(ml.x - (M == -INFINITY ? 0.f : M));
+        L = fmaf(f, ml.y, L);
+        a.x = fmaf(f, v.x, a.x);
+        a.y = fmaf(f, v.y, a.y);
+        a.z = fmaf(f, v.z, a.z);
+        a.w = fmaf(f, v.w, a.w);
+    }
+    // n parts, the rows given by a function of the index (two passes: maxima, then sums)
+    template <typename F>
+    __device__ __forceinline__ void take_all(int n, F row, int sub) {
+        float top = M;
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) top = fmaxf(top, row(k)[64]);
+        raise(top);
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+            const float* r = row(k);
+            take(*reinterpret_cast<const float2*>(r + 64), *reinterpret_cast<const float4*>(r + 4 * sub));
+        }
+    }
+    __device__ __forceinline__ void put(float* r, int sub) const {
+        *reinterpret_cast<float4*>(r + 4 * sub) = a;
+        if (sub == 0) *reinterpret_cast<float2*>(r + 64) = make_float2(M, L);
+    }
+    __device__ __forceinline__ void finish(const KvqProblem& P, size_t at, int sub) const {
+        const float inv = 1.f / L;
+        *reinterpret_cast<uint2*>(P.o + at * 64 + 4 * sub) =
+            make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+        if (P.lse != nullptr && sub == 0) P.lse[at] = (M + log2f(L)) * 0.6931471805599453f;
+    }
+    // a sequence without positions: o = 0, lse = -inf
+    __device__ __forceinline__ void nothing(const KvqProblem& P, size_t at, int sub) const {
+        *reinterpret_cast<uint2*>(P.o + at * 64 + 4 * sub) = make_uint2(0, 0);
+        if (P.lse != nullptr && sub == 0) P.lse[at] = -INFINITY;
+    }
+};
+
+// WHOLE: a CTA to each pair ((sequence, KV head)), whose warps share its tiles and join their parts in
+// shared memory.  Else the tiles of all pairs are cut into equal shares, one to a warp; a part that is not
+// a whole pair goes to the workspace, for kvq_merge_kernel.
+template <int NT, int FMT, bool WHOLE>
 __global__ void __launch_bounds__(kQThreads, 1) kvq_attn_kernel(const __grid_constant__ KvqProblem P, const KCtx ctx) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
@@ -127,60 +196,70 @@ __global__ void __launch_bounds__(kQThreads, 1) kvq_attn_kernel(const __grid_con
     fence_barrier_init();
     griddep_wait();
     task_begin(ctx);
-    for (int t = tid; t < P.T; t += kQThreads) {
-        const int2 l = lengths_of(P, t, ctx, blockIdx.x == 0);
-        S.held[t] = l.x;
-        S.len[t] = l.y;
-    }
-    __syncthreads();
-    if (warp == 0) {
-        int run = 0;
-        for (int t0 = 0; t0 < P.T; t0 += 32) {
-            const int t = t0 + lane;
-            int cnt = 0;
-            if (t < P.T) {
-                const Span s = span_of(S.held[t], S.len[t], P.window);
-                cnt = (s.nq + s.nb) * P.nkv;
-            }
-            int incl = cnt;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += v;
-            }
-            if (t < P.T) S.pre[t] = run + incl - cnt;
-            run += __shfl_sync(0xffffffffu, incl, 31);
+    // This warp's tiles [i0, i1), and the sequence, KV head and tile of the pair that i0 is.  In WHOLE the
+    // tiles are counted from the pair's first.
+    int i0, i1;
+    Place cs;
+    if constexpr (WHOLE) {
+        cs.t = blockIdx.x / P.nkv;
+        cs.kvh = blockIdx.x - cs.t * P.nkv;
+        const int2 l = lengths_of(P, cs.t, ctx, cs.kvh == 0 && tid == 0);
+        if (tid == 0) {
+            S.held[cs.t] = l.x;
+            S.len[cs.t] = l.y;
         }
-        if (lane == 0) S.pre[P.T] = run;
-    }
-    __syncthreads();
-
-    // equal shares of the tiles, at least one each, neighbouring shares on different SMs
-    const int total = S.pre[P.T], shares = min(total, kKvqShares);
-    const int w = warp * kKvqCtas + blockIdx.x;
-    if (w < shares) {
-        const int i0 = (int)((long long)w * total / shares), i1 = (int)((long long)(w + 1) * total / shares);
-        uint8_t* ring = smem + (size_t)warp * kQStages * 2 * kQHalf;
-        uint64_t* full = S.full[warp];
-        const uint64_t pol = policy_evict_first();
-
-        auto enter = [&](Place& x) {            // sequence x.t
-            x.s = span_of(S.held[x.t], S.len[x.t], P.window);
-            x.per = x.s.nq + x.s.nb;
-        };
-        auto next = [&](Place& x) {
-            ++x.i;
-            if (++x.c < x.per) return;
-            x.c = 0;
-            if (++x.kvh < P.nkv) return;
-            x.kvh = 0;
-            if (x.i >= i1) return;
-            do ++x.t;
-            while (S.pre[x.t + 1] <= x.i);
-            enter(x);
-        };
-        Place cs;
-        {
+        cs.s = span_of(l.x, l.y, P.window);
+        cs.per = cs.s.nq + cs.s.nb;
+        const Cuts shares(cs.per, kKvqWarps);
+        i0 = cs.i = cs.c = shares.begin(warp);
+        i1 = shares.begin(warp + 1);
+        __syncthreads();
+    } else {
+        griddep_launch();
+        // tiles before each sequence: two sequences to a thread
+        int cnt[2], sum = 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int t = 2 * tid + k;
+            cnt[k] = 0;
+            if (t < P.T) {
+                const int2 l = lengths_of(P, t, ctx, blockIdx.x == 0);
+                S.held[t] = l.x;
+                S.len[t] = l.y;
+                const Span s = span_of(l.x, l.y, P.window);
+                cnt[k] = (s.nq + s.nb) * P.nkv;
+            }
+            sum += cnt[k];
+        }
+        int incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) S.sums[warp] = incl;
+        __syncthreads();
+        int run = incl - sum;
+        for (int i = 0; i < warp; ++i) run += S.sums[i];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int t = 2 * tid + k;
+            if (t < P.T) {
+                S.pre[t] = run;
+                // a sequence without positions has no parts
+                if (cnt[k] == 0 && blockIdx.x == 0)
+                    for (int j = 0; j < P.nkv; ++j) P.parts[t * P.nkv + j] = make_int2(0, 0);
+            }
+            run += cnt[k];
+            if (t == P.T - 1) S.pre[P.T] = run;
+        }
+        __syncthreads();
+        // neighbouring shares are different SMs'
+        const Cuts shares(S.pre[P.T], kKvqShares);
+        const int w = warp * kKvqCtas + blockIdx.x;
+        i0 = shares.begin(w);
+        i1 = shares.begin(w + 1);
+        if (i0 < i1) {
             int t = 0, hi = P.T;                // largest t with pre[t] <= i0
             while (hi - t > 1) {
                 const int mid = (t + hi) >> 1;
@@ -189,11 +268,30 @@ __global__ void __launch_bounds__(kQThreads, 1) kvq_attn_kernel(const __grid_con
             }
             cs.i = i0;
             cs.t = t;
-            enter(cs);
+            cs.s = span_of(S.held[t], S.len[t], P.window);
+            cs.per = cs.s.nq + cs.s.nb;
             const int r = i0 - S.pre[t];
             cs.kvh = r / cs.per;
             cs.c = r - cs.kvh * cs.per;
         }
+    }
+    if (i0 < i1) {
+        uint8_t* ring = smem + (size_t)warp * kQStages * 2 * kQHalf;
+        uint64_t* full = S.full[warp];
+        const uint64_t pol = policy_evict_first();
+
+        auto next = [&](Place& x) {
+            ++x.i;
+            if (++x.c < x.per || WHOLE) return;
+            x.c = 0;
+            if (++x.kvh < P.nkv) return;
+            x.kvh = 0;
+            if (x.i >= i1) return;
+            do ++x.t;
+            while (S.pre[x.t + 1] <= x.i);
+            x.s = span_of(S.held[x.t], S.len[x.t], P.window);
+            x.per = x.s.nq + x.s.nb;
+        };
         Place ld = cs;
         // Scales of the tiles in flight: lane m holds the key scale of the tile's positions 16 m and
         // up, lane 4 + m the logarithm of their value scale; 1 where no position is visible.
@@ -235,7 +333,25 @@ __global__ void __launch_bounds__(kQThreads, 1) kvq_attn_kernel(const __grid_con
             }
         }
 
-        uint32_t qh[NT][4][2], qb[NT][4][2];    // queries in fp16 (scaled) and in bf16
+        // Queries of a (sequence, KV head): lane (g, c) holds dims 16 c to 16 c + 15 of heads 8 nt + g, as
+        // they are and in fp16, times a power of two.
+        uint32_t qh[NT][4][2], qb[NT][4][2];
+        auto load_q = [&]() {
+            const bf16* qa = P.q + ((size_t)cs.t * P.nq + (size_t)cs.kvh * P.G) * 64 + 16 * cq;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int h = nt * 8 + g;
+                uint4 a = make_uint4(0, 0, 0, 0), b = a;
+                if (h < P.G) {
+                    a = *reinterpret_cast<const uint4*>(qa + h * 64);
+                    b = *reinterpret_cast<const uint4*>(qa + h * 64 + 8);
+                }
+                const uint32_t r[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) qb[nt][e >> 1][e & 1] = r[e];
+            }
+        };
+        load_q();
         float qs[NT][2];                        // factor of a score of heads 2 cq, 2 cq + 1
         float m[NT][2], mv[NT][2], l[NT][2], oacc[4][NT][4];
         bool fresh = true, failed = false;
@@ -243,19 +359,14 @@ __global__ void __launch_bounds__(kQThreads, 1) kvq_attn_kernel(const __grid_con
             const int st = done % kQStages;
             if (fresh) {
                 fresh = false;
-                const bf16* qa = P.q + ((size_t)cs.t * P.nq + (size_t)cs.kvh * P.G) * 64 + 16 * cq;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const int h = nt * 8 + g;
-                    uint4 a = make_uint4(0, 0, 0, 0), b = a;
-                    if (h < P.G) {
-                        a = *reinterpret_cast<const uint4*>(qa + h * 64);
-                        b = *reinterpret_cast<const uint4*>(qa + h * 64 + 8);
-                    }
-                    const uint32_t r[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
                     uint32_t top = 0;           // largest magnitude's bits
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) top = max(top, max(r[e] & 0x7fffu, (r[e] >> 16) & 0x7fffu));
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t x = qb[nt][e >> 1][e & 1];
+                        top = max(top, max(x & 0x7fffu, (x >> 16) & 0x7fffu));
+                    }
                     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
                     // a power of two takes the largest to [2^14, 2^15): fp16 holds bf16's bits down to
@@ -266,8 +377,7 @@ __global__ void __launch_bounds__(kQThreads, 1) kvq_attn_kernel(const __grid_con
                     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const uint32_t x = r[2 * kk + e];
-                            qb[nt][kk][e] = x;
+                            const uint32_t x = qb[nt][kk][e];
                             qh[nt][kk][e] = pack_f16x2(__uint_as_float(x << 16) * up,
                                                        __uint_as_float(x & 0xffff0000u) * up);
                         }
@@ -469,10 +579,12 @@ __global__ void __launch_bounds__(kQThreads, 1) kvq_attn_kernel(const __grid_con
             }
             // ---- end of the pair, or of the share ----
             const bool pair_ends = cs.c == cs.per - 1;
-            if (pair_ends || cs.i == i1 - 1) {
-                const int pair = cs.t * P.nkv + cs.kvh;
-                const int begin = cs.i - cs.c;  // the pair's first tile
-                const bool whole = pair_ends && begin >= i0;
+            if ((!WHOLE && pair_ends) || cs.i == i1 - 1) {
+                const int pair = cs.t * P.nkv + cs.kvh, begin = cs.i - cs.c;
+                const bool all = pair_ends && begin >= i0;
+                const int w = warp * kKvqCtas + blockIdx.x;
+                // WHOLE: into the warp's own stages, where nothing is loaded any more
+                float* rows = WHOLE ? reinterpret_cast<float*>(ring) : P.acc + (size_t)(w + pair) * P.G * kPartRow;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -483,14 +595,14 @@ __global__ void __launch_bounds__(kQThreads, 1) kvq_attn_kernel(const __grid_con
                         if (h >= P.G) continue;
                         const float ref = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
                         // sum of weights (to base m) times V, dims 8 g to 8 g + 7
-                        const float f = ex2(mv[nt][e] - ref - kPShift) * (whole ? 1.f / l[nt][e] : 1.f);
+                        const float f = ex2(mv[nt][e] - ref - kPShift) * (all ? 1.f / l[nt][e] : 1.f);
                         float x[8];
 #pragma unroll
                         for (int md = 0; md < 4; ++md) {
                             x[2 * md] = oacc[md][nt][e] * f;
                             x[2 * md + 1] = oacc[md][nt][2 + e] * f;
                         }
-                        if (whole) {
+                        if (all) {
                             const size_t at = (size_t)cs.t * P.nq + cs.kvh * P.G + h;
                             *reinterpret_cast<uint4*>(P.o + at * 64 + 8 * g) =
                                 make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
@@ -498,109 +610,92 @@ __global__ void __launch_bounds__(kQThreads, 1) kvq_attn_kernel(const __grid_con
                             if (P.lse != nullptr && g == 0)
                                 P.lse[at] = (m[nt][e] + log2f(l[nt][e])) * 0.6931471805599453f;
                         } else {
-                            const size_t row = (size_t)(w + pair) * P.G + h;
-                            float4* dst = reinterpret_cast<float4*>(P.acc + row * 64 + 8 * g);
-                            dst[0] = make_float4(x[0], x[1], x[2], x[3]);
-                            dst[1] = make_float4(x[4], x[5], x[6], x[7]);
-                            if (g == 0) *reinterpret_cast<float2*>(P.ml + row * 2) = make_float2(m[nt][e], l[nt][e]);
+                            float* r = rows + h * kPartRow;
+                            *reinterpret_cast<float4*>(r + 8 * g) = make_float4(x[0], x[1], x[2], x[3]);
+                            *reinterpret_cast<float4*>(r + 8 * g + 4) = make_float4(x[4], x[5], x[6], x[7]);
+                            if (g == 0) *reinterpret_cast<float2*>(r + 64) = make_float2(m[nt][e], l[nt][e]);
                         }
                     }
                 // the share that begins a pair says where its parts are
-                if (begin >= i0 && lane == 0) {
-                    const long long last = ((long long)(begin + cs.per) * shares - 1) / total;
-                    P.parts[pair] = make_int2(w + pair, (int)last - w + 1);
-                }
+                if (!WHOLE && begin >= i0 && lane == 0)
+                    P.parts[pair] = make_int2(w + pair, Cuts(S.pre[P.T], kKvqShares).of(begin + cs.per - 1) - w + 1);
                 fresh = true;
             }
             next(cs);
+            if (!WHOLE && fresh && cs.i < i1) load_q();
         }
         if (failed)                             // loads still in flight
             for (uint32_t n = done; n < issued; ++n)
                 (void)mbar_wait(&full[n % kQStages], (n / kQStages) & 1u, 10000000ull);
     }
-    griddep_launch();
+
+    if constexpr (WHOLE) {
+        __syncthreads();
+        const int n = min(cs.per, kKvqWarps), sub = tid & 15;   // sixteen threads to a head
+        for (int h = tid >> 4; h < P.G; h += kQThreads / 16) {
+            const size_t at = (size_t)cs.t * P.nq + cs.kvh * P.G + h;
+            Join j;
+            if (n > 1) {
+                j.take_all(n, [&](int k) {
+                    return reinterpret_cast<const float*>(smem + (size_t)k * kQStages * 2 * kQHalf) + h * kPartRow;
+                }, sub);
+                j.finish(P, at, sub);
+            } else if (n == 0) {
+                j.nothing(P, at, sub);
+            }
+        }
+    }
     task_end(ctx);
 }
 
-// Joins the parts of the pairs that more than one share has worked on, in the shares' order; `split`
-// warps to a (sequence, query head), lane l holds dims 2l and 2l + 1.
-__global__ void __launch_bounds__(512) kvq_merge_kernel(const __grid_constant__ KvqProblem P, const int split, const KCtx ctx) {
-    __shared__ float part[16][66];
+// Joins the parts of the pairs that more than one share has worked on, in the shares' order: `heads` heads
+// to a CTA, `pieces` groups of sixteen threads to a head.
+__global__ void __launch_bounds__(512) kvq_merge_kernel(const __grid_constant__ KvqProblem P, const int heads, const int pieces, const KCtx ctx) {
+    __shared__ __align__(16) float rows[32][kPartRow];
     griddep_wait();
     task_begin(ctx);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part_of = warp % split;
     const int pair = blockIdx.x, t = pair / P.nkv, kvh = pair - t * P.nkv;
-    const int h = blockIdx.y * (blockDim.x / 32 / split) + warp / split;
-    const int2 len = lengths_of(P, t, ctx, false);
-    const bool none = len.x + len.y == 0;
-    const int2 q = none ? make_int2(0, 0) : P.parts[pair];
-    if (!none && q.y == 1) {                    // written already
+    const int2 q = P.parts[pair];
+    const int group = threadIdx.x >> 4, sub = threadIdx.x & 15, piece = group / heads;
+    const int h = blockIdx.y * heads + group % heads;
+    if (q.y == 1) {                             // written already
         task_end(ctx);
         return;
     }
-    float M = -INFINITY, L = 0.f;
-    float2 a = make_float2(0.f, 0.f);
+    const size_t at = (size_t)t * P.nq + kvh * P.G + h;
+    Join j;
     if (h < P.G) {
-        const int k0 = q.y * part_of / split, k1 = q.y * (part_of + 1) / split;
-        const size_t step = P.G, row = (size_t)q.x * P.G + h;
-        for (int k = k0; k < k1; k += 8) {
-            float2 ml[8], v[8];
+        const float* first = P.acc + ((size_t)q.x * P.G + h) * kPartRow;
+        const unsigned step = P.G * kPartRow;
+        const int k1 = q.y * (piece + 1) / pieces;
+        constexpr int kBatch = 8;
+#pragma unroll 1
+        for (int k = q.y * piece / pieces; k < k1; k += kBatch) {
+            float2 ml[kBatch];
+            float4 v[kBatch];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                ml[i] = make_float2(-INFINITY, 0.f);
-                v[i] = make_float2(0.f, 0.f);
-                if (k + i < k1) {
-                    ml[i] = __ldcg(reinterpret_cast<const float2*>(P.ml + (row + (k + i) * step) * 2));
-                    v[i] = __ldcg(reinterpret_cast<const float2*>(P.acc + (row + (k + i) * step) * 64 + 2 * lane));
-                }
+            for (int i = 0; i < kBatch; ++i) {
+                const float* r = first + (size_t)step * min(k + i, k1 - 1);
+                ml[i] = __ldcg(reinterpret_cast<const float2*>(r + 64));
+                v[i] = __ldcg(reinterpret_cast<const float4*>(r + 4 * sub));
             }
-            float top = M;
+            float top = j.M;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) top = fmaxf(top, ml[i].x);
-            const float sub = top == -INFINITY ? 0.f : top, old = ex2(M - sub);
-            M = top;
-            L *= old;
-            a.x *= old;
-            a.y *= old;
+            for (int i = 0; i < kBatch; ++i) top = fmaxf(top, ml[i].x);
+            j.raise(top);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float wk = ex2(ml[i].x - sub);
-                L = fmaf(wk, ml[i].y, L);
-                a.x = fmaf(wk, v[i].x, a.x);
-                a.y = fmaf(wk, v[i].y, a.y);
-            }
+            for (int i = 0; i < kBatch; ++i)
+                if (k + i < k1) j.take(ml[i], v[i]);
         }
     }
-    if (split > 1) {
-        part[warp][2 * lane] = a.x;
-        part[warp][2 * lane + 1] = a.y;
-        if (lane == 0) {
-            part[warp][64] = M;
-            part[warp][65] = L;
-        }
+    if (pieces > 1) {
+        j.put(rows[group], sub);
         __syncthreads();
-        if (part_of == 0) {
-            float top = M;
-            for (int i = 1; i < split; ++i) top = fmaxf(top, part[warp + i][64]);
-            const float sub = top == -INFINITY ? 0.f : top, old = ex2(M - sub);
-            M = top;
-            L *= old;
-            a.x *= old;
-            a.y *= old;
-            for (int i = 1; i < split; ++i) {
-                const float wk = ex2(part[warp + i][64] - sub);
-                L = fmaf(wk, part[warp + i][65], L);
-                a.x = fmaf(wk, part[warp + i][2 * lane], a.x);
-                a.y = fmaf(wk, part[warp + i][2 * lane + 1], a.y);
-            }
-        }
+        if (piece == 0) j.take_all(pieces - 1, [&](int i) { return &rows[group + (i + 1) * heads][0]; }, sub);
     }
-    if (part_of == 0 && h < P.G) {
-        // a sequence without positions: o = 0, lse = -inf
-        const float inv = none ? 0.f : 1.f / L;
-        const size_t at = (size_t)t * P.nq + kvh * P.G + h;
-        *reinterpret_cast<uint32_t*>(P.o + at * 64 + 2 * lane) = pack_bf16x2(a.x * inv, a.y * inv);
-        if (P.lse != nullptr && lane == 0) P.lse[at] = none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    if (piece == 0 && h < P.G) {
+        if (q.y == 0) j.nothing(P, at, sub);
+        else j.finish(P, at, sub);
     }
     task_end(ctx);
 }
@@ -774,19 +869,23 @@ __global__ void __launch_bounds__(512) kvq_fold_len_kernel(const __grid_constant
 int enqueue_kvq_attention(Launcher& L, const KvqProblem& p, const KCtx& c) {
     const size_t smem = 128 + (size_t)kKvqWarps * kQStages * 2 * kQHalf + sizeof(KvqSmem);
     void* args[] = {(void*)&p, (void*)&c};
-    static const void* const kern[2][2] = {
-        {(const void*)kvq_attn_kernel<1, KVQ_E4M3>, (const void*)kvq_attn_kernel<2, KVQ_E4M3>},
-        {(const void*)kvq_attn_kernel<1, KVQ_INT8>, (const void*)kvq_attn_kernel<2, KVQ_INT8>}};
-    const int e = L.launch(kern[p.format][p.G > 8], dim3(kKvqCtas), dim3(kQThreads), smem, args, true);
-    if (e) return e;
-    // parts of a pair: about kKvqShares / pairs when every sequence is as long
+    // [format][more than 8 heads][whole]
+    static const void* const kern[2][2][2] = {
+        {{(const void*)kvq_attn_kernel<1, KVQ_E4M3, false>, (const void*)kvq_attn_kernel<1, KVQ_E4M3, true>},
+         {(const void*)kvq_attn_kernel<2, KVQ_E4M3, false>, (const void*)kvq_attn_kernel<2, KVQ_E4M3, true>}},
+        {{(const void*)kvq_attn_kernel<1, KVQ_INT8, false>, (const void*)kvq_attn_kernel<1, KVQ_INT8, true>},
+         {(const void*)kvq_attn_kernel<2, KVQ_INT8, false>, (const void*)kvq_attn_kernel<2, KVQ_INT8, true>}}};
+    // A CTA to each pair where none can have more than a few tiles.
     const int pairs = p.T * p.nkv;
-    int split = 1;
-    while (split < 16 && pairs * split * 4 < kKvqShares) split *= 2;
-    int heads = 1;                              // to a CTA
-    while (heads * 2 * split <= 16 && heads < p.G) heads *= 2;
-    void* args2[] = {(void*)&p, (void*)&split, (void*)&c};
-    return L.launch((const void*)kvq_merge_kernel, dim3(pairs, (p.G + heads - 1) / heads), dim3(32 * split * heads), 0, args2, true);
+    const bool whole = pairs <= kKvqCtas && p.cap / kQTile + p.tail_cap / kQTail <= kWholeTiles;
+    const int e = L.launch(kern[p.format][p.G > 8][whole], dim3(whole ? pairs : kKvqCtas), dim3(kQThreads), smem, args, true);
+    if (e || whole) return e;
+    // parts of a pair: about kKvqShares / pairs when every sequence is as long; eight to a group at most
+    int heads = 1, pieces = 1;
+    while (pieces < 32 && pairs * pieces * 8 < kKvqShares) pieces *= 2;
+    while (heads * 2 * pieces <= 16 && heads < p.G) heads *= 2;
+    void* args2[] = {(void*)&p, (void*)&heads, (void*)&pieces, (void*)&c};
+    return L.launch((const void*)kvq_merge_kernel, dim3(pairs, (p.G + heads - 1) / heads), dim3(16 * heads * pieces), 0, args2, true);
 }
 
 int enqueue_kvq_fold(Launcher& L, const FoldProblem& p, const KCtx& c) {

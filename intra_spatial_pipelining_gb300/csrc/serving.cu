@@ -503,18 +503,11 @@ int kvq_fold(const sgp_dims* d, const sgp_layer* from, const sgp_kvq* to, const 
     return launched(enqueue_kvq_fold(L, p, host_ctx(ws, OP_FOLD)), "fold");
 }
 
-struct KvqLayout {
-    size_t parts, ml, acc, total;
-};
+size_t kvq_parts(const sgp_dims& d, int T) { return al256((size_t)T * d.n_kv_heads * sizeof(int2)); }
 
-KvqLayout kvq_layout(const sgp_dims& d, int T) {
-    const size_t pairs = (size_t)T * d.n_kv_heads, rows = (kKvqShares + pairs) * (d.n_q_heads / d.n_kv_heads);
-    KvqLayout y;
-    y.parts = kStatusBytes;
-    y.ml = y.parts + al256(pairs * sizeof(int2));
-    y.acc = y.ml + al256(rows * 2 * 4);
-    y.total = y.acc + al256(rows * 64 * 4);
-    return y;
+size_t kvq_bytes(const sgp_dims& d, int T) {
+    const size_t slots = kKvqShares + (size_t)T * d.n_kv_heads;
+    return kStatusBytes + kvq_parts(d, T) + slots * (d.n_q_heads / d.n_kv_heads) * kPartRow * 4;
 }
 
 int kvq_attention(const sgp_dims* d, const sgp_kvq* kvq, const int32_t* kvq_len, const sgp_layer* cache,
@@ -528,8 +521,7 @@ int kvq_attention(const sgp_dims* d, const sgp_kvq* kvq, const int32_t* kvq_len,
     if (lse && bad4(lse)) return host_fail_arg("lse not aligned");
     const size_t rows = (size_t)T * d->n_q_heads;
     if (q != o && overlap(q, rows * 128, o, rows * 128)) return host_fail_arg("q and o overlap");
-    const KvqLayout y = kvq_layout(*d, T);
-    if ((r = check_workspace(ws, ws_bytes, y.total))) return r;
+    if ((r = check_workspace(ws, ws_bytes, kvq_bytes(*d, T)))) return r;
     uint8_t* w = static_cast<uint8_t*>(ws);
     KvqProblem p;
     memset(&p, 0, sizeof(p));
@@ -548,9 +540,8 @@ int kvq_attention(const sgp_dims* d, const sgp_kvq* kvq, const int32_t* kvq_len,
     p.q = static_cast<const bf16*>(q);
     p.o = static_cast<bf16*>(o);
     p.lse = lse;
-    p.parts = reinterpret_cast<int2*>(w + y.parts);
-    p.ml = reinterpret_cast<float*>(w + y.ml);
-    p.acc = reinterpret_cast<float*>(w + y.acc);
+    p.parts = reinterpret_cast<int2*>(w + kStatusBytes);
+    p.acc = reinterpret_cast<float*>(w + kStatusBytes + kvq_parts(*d, T));
     p.T = T;
     p.nq = d->n_q_heads;
     p.nkv = d->n_kv_heads;
@@ -686,7 +677,7 @@ extern "C" size_t sgp_kvq_attention_workspace_bytes(const sgp_dims* d, int n_tok
     size_t bytes = 0;
     guarded([&] {
         if (check_heads(d, true) == SGP_OK && check_tokens(n_tokens) == SGP_OK)
-            bytes = kvq_layout(*d, n_tokens).total;
+            bytes = kvq_bytes(*d, n_tokens);
         return SGP_OK;
     });
     return bytes;

@@ -114,11 +114,12 @@ struct RopeProblem {
     float eps, amplitude;
 };
 
-// A cache in 8 bits (see k_kvq.cu).  The attention's tiles are cut into kKvqShares equal shares (or one
-// tile each), one to a warp; the part of pair i ((sequence, KV head)) that share w has worked on is in
-// slot w + i.  Fixed, so that results never depend on the SM count.
+// A cache in 8 bits (see k_kvq.cu).  The attention's tiles are cut into kKvqShares equal shares, one to a
+// warp; the part of pair i ((sequence, KV head)) that share w has worked on is in slot w + i.  Fixed, so
+// that results never depend on the SM count.
 enum { KVQ_E4M3 = 0, KVQ_INT8 = 1 };
 constexpr int kKvqWarps = 12, kKvqCtas = 152, kKvqShares = kKvqWarps * kKvqCtas;
+constexpr int kPartRow = 68;            // 64 dims, maximum, sum
 constexpr float kKvqSmallest = 0x1p-110f;   // a block's largest magnitude counts as at least this
 
 struct KvqProblem {
@@ -133,8 +134,7 @@ struct KvqProblem {
     const bf16* q;          // [T][nq * 64]
     bf16* o;
     float* lse;             // [T][nq] or NULL
-    float* ml;              // [slot][G][2]  (max, sum)
-    float* acc;             // [slot][G][64]
+    float* acc;             // [slot][G][kPartRow]
     int2* parts;            // [T * nkv] first slot, slots (1: written already)
     int T, nq, nkv, G, cap, tail_cap, window, block, block_log2, format;
     float scale_log2;
