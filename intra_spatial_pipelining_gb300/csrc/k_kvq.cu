@@ -215,7 +215,6 @@ __global__ void __launch_bounds__(kQThreads, 1) kvq_attn_kernel(const __grid_con
         i1 = shares.begin(warp + 1);
         __syncthreads();
     } else {
-        griddep_launch();
         // tiles before each sequence: two sequences to a thread
         int cnt[2], sum = 0;
 #pragma unroll
@@ -880,9 +879,9 @@ int enqueue_kvq_attention(Launcher& L, const KvqProblem& p, const KCtx& c) {
     const bool whole = pairs <= kKvqCtas && p.cap / kQTile + p.tail_cap / kQTail <= kWholeTiles;
     const int e = L.launch(kern[p.format][p.G > 8][whole], dim3(whole ? pairs : kKvqCtas), dim3(kQThreads), smem, args, true);
     if (e || whole) return e;
-    // parts of a pair: about kKvqShares / pairs when every sequence is as long; eight to a group at most
+    // parts of a pair: about kKvqShares / pairs when every sequence is as long; about four to a group
     int heads = 1, pieces = 1;
-    while (pieces < 32 && pairs * pieces * 8 < kKvqShares) pieces *= 2;
+    while (pieces < 32 && pairs * pieces * 4 < kKvqShares) pieces *= 2;
     while (heads * 2 * pieces <= 16 && heads < p.G) heads *= 2;
     void* args2[] = {(void*)&p, (void*)&heads, (void*)&pieces, (void*)&c};
     return L.launch((const void*)kvq_merge_kernel, dim3(pairs, (p.G + heads - 1) / heads), dim3(16 * heads * pieces), 0, args2, true);
