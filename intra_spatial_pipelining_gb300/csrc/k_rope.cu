@@ -11,143 +11,247 @@ namespace sgp {
 
 namespace {
 
-// Four lanes to a row, a warp to eight rows of one token at a time; a lane holds 16 elements as two
-// 16-byte chunks such that both elements of each of its pairs are its own: frequencies 8 c to 8 c + 7
-// for lane c of the four, in either layout.  Lane i of the warp computes cosine and sine of pair i
-// once for all heads.  The angle is a fraction of a turn in 64-bit fixed point, position times
-// (frequency / 2 pi) modulo 1, exact however far the position.
-constexpr int kRThreads = 256;
-constexpr int kRWarps = kRThreads / 32;
+// A warp takes chunks of at most 32 rows of one token through a ring of its own in shared memory, filled
+// by bulk copies: more is under way than registers would hold.  Four lanes take a row, the warp eight at a
+// time; a lane holds 16 elements as two 16-byte pieces such that both elements of each of its pairs are its
+// own: frequencies 8 c to 8 c + 7 for lane c of the four, in either layout.  Lane i of the warp computes
+// cosine and sine of pair i once for a token.  The angle is a fraction of a turn in 64-bit fixed point,
+// position times (frequency / 2 pi) modulo 1, exact however far the position.
+constexpr int kRWarps = 12;
+constexpr int kRThreads = 32 * kRWarps;
+constexpr int kRRows = 32;                      // rows of a chunk
+constexpr int kRStages = 4;
+constexpr int kRStage = kRRows * 128;
 
-__global__ void __launch_bounds__(kRThreads) qk_rope_kernel(const __grid_constant__ RopeProblem P, const int parts, const KCtx ctx) {
-    __shared__ unsigned long long turns[32];
-    __shared__ __align__(16) float2 trig[kRWarps][32];
+struct RopeSmem {
+    uint64_t full[kRWarps][kRStages];
+    unsigned long long turns[32];
+    float2 trig[kRWarps][32];
+};
+
+// Chunks of a token: of q, of k, of v.
+struct RopeChunks {
+    int q, k, v;
+};
+
+// A warp's chunk.
+struct RopePlace {
+    int left, t, k;                             // chunks left; token, chunk of the token
+};
+
+__global__ void __launch_bounds__(kRThreads, 1) qk_rope_kernel(const __grid_constant__ RopeProblem P, const RopeChunks C, const KCtx ctx) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    RopeSmem& S = *reinterpret_cast<RopeSmem*>(smem + (size_t)kRWarps * kRStages * kRStage);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-    if (tid < 32) turns[tid] = P.turns[tid];
+    if (tid < kRWarps * kRStages) mbar_init(&S.full[0][0] + tid, 1);
+    if (tid < 32) S.turns[tid] = P.turns[tid];
+    fence_barrier_init();
     __syncthreads();
     griddep_wait();
     task_begin(ctx);
-    const long long item = (long long)blockIdx.x * kRWarps + warp;
-    if (item < (long long)P.T * parts) {
-        const int t = (int)(item / parts), part = (int)(item - (long long)t * parts);
-        const int half = P.rot / 2;
-        {
-            const unsigned long long turn = turns[lane] * (unsigned long long)(long long)P.pos[t];
-            float sn, cs;
-            sincospif((float)(int)(turn >> 32) * 0x1p-31f, &sn, &cs);
-            trig[warp][lane] = lane < half ? make_float2(cs * P.amplitude, sn * P.amplitude) : make_float2(1.f, 0.f);
-        }
-        __syncwarp();
-        float2 r[8];
+    // Many tokens go round the warps one by one: what is read and written at a time then lies close
+    // together.  Of fewer the warps take equal runs of chunks.
+    const int per = C.q + C.k + C.v, total = P.T * per, warps = gridDim.x * kRWarps;
+    const int w = warp * gridDim.x + blockIdx.x;
+    const bool round = P.T >= 4 * warps;
+    const int each = total / warps, more = total - each * warps;
+    const int left = round ? (w < P.T ? (P.T - 1 - w) / warps + 1 : 0) * per : each + (w < more);
+    if (left > 0) {
+        uint8_t* ring = smem + (size_t)warp * kRStages * kRStage;
+        uint64_t* full = S.full[warp];
+        auto next = [&](RopePlace& x) {
+            --x.left;
+            if (++x.k == per) {
+                x.k = 0;
+                x.t += round ? warps : 1;
+            }
+        };
+        // A token's row in the caches; negative: it has none.
+        auto place = [&](int t, bool tell) -> long long {
+            const int s = P.seq != nullptr ? P.seq[t] : t, at = P.slot[t];
+            const bool out = s >= P.n_seqs || (s >= 0 && (at < 0 || at >= P.cap));
+            if (out && tell) report(ctx, ST_BOUNDS, (uint32_t)t);
+            return s < 0 || out ? -1 : (long long)s * P.nkv * P.cap + at;
+        };
+        const bool in_place = P.k_cache != nullptr && P.k == nullptr;
+        auto issue = [&](RopePlace& x, int st) {
+            uint8_t* dst = ring + st * kRStage;
+            if (x.k >= C.q && x.k < C.q + C.k && in_place) {
+                const int j = (x.k - C.q) * kRRows + lane;
+                const long long at = place(x.t, false);
+                const bool live = j < P.nkv && at >= 0;
+                const unsigned rows = __popc(__ballot_sync(0xffffffffu, live));
+                if (lane == 0) mbar_arrive_expect_tx(&full[st], rows * 128);
+                __syncwarp();
+                if (live) bulk_load(dst + lane * 128, P.k_cache + (at + (long long)j * P.cap) * 64, 128, &full[st]);
+            } else if (lane == 0) {
+                const bf16* src;
+                int rows, first;
+                if (x.k < C.q) {
+                    first = x.k * kRRows;
+                    rows = P.nq - first;
+                    src = P.q + x.t * P.ld_q;
+                } else {
+                    const bool v = x.k >= C.q + C.k;
+                    first = (x.k - C.q - (v ? C.k : 0)) * kRRows;
+                    rows = P.nkv - first;
+                    src = v ? P.v + x.t * P.ld_v : P.k + x.t * P.ld_k;
+                }
+                const uint32_t bytes = min(rows, kRRows) * 128;
+                mbar_arrive_expect_tx(&full[st], bytes);
+                bulk_load(dst, src + first * 64, bytes, &full[st]);
+            }
+            next(x);
+        };
+        RopePlace cs;
+        cs.left = left;
+        const int first = round ? w * per : w * each + min(w, more);
+        cs.t = first / per;
+        cs.k = first - cs.t * per;
+        RopePlace ld = cs;
+        uint32_t issued = 0, done = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float4 v = *reinterpret_cast<const float4*>(&trig[warp][8 * c + 2 * i]);
-            r[2 * i] = make_float2(v.x, v.y);
-            r[2 * i + 1] = make_float2(v.z, v.w);
-        }
-        // this lane's chunks of 8 elements
+        for (int st = 0; st < kRStages; ++st)
+            if (ld.left > 0) {
+                issue(ld, st);
+                ++issued;
+            }
+        // this lane's two pieces of 8 elements
         int c0 = 2 * c, c1 = 2 * c + 1;
         if (!P.interleaved) {
-            const int n = P.rot / 16;           // lanes with rotated chunks
+            const int n = P.rot / 16;           // lanes with rotated pieces
             c0 = c < n ? c : 2 * n + 2 * (c - n);
             c1 = c < n ? c + n : c0 + 1;
         }
-        // the token's row of the caches
-        bool cached = P.k_cache != nullptr;
-        size_t base = 0, step = 0;
-        if (cached) {
-            const int s = P.seq != nullptr ? P.seq[t] : t, at = P.slot[t];
-            const bool out = s >= P.n_seqs || (s >= 0 && (at < 0 || at >= P.cap));
-            if (out && part == 0 && lane == 0) report(ctx, ST_BOUNDS, (uint32_t)t);
-            cached = s >= 0 && !out;
-            if (cached) {
-                base = ((size_t)s * P.nkv * P.cap + at) * 64;
-                step = (size_t)P.cap * 64;
-            }
-        }
-        const int rows = P.nq + 2 * P.nkv, groups = (rows + 7) / 8;
-        const int g0 = groups * part / parts, g1 = groups * (part + 1) / parts;
-#pragma unroll 2
-        for (int grp = g0; grp < g1; ++grp) {
-            const int row = grp * 8 + g;
-            const bf16 *src = nullptr, *gain = nullptr;
-            bf16* dst = nullptr;
-            bool turned = true;
-            if (row < P.nq) {
-                if (P.q != nullptr) {
-                    src = P.q + t * P.ld_q + row * 64;
-                    dst = P.q_out + t * P.ld_q_out + row * 64;
-                    gain = P.g_q;
+        float2 r[8];
+        long long at = -1;                      // the token's row in the caches
+        int token = -1, st = 0, parity = 0;
+        bool failed = false;
+        while (cs.left > 0) {
+            if (cs.t != token) {
+                token = cs.t;
+                const int pos = P.pos[token];
+                if (P.k_cache != nullptr) at = place(token, lane == 0);
+                const unsigned long long turn = S.turns[lane] * (unsigned long long)(long long)pos;
+                float sn, cn;
+                sincospif((float)(int)(turn >> 32) * 0x1p-31f, &sn, &cn);
+                __syncwarp();
+                S.trig[warp][lane] = lane < P.rot / 2 ? make_float2(cn * P.amplitude, sn * P.amplitude) : make_float2(1.f, 0.f);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 v = *reinterpret_cast<const float4*>(&S.trig[warp][8 * c + 2 * i]);
+                    r[2 * i] = make_float2(v.x, v.y);
+                    r[2 * i + 1] = make_float2(v.z, v.w);
                 }
-            } else if (row < P.nq + P.nkv) {
-                const int j = row - P.nq;
+            }
+            // where the chunk goes
+            const bf16* gain = P.g_q;
+            bf16* dst;
+            long long step = 64;
+            int rows;
+            bool turned = true, kept = true;
+            if (cs.k < C.q) {
+                const int first = cs.k * kRRows;
+                rows = P.nq - first;
+                dst = P.q_out + token * P.ld_q_out + first * 64;
+            } else {
+                turned = cs.k < C.q + C.k;
+                const int first = (cs.k - C.q - (turned ? 0 : C.k)) * kRRows;
+                rows = P.nkv - first;
                 gain = P.g_k;
-                if (P.k_cache == nullptr) {
-                    if (P.k != nullptr) {
-                        src = P.k + t * P.ld_k + j * 64;
-                        dst = P.k_out + t * P.ld_k_out + j * 64;
-                    }
-                } else if (cached) {
-                    dst = P.k_cache + base + j * step;
-                    src = P.k != nullptr ? P.k + t * P.ld_k + j * 64 : dst;
-                }
-            } else if (row < rows && cached && P.v != nullptr) {
-                const int j = row - P.nq - P.nkv;
-                src = P.v + t * P.ld_v + j * 64;
-                dst = P.v_cache + base + j * step;
-                turned = false;
-            }
-            uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
-            if (src != nullptr) {
-                x0 = *reinterpret_cast<const uint4*>(src + 8 * c0);
-                x1 = *reinterpret_cast<const uint4*>(src + 8 * c1);
-            }
-            float a[8], b[8];
-            unpack8(x0, a);
-            unpack8(x1, b);
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(a[i], a[i], fmaf(b[i], b[i], ss));
-            ss += __shfl_xor_sync(0xffffffffu, ss, 1);
-            ss += __shfl_xor_sync(0xffffffffu, ss, 2);
-            if (src == nullptr) continue;
-            if (turned) {
-                if (gain != nullptr) {
-                    const float inv = rsqrtf(fmaf(ss, 1.f / 64.f, P.eps));
-                    float ga[8], gb[8];
-                    unpack8(*reinterpret_cast<const uint4*>(gain + 8 * c0), ga);
-                    unpack8(*reinterpret_cast<const uint4*>(gain + 8 * c1), gb);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        a[i] *= inv * ga[i];
-                        b[i] *= inv * gb[i];
-                    }
-                }
-                if (P.interleaved) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float u = a[2 * i], v = a[2 * i + 1], y = b[2 * i], z = b[2 * i + 1];
-                        a[2 * i] = u * r[i].x - v * r[i].y;
-                        a[2 * i + 1] = v * r[i].x + u * r[i].y;
-                        b[2 * i] = y * r[4 + i].x - z * r[4 + i].y;
-                        b[2 * i + 1] = z * r[4 + i].x + y * r[4 + i].y;
-                    }
+                if (P.k_cache != nullptr) {
+                    kept = at >= 0;
+                    step = (long long)P.cap * 64;
+                    dst = (turned ? P.k_cache : P.v_cache) + at * 64 + first * step;
                 } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float u = a[i], v = b[i];
-                        a[i] = u * r[i].x - v * r[i].y;
-                        b[i] = v * r[i].x + u * r[i].y;
-                    }
+                    dst = P.k_out + token * P.ld_k_out + first * 64;
                 }
-                x0 = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]),
-                                pack_bf16x2(a[6], a[7]));
-                x1 = make_uint4(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]), pack_bf16x2(b[4], b[5]),
-                                pack_bf16x2(b[6], b[7]));
             }
-            *reinterpret_cast<uint4*>(dst + 8 * c0) = x0;
-            *reinterpret_cast<uint4*>(dst + 8 * c1) = x1;
+            rows = min(rows, kRRows);
+            const bool ok = mbar_wait(&full[st], parity, ctx.timeout_ns);
+            if (__any_sync(0xffffffffu, !ok)) {
+                if (lane == 0) report(ctx, ST_TIMEOUT, 30);
+                failed = true;
+                break;
+            }
+            if (kept) {
+                const uint8_t* row = ring + st * kRStage + g * 128;
+                dst += g * step;
+                uint4 gain0, gain1;
+                if (turned && gain != nullptr) {
+                    gain0 = *reinterpret_cast<const uint4*>(gain + c0 * 8);
+                    gain1 = *reinterpret_cast<const uint4*>(gain + c1 * 8);
+                }
+#pragma unroll 1
+                for (int j = g; j - g < rows; j += 8) {
+                    uint4 x0 = *reinterpret_cast<const uint4*>(row + c0 * 16), x1 = *reinterpret_cast<const uint4*>(row + c1 * 16);
+                    row += 1024;
+                    if (turned) {
+                        float a[8], b[8];
+                        unpack8(x0, a);
+                        unpack8(x1, b);
+                        if (gain != nullptr) {
+                            float ss = 0.f;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) ss = fmaf(a[i], a[i], fmaf(b[i], b[i], ss));
+                            ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+                            ss += __shfl_xor_sync(0xffffffffu, ss, 2);
+                            const float inv = rsqrtf(fmaf(ss, 1.f / 64.f, P.eps));
+                            float ga[8], gb[8];
+                            unpack8(gain0, ga);
+                            unpack8(gain1, gb);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                a[i] *= inv * ga[i];
+                                b[i] *= inv * gb[i];
+                            }
+                        }
+                        if (P.interleaved) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float u = a[2 * i], v = a[2 * i + 1], y = b[2 * i], z = b[2 * i + 1];
+                                a[2 * i] = u * r[i].x - v * r[i].y;
+                                a[2 * i + 1] = v * r[i].x + u * r[i].y;
+                                b[2 * i] = y * r[4 + i].x - z * r[4 + i].y;
+                                b[2 * i + 1] = z * r[4 + i].x + y * r[4 + i].y;
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float u = a[i], v = b[i];
+                                a[i] = u * r[i].x - v * r[i].y;
+                                b[i] = v * r[i].x + u * r[i].y;
+                            }
+                        }
+                        x0 = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]),
+                                        pack_bf16x2(a[6], a[7]));
+                        x1 = make_uint4(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]), pack_bf16x2(b[4], b[5]),
+                                        pack_bf16x2(b[6], b[7]));
+                    }
+                    if (j < rows) {
+                        *reinterpret_cast<uint4*>(dst + c0 * 8) = x0;
+                        *reinterpret_cast<uint4*>(dst + c1 * 8) = x1;
+                    }
+                    dst += 8 * step;
+                }
+            }
+            ++done;
+            fence_proxy_async();
+            __syncwarp();
+            if (ld.left > 0) {
+                issue(ld, st);
+                ++issued;
+            }
+            if (++st == kRStages) {
+                st = 0;
+                parity ^= 1;
+            }
+            next(cs);
         }
+        if (failed)                             // loads still in flight
+            for (uint32_t n = done; n < issued; ++n)
+                (void)mbar_wait(&full[n % kRStages], (n / kRStages) & 1u, 10000000ull);
     }
     task_end(ctx);
 }
@@ -155,13 +259,15 @@ __global__ void __launch_bounds__(kRThreads) qk_rope_kernel(const __grid_constan
 }  // namespace
 
 int enqueue_qk_rope(Launcher& L, const RopeProblem& p, const KCtx& c, int sms) {
-    // warps to a token: one, or enough of them to give every SM sixteen
-    const int groups = (p.nq + 2 * p.nkv + 7) / 8;
-    int parts = (16 * sms + p.T - 1) / p.T;
-    if (parts > groups) parts = groups;
-    const long long warps = (long long)p.T * parts;
-    void* args[] = {(void*)&p, (void*)&parts, (void*)&c};
-    return L.launch((const void*)qk_rope_kernel, dim3((unsigned)((warps + kRWarps - 1) / kRWarps)), dim3(kRThreads), 0, args, true);
+    const int chunks = (p.nkv + kRRows - 1) / kRRows;
+    RopeChunks C;
+    C.q = p.q != nullptr ? (p.nq + kRRows - 1) / kRRows : 0;
+    C.k = p.k != nullptr || p.k_cache != nullptr ? chunks : 0;
+    C.v = p.v != nullptr ? chunks : 0;
+    const int total = p.T * (C.q + C.k + C.v);
+    const size_t smem = (size_t)kRWarps * kRStages * kRStage + sizeof(RopeSmem);
+    void* args[] = {(void*)&p, (void*)&C, (void*)&c};
+    return L.launch((const void*)qk_rope_kernel, dim3(total < sms ? total : sms), dim3(kRThreads), smem, args, true);
 }
 
 }  // namespace sgp
