@@ -58,6 +58,12 @@ __device__ __forceinline__ float lg2(float x) {
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// NaN if one of them is
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
 // two fp32 operations in one instruction
@@ -97,6 +103,7 @@ constexpr int kQTail = 32;                      // bf16 positions of a tile: as 
 constexpr int kQHalf = 4096;                    // K (or V) bytes of a tile
 constexpr int kQStages = 2;
 constexpr int kQMax = 512;                      // sequences
+static_assert(2 * kQThreads >= kQMax, "the plan takes two sequences to a thread");
 constexpr int kWholeTiles = 24;
 constexpr float kPShift = 14.f;                 // weights of V are below 2^14: fp16 down to 2^-28 of the largest
 
@@ -204,8 +211,10 @@ struct Join {
 
 // WHOLE: a CTA to each pair ((sequence, KV head)), whose warps share its tiles and join their parts in
 // shared memory.  Else the tiles of all pairs are cut into equal shares, one to a warp; a part that is not
-// a whole pair goes to the workspace, for kvq_merge_kernel.
-template <int NT, int FMT, bool WHOLE>
+// a whole pair goes to the workspace, for kvq_merge_kernel.  ALIKE: a tile has one scale (blocks of 64 and
+// more); no branch in the loop, which the compiler would not interleave what is around it with (512
+// sequences of up to 32,768 positions, int8: 160.3 us, 175.6 with the branch, 165.9 without the case).
+template <int NT, int FMT, bool WHOLE, bool ALIKE>
 __global__ void __launch_bounds__(kQThreads, 1) kvq_attn_kernel(const __grid_constant__ KvqProblem P, const KCtx ctx) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
@@ -446,6 +455,8 @@ __global__ void __launch_bounds__(kQThreads, 1) kvq_attn_kernel(const __grid_con
             // ---- S^T = K q^T ----
             if (coded) {
                 const float own = lane < 4 ? sc[0] : lg2(sc[0]);
+                // a lane with a visible position's scale
+                const int one = min(lo >> 4, 3);
 #pragma unroll
                 for (int mt = 0; mt < 4; ++mt) {
                     const uint4 k0 = *reinterpret_cast<const uint4*>(kt + (mt * 16 + rho) * 64 + cq * 16);
@@ -459,12 +470,28 @@ __global__ void __launch_bounds__(kQThreads, 1) kvq_attn_kernel(const __grid_con
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) mma16816_f16(s[mt][nt], a, qh[nt][kk][0], qh[nt][kk][1]);
                     }
-                    const float ksc = __shfl_sync(0xffffffffu, own, mt);
-                    lsv[mt] = __shfl_sync(0xffffffffu, own, 4 + mt);
+                }
+                if constexpr (ALIKE) {
+                    const float ksc = __shfl_sync(0xffffffffu, own, one);
+                    lsv[0] = __shfl_sync(0xffffffffu, own, 4 + one);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float f[2] = {qs[nt][0] * ksc, qs[nt][1] * ksc};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) s[mt][nt][e] *= qs[nt][e & 1] * ksc;
+                        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) s[mt][nt][e] *= f[e & 1];
+                    }
+                } else {
+#pragma unroll
+                    for (int mt = 0; mt < 4; ++mt) {
+                        const float ksc = __shfl_sync(0xffffffffu, own, mt);
+                        lsv[mt] = __shfl_sync(0xffffffffu, own, 4 + mt);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) s[mt][nt][e] *= qs[nt][e & 1] * ksc;
+                    }
                 }
             } else {
 #pragma unroll
@@ -490,7 +517,7 @@ __global__ void __launch_bounds__(kQThreads, 1) kvq_attn_kernel(const __grid_con
             uint32_t pk[4][NT][2];              // weights, [position half]
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float mx[2] = {-INFINITY, -INFINITY}, mw[2] = {-INFINITY, -INFINITY};
+                float top[4][2];                // maxima of 16 positions, of this lane's
 #pragma unroll
                 for (int mt = 0; mt < 4; ++mt) {
 #pragma unroll
@@ -500,35 +527,43 @@ __global__ void __launch_bounds__(kQThreads, 1) kvq_attn_kernel(const __grid_con
                             s[mt][nt][2 * hf] = s[mt][nt][2 * hf + 1] = -INFINITY;
                     }
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float top = fmaxf(s[mt][nt][e], s[mt][nt][2 + e]);
-                        mx[e] = fmaxf(mx[e], top);
-                        mw[e] = fmaxf(mw[e], top + lsv[mt]);
-                    }
+                    for (int e = 0; e < 2; ++e) top[mt][e] = fmaxf(s[mt][nt][e], s[mt][nt][2 + e]);
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
+                    float mx = fmaxf(fmaxf(top[0][e], top[1][e]), fmaxf(top[2][e], top[3][e])), mw;
+                    if constexpr (!ALIKE)
+                        mw = fmaxf(fmaxf(top[0][e] + lsv[0], top[1][e] + lsv[1]), fmaxf(top[2][e] + lsv[2], top[3][e] + lsv[3]));
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) {
-                        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], o));
-                        mw[e] = fmaxf(mw[e], __shfl_xor_sync(0xffffffffu, mw[e], o));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                        if constexpr (!ALIKE) mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, o));
                     }
-                    const float n = fmaxf(m[nt][e], mx[e]), nv = fmaxf(mv[nt][e], mw[e]);
+                    if constexpr (ALIKE) mw = mx + lsv[0];
+                    const float n = fmaxf(m[nt][e], mx), nv = fmaxf(mv[nt][e], mw);
                     const float sub = n == -INFINITY ? 0.f : n, subv = nv == -INFINITY ? 0.f : nv;
                     const float c = ex2(m[nt][e] - sub), cv = ex2(mv[nt][e] - subv);
                     m[nt][e] = n;
                     mv[nt][e] = nv;
+                    // a weight of V is the weight to base m times f (value scales more than 2^112 apart are
+                    // not told apart)
+                    const float to = sub - subv + kPShift;
+                    float f[4];
+                    if constexpr (ALIKE) {
+                        f[0] = f[1] = f[2] = f[3] = ex2(min_nan(lsv[0] + to, 126.f));
+                    } else {
+#pragma unroll
+                        for (int mt = 0; mt < 4; ++mt) f[mt] = ex2(min_nan(lsv[mt] + to, 126.f));
+                    }
                     float sum = 0.f;
 #pragma unroll
-                    for (int mt = 0; mt < 4; ++mt) {
-                        const float add = lsv[mt] - subv + kPShift;
+                    for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
                         for (int hf = 0; hf < 2; ++hf) {
-                            const float x = s[mt][nt][2 * hf + e];
-                            sum += ex2(x - sub);
-                            s[mt][nt][2 * hf + e] = ex2(x + add);
+                            const float x = ex2(s[mt][nt][2 * hf + e] - sub);
+                            sum += x;
+                            s[mt][nt][2 * hf + e] = x * f[mt];
                         }
-                    }
                     l[nt][e] = fmaf(l[nt][e], c, sum);
 #pragma unroll
                     for (int md = 0; md < 4; ++md) {
@@ -921,16 +956,20 @@ __global__ void __launch_bounds__(512) kvq_fold_len_kernel(const __grid_constant
 int enqueue_kvq_attention(Launcher& L, const KvqProblem& p, const KCtx& c) {
     const size_t smem = 128 + (size_t)kKvqWarps * kQStages * 2 * kQHalf + sizeof(KvqSmem);
     void* args[] = {(void*)&p, (void*)&c};
-    // [format][more than 8 heads][whole]
-    static const void* const kern[2][2][2] = {
-        {{(const void*)kvq_attn_kernel<1, KVQ_E4M3, false>, (const void*)kvq_attn_kernel<1, KVQ_E4M3, true>},
-         {(const void*)kvq_attn_kernel<2, KVQ_E4M3, false>, (const void*)kvq_attn_kernel<2, KVQ_E4M3, true>}},
-        {{(const void*)kvq_attn_kernel<1, KVQ_INT8, false>, (const void*)kvq_attn_kernel<1, KVQ_INT8, true>},
-         {(const void*)kvq_attn_kernel<2, KVQ_INT8, false>, (const void*)kvq_attn_kernel<2, KVQ_INT8, true>}}};
+    // [format][more than 8 heads][whole, else blocks of a tile and more]
+    static const void* const kern[2][2][3] = {
+        {{(const void*)kvq_attn_kernel<1, KVQ_E4M3, false, false>, (const void*)kvq_attn_kernel<1, KVQ_E4M3, false, true>,
+          (const void*)kvq_attn_kernel<1, KVQ_E4M3, true, false>},
+         {(const void*)kvq_attn_kernel<2, KVQ_E4M3, false, false>, (const void*)kvq_attn_kernel<2, KVQ_E4M3, false, true>,
+          (const void*)kvq_attn_kernel<2, KVQ_E4M3, true, false>}},
+        {{(const void*)kvq_attn_kernel<1, KVQ_INT8, false, false>, (const void*)kvq_attn_kernel<1, KVQ_INT8, false, true>,
+          (const void*)kvq_attn_kernel<1, KVQ_INT8, true, false>},
+         {(const void*)kvq_attn_kernel<2, KVQ_INT8, false, false>, (const void*)kvq_attn_kernel<2, KVQ_INT8, false, true>,
+          (const void*)kvq_attn_kernel<2, KVQ_INT8, true, false>}}};
     // A CTA to each pair where none can have more than a few tiles.
     const int pairs = p.T * p.nkv;
     const bool whole = pairs <= kKvqCtas && p.cap / kQTile + p.tail_cap / kQTail <= kWholeTiles;
-    const int e = L.launch(kern[p.format][p.G > 8][whole], dim3(whole ? pairs : kKvqCtas), dim3(kQThreads), smem, args, true);
+    const int e = L.launch(kern[p.format][p.G > 8][whole ? 2 : p.block >= kQTile], dim3(whole ? pairs : kKvqCtas), dim3(kQThreads), smem, args, true);
     if (e || whole) return e;
     // parts of a pair: about kKvqShares / pairs when every sequence is as long; about four to a group
     int heads = 1, pieces = 1;
