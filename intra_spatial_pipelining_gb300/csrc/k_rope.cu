@@ -17,9 +17,9 @@ namespace {
 // own: frequencies 8 c to 8 c + 7 for lane c of the four, in either layout.  Lane i of the warp computes
 // cosine and sine of pair i once for a token.  The angle is a fraction of a turn in 64-bit fixed point,
 // position times (frequency / 2 pi) modulo 1, exact however far the position.
-constexpr int kRWarps = 12;
+constexpr int kRWarps = 16;
 constexpr int kRThreads = 32 * kRWarps;
-constexpr int kRRows = 32;                      // rows of a chunk
+constexpr int kRRows = 16;                      // rows of a chunk
 constexpr int kRStages = 4;
 constexpr int kRStage = kRRows * 128;
 
@@ -66,9 +66,10 @@ __global__ void __launch_bounds__(kRThreads, 1) qk_rope_kernel(const __grid_cons
                 x.t += round ? warps : 1;
             }
         };
-        // A token's row in the caches; negative: it has none.
-        auto place = [&](int t, bool tell) -> long long {
-            const int s = P.seq != nullptr ? P.seq[t] : t, at = P.slot[t];
+        // A token's sequence and slot, and its row in the caches; negative: it has none.
+        auto where = [&](int t) { return make_int2(P.seq != nullptr ? P.seq[t] : t, P.slot[t]); };
+        auto place = [&](int t, int2 x, bool tell) -> long long {
+            const int s = x.x, at = x.y;
             const bool out = s >= P.n_seqs || (s >= 0 && (at < 0 || at >= P.cap));
             if (out && tell) report(ctx, ST_BOUNDS, (uint32_t)t);
             return s < 0 || out ? -1 : (long long)s * P.nkv * P.cap + at;
@@ -78,7 +79,7 @@ __global__ void __launch_bounds__(kRThreads, 1) qk_rope_kernel(const __grid_cons
             uint8_t* dst = ring + st * kRStage;
             if (x.k >= C.q && x.k < C.q + C.k && in_place) {
                 const int j = (x.k - C.q) * kRRows + lane;
-                const long long at = place(x.t, false);
+                const long long at = place(x.t, where(x.t), false);
                 const bool live = j < P.nkv && at >= 0;
                 const unsigned rows = __popc(__ballot_sync(0xffffffffu, live));
                 if (lane == 0) mbar_arrive_expect_tx(&full[st], rows * 128);
@@ -123,6 +124,15 @@ __global__ void __launch_bounds__(kRThreads, 1) qk_rope_kernel(const __grid_cons
             c0 = c < n ? c : 2 * n + 2 * (c - n);
             c1 = c < n ? c + n : c0 + 1;
         }
+        // the next token's position and place, loaded while this one is worked on
+        int pos = 0;
+        int2 put = make_int2(-1, 0);
+        auto ahead = [&](int t) {
+            if (t >= P.T) return;
+            pos = P.pos[t];
+            if (P.k_cache != nullptr) put = where(t);
+        };
+        ahead(cs.t);
         float2 r[8];
         long long at = -1;                      // the token's row in the caches
         int token = -1, st = 0, parity = 0;
@@ -130,9 +140,9 @@ __global__ void __launch_bounds__(kRThreads, 1) qk_rope_kernel(const __grid_cons
         while (cs.left > 0) {
             if (cs.t != token) {
                 token = cs.t;
-                const int pos = P.pos[token];
-                if (P.k_cache != nullptr) at = place(token, lane == 0);
+                if (P.k_cache != nullptr) at = place(token, put, lane == 0);
                 const unsigned long long turn = S.turns[lane] * (unsigned long long)(long long)pos;
+                ahead(token + (round ? warps : 1));
                 float sn, cn;
                 sincospif((float)(int)(turn >> 32) * 0x1p-31f, &sn, &cn);
                 __syncwarp();
