@@ -104,7 +104,6 @@ constexpr int kQHalf = 4096;                    // K (or V) bytes of a tile
 constexpr int kQStages = 2;
 constexpr int kQMax = 512;                      // sequences
 static_assert(2 * kQThreads >= kQMax, "the plan takes two sequences to a thread");
-constexpr int kWholeTiles = 24;
 constexpr float kPShift = 14.f;                 // weights of V are below 2^14: fp16 down to 2^-28 of the largest
 
 // n things cut into `parts` runs, the longer ones first.
@@ -209,11 +208,29 @@ struct Join {
     }
 };
 
+// One query group against one KV head at a time: q^T are the columns of warp-level products,
+//     S^T = K q^T   (16 positions x 8 heads, 64 dims),   O^T += V^T P^T   (16 dims x 8 heads, 16 positions),
+// K and V decoded to fp16 in registers (exact), fp32 sums.  A scale is a factor of the scores, or of the
+// weights before they are rounded for the second product: with m the running maximum of the scores s and mv
+// that of s + log2(v_scale), a weight of V is 2^(s + log2(v_scale) - mv + 14), at most 2^14, so that fp16
+// holds all that counts however the scales differ, while the sum of the weights goes by m alone.
+// Tiles of 64 positions (32 of the bf16 cache, the same bytes) come by bulk copies into a ring of each
+// warp's own, two stages; the order of a product's positions and dims is free, so lanes read K and V from
+// shared memory as they lie: 16 bytes of one position for K, 8 of each of four for V, whose rows are taken
+// such that a quad's lanes read both parities (two-way conflicts instead of four).
+// Bound by HBM for long caches: 512 sequences of up to 32,768 positions on one head (int8) 160.8 us, 0.98 of
+// a copy's rate (e4m3, whose codes the compiler unpacks with more instructions, 170); 64 sequences x 8 heads
+// of up to 8192 49.4, of which 1.3 are the plan, about 4 the shares' uneven ends and 3.5 the join; 10 warps
+// instead of 12: 198 and 55.  Beyond 8 heads to a group the instructions bound it (16: 64.6).
+//
 // WHOLE: a CTA to each pair ((sequence, KV head)), whose warps share its tiles and join their parts in
-// shared memory.  Else the tiles of all pairs are cut into equal shares, one to a warp; a part that is not
-// a whole pair goes to the workspace, for kvq_merge_kernel.  ALIKE: a tile has one scale (blocks of 64 and
-// more); no branch in the loop, which the compiler would not interleave what is around it with (512
-// sequences of up to 32,768 positions, int8: 160.3 us, 175.6 with the branch, 165.9 without the case).
+// shared memory (2 sequences x 8 heads of up to 512 positions: 5.0 us).  Else the tiles of all pairs are cut
+// into equal shares, one to a warp; a part that is not a whole pair goes to the workspace, for
+// kvq_merge_kernel.  (A join by the last CTA to arrive: as long, since its code is met cold, and shares of
+// neighbouring tiles on one SM end less evenly.)
+// ALIKE: a tile has one scale (blocks of 64 and more); a form of its own, because with a branch in the loop
+// the compiler does not interleave what is around it (the first case above 175.6 us with the branch, 165.9
+// without the case).
 template <int NT, int FMT, bool WHOLE, bool ALIKE>
 __global__ void __launch_bounds__(kQThreads, 1) kvq_attn_kernel(const __grid_constant__ KvqProblem P, const KCtx ctx) {
     extern __shared__ uint8_t smem_raw[];
@@ -703,7 +720,8 @@ __global__ void __launch_bounds__(kQThreads, 1) kvq_attn_kernel(const __grid_con
 }
 
 // Joins the parts of the pairs that more than one share has worked on, in the shares' order: `heads` heads
-// to a CTA, `pieces` groups of sixteen threads to a head.
+// to a CTA, `pieces` groups of sixteen threads to a head.  Latency: two dependent loads behind the first
+// kernel's end, 3.5 us.  It is not launched early: waiting CTAs cost the first kernel 0.7 to 1.3 us.
 __global__ void __launch_bounds__(512) kvq_merge_kernel(const __grid_constant__ KvqProblem P, const int heads, const int pieces, const KCtx ctx) {
     __shared__ __align__(16) float rows[32][kPartRow];
     griddep_wait();
@@ -800,9 +818,13 @@ __device__ __noinline__ uint32_t divide4(uint32_t a, uint32_t b, float s) {
     return code;
 }
 
-// One warp holds 32 positions of one (sequence, KV head, tensor) in registers; lane l has the dims
-// 16 (l & 3) to 16 (l & 3) + 15 of rows 8 i + l / 4.  Blocks of more positions join their warps'
-// maxima in shared memory.
+// One warp holds 32 positions of one (sequence, KV head, tensor) in registers, so that they are read once;
+// lane l has the dims 16 (l & 3) to 16 (l & 3) + 15 of rows 8 i + l / 4.  Blocks of more positions join
+// their warps' maxima in shared memory; magnitudes compare as integers, which sorts infinities and NaN
+// above every number.  The first CTA of a (sequence, KV head, tensor) also moves the rest: fewer than 128
+// rows, which it holds in registers before it or anyone else overwrites the rows that it reads.
+// Bound by HBM: 64 sequences x 8 heads of up to 8192 positions, 797 MB, 124.4 us in e4m3 (0.95 of a copy's
+// rate), 134 in int8; 128 threads to a CTA 137.6.  Short ones are latency (64 x 8 of up to 127: 5.7).
 template <int FMT>
 __global__ void __launch_bounds__(kFThreads, 4) kvq_fold_kernel(const __grid_constant__ FoldProblem P, const KCtx ctx) {
     __shared__ uint32_t tops[kFThreads / 32];
@@ -966,12 +988,16 @@ int enqueue_kvq_attention(Launcher& L, const KvqProblem& p, const KCtx& c) {
           (const void*)kvq_attn_kernel<1, KVQ_INT8, true, false>},
          {(const void*)kvq_attn_kernel<2, KVQ_INT8, false, false>, (const void*)kvq_attn_kernel<2, KVQ_INT8, false, true>,
           (const void*)kvq_attn_kernel<2, KVQ_INT8, true, false>}}};
-    // A CTA to each pair where none can have more than a few tiles.
+    // A CTA to each pair where none can have many tiles, by capacity (lengths are on the device); the more
+    // pairs, the longer the other form takes.  Replayed, a CTA to each and shares with a join: 16 pairs of
+    // 512 positions 5.0 and 7.9 us, 1024 6.5 and 8.0, 1536 8.2 and 8.0, 2048 9.2 and 8.0, 4096 14.6 and
+    // 8.4; 148 pairs of up to 500 5.1 and 8.3, 1000 6.8 and 8.9, 2000 9.6 and 11.4, 3001 13.2 and 13.1.
     const int pairs = p.T * p.nkv;
-    const bool whole = pairs <= kKvqCtas && p.cap / kQTile + p.tail_cap / kQTail <= kWholeTiles;
+    const bool whole = pairs <= kKvqCtas && p.cap / kQTile + p.tail_cap / kQTail <= 24 + pairs / 6;
     const int e = L.launch(kern[p.format][p.G > 8][whole ? 2 : p.block >= kQTile], dim3(whole ? pairs : kKvqCtas), dim3(kQThreads), smem, args, true);
     if (e || whole) return e;
-    // parts of a pair: about kKvqShares / pairs when every sequence is as long; about four to a group
+    // Parts of a pair: about kKvqShares / pairs when every sequence is as long; two to four to a group (8
+    // pairs of 228 parts, 512 of 5, 148 of 13: with eight to a group 0.1, 0 and 0.5 us more).
     int heads = 1, pieces = 1;
     while (pieces < 32 && pairs * pieces * 4 < kKvqShares) pieces *= 2;
     while (heads * 2 * pieces <= 16 && heads < p.G) heads *= 2;

@@ -417,12 +417,19 @@ KVQ = {
 }
 
 
+# Short caches and caches with much room take different ways to the same sums.
+ROOM = 4096
+
+
+@pytest.mark.parametrize("room", [0, ROOM])
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("name", KVQ)
-def test_kvq_attention(name, fmt):
+def test_kvq_attention(name, fmt, room):
     nq, nkv, held, tail, window = KVQ[name]
+    if room and len(held) > 100:
+        pytest.skip("many sequences go one way in any case")
     for block in (16, 64, 128):
-        x = Kvq(sum(map(ord, name)) + block, nq, nkv, held, tail, block, fmt, window)
+        x = Kvq(sum(map(ord, name)) + block, nq, nkv, held, tail, block, fmt, window, cap=max(held) + 128 + room if room else None)
         x.run()
         x.check()
         first = x.o.clone()
@@ -430,12 +437,14 @@ def test_kvq_attention(name, fmt):
         assert torch.equal(first, x.o)
 
 
+@pytest.mark.parametrize("room", [0, ROOM])
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("block", [16, 32, 64, 128])
-def test_kvq_attention_lengths_around_blocks_and_tiles(block, fmt):
+def test_kvq_attention_lengths_around_blocks_and_tiles(block, fmt, room):
     held = [block * i for i in range(0, 10)] * 2
     for window in (0, 1, 15, 16, 17, 63, 64, 65, 130):
-        x = Kvq(block + window, 8, 1, held, [(t * 5) % 67 for t in range(20)], block, fmt, window)
+        x = Kvq(block + window, 8, 1, held, [(t * 5) % 67 for t in range(20)], block, fmt, window,
+                cap=1280 + room if room else None)
         x.run()
         x.check()
 
@@ -447,11 +456,12 @@ def test_kvq_attention_without_a_bf16_cache(fmt):
     x.check()
 
 
+@pytest.mark.parametrize("room", [0, ROOM])
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("scale", [0.0, 1e-30, 40.0, 1e30])
-def test_kvq_attention_query_sizes(fmt, scale):
+def test_kvq_attention_query_sizes(fmt, scale, room):
     """Weights all alike, one position that takes all, queries near the ends of the range."""
-    x = Kvq(9, 16, 2, [768, 256], [30, 0], 64, fmt, scale=min(scale, 1e3))
+    x = Kvq(9, 16, 2, [768, 256], [30, 0], 64, fmt, scale=min(scale, 1e3), cap=832 + room)
     if scale > 1e3:                                           # large queries on small keys
         x.q *= 1e27
         x.ks *= 2.0 ** -95
@@ -460,11 +470,12 @@ def test_kvq_attention_query_sizes(fmt, scale):
     x.check()
 
 
+@pytest.mark.parametrize("room", [0, ROOM])
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
-def test_kvq_attention_value_scales_far_apart(fmt):
+def test_kvq_attention_value_scales_far_apart(fmt, room):
     """Blocks whose values are 2^60 times others', where the weights make up for it: the small weights
     of the large values count as much as the large weights of the small ones."""
-    x = Kvq(4, 8, 1, [512, 512], [20, 20], 64, fmt, spread=0)
+    x = Kvq(4, 8, 1, [512, 512], [20, 20], 64, fmt, spread=0, cap=576 + room)
     x.q[:] = 0
     x.q[:, :, 0] = 16.0                                       # the score: 2 k[0]
     unit = 0x40 if fmt == "e4m3" else 64                      # 2, and 64
@@ -478,11 +489,13 @@ def test_kvq_attention_value_scales_far_apart(fmt):
     x.check()
 
 
-def test_kvq_attention_scales_of_zero_and_nan():
+@pytest.mark.parametrize("block", [32, 64])
+@pytest.mark.parametrize("room", [0, ROOM])
+def test_kvq_attention_scales_of_zero_and_nan(room, block):
     """A value scale of 0 gives values of 0; NaN in a scale that is seen shows in that head alone."""
-    x = Kvq(5, 16, 2, [256, 256, 256], [5, 5, 5], 64, "int8")
+    x = Kvq(5, 16, 2, [256, 256, 256], [5, 5, 5], block, "int8", cap=320 + room)
     x.vs[0, 0, 1] = 0
-    x.vs[0, 1, :4] = 0
+    x.vs[0, 1, :256 // block] = 0
     x.ks[1, 1, 2] = NAN
     x.vs[2, 0, 0] = NAN
     x.run()
@@ -493,9 +506,10 @@ def test_kvq_attention_scales_of_zero_and_nan():
     x.compare(seqs=[0])
 
 
-def test_kvq_attention_infinities_stay_with_their_sequence():
+@pytest.mark.parametrize("room", [0, ROOM])
+def test_kvq_attention_infinities_stay_with_their_sequence(room):
     """Infinite keys of one sequence and a NaN query head of another."""
-    x = Kvq(6, 16, 2, [256, 128, 0, 128], [9, 40, 33, 7], 64, "e4m3")
+    x = Kvq(6, 16, 2, [256, 128, 0, 128], [9, 40, 33, 7], 64, "e4m3", cap=320 + room)
     x.k[1, :, 3] = math.inf
     x.q[2, 5] = NAN
     x.q[3, 9] = NAN
@@ -507,9 +521,10 @@ def test_kvq_attention_infinities_stay_with_their_sequence():
         assert torch.isfinite(x.o[t, [i for i in range(16) if i != h]]).all()
 
 
-def test_kvq_attention_reports_bad_lengths():
-    x = Kvq(7, 8, 1, [256, 128, 128, 64, 128, 128], [5, 7, 9, 11, 1, 1], 64, "int8", cap=320)
-    x.h[0], x.h[1], x.h[2] = 384, -64, 100
+@pytest.mark.parametrize("room", [0, ROOM])
+def test_kvq_attention_reports_bad_lengths(room):
+    x = Kvq(7, 8, 1, [256, 128, 128, 64, 128, 128], [5, 7, 9, 11, 1, 1], 64, "int8", cap=320 + room)
+    x.h[0], x.h[1], x.h[2] = 384 + room, -64, 100
     x.n[3], x.n[4] = -1, x.k.shape[2] + 1
     x.run()
     assert status(x.ws) == sgp.SGP_ERR_DEVICE_BOUNDS
@@ -522,7 +537,7 @@ def test_kvq_attention_reports_bad_lengths():
 
 
 def test_kvq_attention_output_may_be_the_query():
-    for held in ([2048, 512], [128 * (t % 3) for t in range(300)]):
+    for held in ([2048, 512], [256, 512, 64], [128 * (t % 3) for t in range(300)]):
         x = Kvq(8, 16, 2, held, [3] * len(held), 64, "e4m3")
         x.run()
         x.check()
@@ -557,10 +572,10 @@ def test_kvq_attention_in_the_workspace_of_a_larger_call():
     x.check()
 
 
-@pytest.mark.parametrize("fmt,block", [("e4m3", 64), ("int8", 16)])
-def test_rows_behind_the_last_sequence_are_left_as_they_were(fmt, block):
+@pytest.mark.parametrize("fmt,block,room", [("e4m3", 64, 0), ("int8", 16, ROOM)])
+def test_rows_behind_the_last_sequence_are_left_as_they_were(fmt, block, room):
     T = 5
-    x = Kvq(12, 16, 2, [128, 256, 0, 512, 128, 128, 128, 128], [3, 0, 0, 40, 64, 1, 1, 1], block, fmt)
+    x = Kvq(12, 16, 2, [128, 256, 0, 512, 128, 128, 128, 128], [3, 0, 0, 40, 64, 1, 1, 1], block, fmt, cap=640 + room)
     x.q[T:], x.k[T:], x.v[T:] = NAN, NAN, NAN
     x.n[T:], x.h[T:] = 1 << 30, 1 << 30
     x.o.fill_(5.0)
@@ -625,11 +640,12 @@ def test_far_into_long_caches():
 # ---------------------------------------------------------------------------------------
 # streams, graphs, the binding
 # ---------------------------------------------------------------------------------------
-def test_captured_and_beside_another_stream():
+@pytest.mark.parametrize("room", [0, ROOM])
+def test_captured_and_beside_another_stream(room):
     """Rotation, attention and fold captured into one graph, replayed while another stream runs the
     same operators in workspaces of its own."""
     def make(seed):
-        x = Kvq(seed, 16, 2, [512, 0, 256], [70, 64, 3], 64, "e4m3", cap=1024, tail_cap=200)
+        x = Kvq(seed, 16, 2, [512, 0, 256], [70, 64, 3], 64, "e4m3", cap=1024 + room, tail_cap=200)
         x.slot = ints([69, 63, 2])
         return x, Rope(3, 16, 2, 64, "half", "none", False, 9)
     a, r = make(20)
