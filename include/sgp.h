@@ -412,7 +412,8 @@ int sgp_lora_apply(const sgp_lora* lora, const int32_t* adapter_of, const void* 
  *   - Eviction: kept keys keep the rotation of the position that they had, so slots are positions no
  *     longer, and the layer's next q and key would be rotated for one that lies before kept keys.
  *     Run SGP_OP_QKV with rope_theta = 0 in its dims; then rotate view->q and the new row, slot
- *     kv_len - 1 of k_cache, for the sequence's own count of positions, before the attention.  Keys of
+ *     kv_len - 1 of k_cache, for the sequence's own count of positions, before the attention
+ *     (sgp_qk_rope_append with the new keys in their slots does both).  Keys of
  *     a prefix may then be rotated for p, and own positions for len, len + 1, ...  A window counts
  *     slots, not positions.
  *   - Adapters on q: as after an eviction, between SGP_OP_QKV and the rotation.
@@ -543,7 +544,7 @@ size_t sgp_kvq_attention_workspace_bytes(const sgp_dims* dims, int n_tokens);
  *   lse        device fp32 [n_tokens][n_q] or NULL, as sgp_prefix_attention writes it
  * Sums, maxima and lse are fp32; for their product with v the weights, times v's scale, are rounded to
  * fp16 over coded positions (relative to the largest of them, down to 2^-28 of it) and to bf16 over the
- * others.  A sequence that sees no position gets o = 0 and lse = -inf.  What caches, codes and scales
+ * others.  Value scales of one sequence and KV head lie within 2^100 of each other (or are 0).  A sequence that sees no position gets o = 0 and lse = -inf.  What caches, codes and scales
  * hold behind their lengths, or before the window, is not looked at (it may be NaN).
  * Returns SGP_OK, SGP_ERR_INVALID_ARG or SGP_ERR_CUDA. */
 int sgp_kvq_attention(const sgp_dims* dims, const sgp_kvq* kvq, const int32_t* kvq_len,
