@@ -28,6 +28,21 @@ constexpr int kRRows = 16;                      // rows of a chunk
 constexpr int kRStages = 4;
 constexpr int kRStage = kRRows * 128;
 
+// Two bf16 as two numbers, the lower half first.
+__device__ __forceinline__ float2 numbers(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+// A lane's words in the order of its pairs and back: word j of the one result holds the first elements of
+// two pairs, of the other one the second elements.  With neighbouring elements as pairs these are pairs j
+// and j + 4 of its eight, with halves apart pairs 2 j and 2 j + 1, and the words are in order already.
+__device__ __forceinline__ void by_pairs(uint32_t& a, uint32_t& b, bool interleaved) {
+    if (interleaved) {
+        const uint32_t t = __byte_perm(a, b, 0x5410);
+        b = __byte_perm(a, b, 0x7632);
+        a = t;
+    }
+}
+
 struct RopeSmem {
     uint64_t full[kRWarps][kRStages];
     unsigned long long turns[32];
@@ -139,10 +154,12 @@ __global__ void __launch_bounds__(kRThreads, 1) qk_rope_kernel(const __grid_cons
             if (P.k_cache != nullptr) put = where(t);
         };
         ahead(cs.t);
-        float2 r[8];
+        // (first, second) -> (first * ff + second * sf, second * ss + first * fs), gains included
+        float2 ff[4], sf[4], ss[4], fs[4];
+        const bf16* with = nullptr;             // gains that they have in them
         long long at = -1;                      // the token's row in the caches
         int token = -1, st = 0, parity = 0;
-        bool failed = false;
+        bool fresh = false, failed = false;
         while (cs.left > 0) {
             if (cs.t != token) {
                 token = cs.t;
@@ -154,12 +171,7 @@ __global__ void __launch_bounds__(kRThreads, 1) qk_rope_kernel(const __grid_cons
                 __syncwarp();
                 S.trig[warp][lane] = lane < P.rot / 2 ? make_float2(cn * P.amplitude, sn * P.amplitude) : make_float2(1.f, 0.f);
                 __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float4 v = *reinterpret_cast<const float4*>(&S.trig[warp][8 * c + 2 * i]);
-                    r[2 * i] = make_float2(v.x, v.y);
-                    r[2 * i + 1] = make_float2(v.z, v.w);
-                }
+                fresh = true;
             }
             // where the chunk goes
             const bf16* gain = P.g_q;
@@ -191,59 +203,68 @@ __global__ void __launch_bounds__(kRThreads, 1) qk_rope_kernel(const __grid_cons
                 failed = true;
                 break;
             }
+            if (turned && (fresh || gain != with)) {
+                fresh = false;
+                with = gain;
+                uint4 g0 = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u), g1 = g0;     // ones
+                if (gain != nullptr) {
+                    g0 = *reinterpret_cast<const uint4*>(gain + c0 * 8);
+                    g1 = *reinterpret_cast<const uint4*>(gain + c1 * 8);
+                }
+                uint32_t gf[4] = {g0.x, g0.y, g0.z, g0.w}, gs[4] = {g1.x, g1.y, g1.z, g1.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    by_pairs(gf[j], gs[j], P.interleaved);
+                    const float2 t0 = S.trig[warp][8 * c + (P.interleaved ? j : 2 * j)];
+                    const float2 t1 = S.trig[warp][8 * c + (P.interleaved ? j + 4 : 2 * j + 1)];
+                    const float2 f = numbers(gf[j]), s = numbers(gs[j]);
+                    ff[j] = make_float2(t0.x * f.x, t1.x * f.y);
+                    fs[j] = make_float2(t0.y * f.x, t1.y * f.y);
+                    ss[j] = make_float2(t0.x * s.x, t1.x * s.y);
+                    sf[j] = make_float2(-t0.y * s.x, -t1.y * s.y);
+                }
+            }
             if (kept) {
                 const uint8_t* row = ring + st * kRStage + g * 128;
                 dst += g * step;
-                uint4 gain0, gain1;
-                if (turned && gain != nullptr) {
-                    gain0 = *reinterpret_cast<const uint4*>(gain + c0 * 8);
-                    gain1 = *reinterpret_cast<const uint4*>(gain + c1 * 8);
-                }
 #pragma unroll 1
                 for (int j = g; j - g < rows; j += 8) {
                     uint4 x0 = *reinterpret_cast<const uint4*>(row + c0 * 16), x1 = *reinterpret_cast<const uint4*>(row + c1 * 16);
                     row += 1024;
                     if (turned) {
-                        float a[8], b[8];
-                        unpack8(x0, a);
-                        unpack8(x1, b);
+                        uint32_t u[4] = {x0.x, x0.y, x0.z, x0.w}, v[4] = {x1.x, x1.y, x1.z, x1.w};
+                        float2 f[4], s[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            by_pairs(u[i], v[i], P.interleaved);
+                            f[i] = numbers(u[i]);
+                            s[i] = numbers(v[i]);
+                        }
+                        float2 inv = make_float2(1.f, 1.f);
                         if (gain != nullptr) {
-                            float ss = 0.f;
+                            float2 sum = mul2(f[0], f[0]);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) ss = fmaf(a[i], a[i], fmaf(b[i], b[i], ss));
-                            ss += __shfl_xor_sync(0xffffffffu, ss, 1);
-                            ss += __shfl_xor_sync(0xffffffffu, ss, 2);
-                            const float inv = rsqrtf(fmaf(ss, 1.f / 64.f, P.eps));
-                            float ga[8], gb[8];
-                            unpack8(gain0, ga);
-                            unpack8(gain1, gb);
+                            for (int i = 1; i < 4; ++i) sum = fma2(f[i], f[i], sum);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                a[i] *= inv * ga[i];
-                                b[i] *= inv * gb[i];
-                            }
+                            for (int i = 0; i < 4; ++i) sum = fma2(s[i], s[i], sum);
+                            float q = sum.x + sum.y;
+                            q += __shfl_xor_sync(0xffffffffu, q, 1);
+                            q += __shfl_xor_sync(0xffffffffu, q, 2);
+                            inv.x = inv.y = rsqrtf(fmaf(q, 1.f / 64.f, P.eps));
                         }
-                        if (P.interleaved) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float u = a[2 * i], v = a[2 * i + 1], y = b[2 * i], z = b[2 * i + 1];
-                                a[2 * i] = u * r[i].x - v * r[i].y;
-                                a[2 * i + 1] = v * r[i].x + u * r[i].y;
-                                b[2 * i] = y * r[4 + i].x - z * r[4 + i].y;
-                                b[2 * i + 1] = z * r[4 + i].x + y * r[4 + i].y;
+                        for (int i = 0; i < 4; ++i) {
+                            float2 y = fma2(s[i], sf[i], mul2(f[i], ff[i])), z = fma2(f[i], fs[i], mul2(s[i], ss[i]));
+                            if (gain != nullptr) {
+                                y = mul2(y, inv);
+                                z = mul2(z, inv);
                             }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float u = a[i], v = b[i];
-                                a[i] = u * r[i].x - v * r[i].y;
-                                b[i] = v * r[i].x + u * r[i].y;
-                            }
+                            u[i] = pack_bf16x2(y.x, y.y);
+                            v[i] = pack_bf16x2(z.x, z.y);
+                            by_pairs(u[i], v[i], P.interleaved);
                         }
-                        x0 = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]),
-                                        pack_bf16x2(a[6], a[7]));
-                        x1 = make_uint4(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]), pack_bf16x2(b[4], b[5]),
-                                        pack_bf16x2(b[6], b[7]));
+                        x0 = make_uint4(u[0], u[1], u[2], u[3]);
+                        x1 = make_uint4(v[0], v[1], v[2], v[3]);
                     }
                     if (j < rows) {
                         *reinterpret_cast<uint4*>(dst + c0 * 8) = x0;
