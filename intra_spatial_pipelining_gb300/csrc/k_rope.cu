@@ -138,7 +138,8 @@ __global__ void __launch_bounds__(kRThreads, 1) qk_rope_kernel(const __grid_cons
                 issue(ld, st);
                 ++issued;
             }
-        // this lane's two pieces of 8 elements
+        // this lane's two pieces of 8 elements; whether its pairs are rotated, all of them or none
+        const bool spin = c < P.rot / 16;
         int c0 = 2 * c, c1 = 2 * c + 1;
         if (!P.interleaved) {
             const int n = P.rot / 16;           // lanes with rotated pieces
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(kRThreads, 1) qk_rope_kernel(const __grid_cons
                 for (int j = g; j - g < rows; j += 8) {
                     uint4 x0 = *reinterpret_cast<const uint4*>(row + c0 * 16), x1 = *reinterpret_cast<const uint4*>(row + c1 * 16);
                     row += 1024;
-                    if (turned) {
+                    if (turned && (spin || gain != nullptr)) {
                         uint32_t u[4] = {x0.x, x0.y, x0.z, x0.w}, v[4] = {x1.x, x1.y, x1.z, x1.w};
                         float2 f[4], s[4];
 #pragma unroll
@@ -254,7 +255,11 @@ __global__ void __launch_bounds__(kRThreads, 1) qk_rope_kernel(const __grid_cons
                         }
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            float2 y = fma2(s[i], sf[i], mul2(f[i], ff[i])), z = fma2(f[i], fs[i], mul2(s[i], ss[i]));
+                            float2 y = mul2(f[i], ff[i]), z = mul2(s[i], ss[i]);
+                            if (spin) {         // elsewhere 0 times an infinity would not be 0
+                                y = fma2(s[i], sf[i], y);
+                                z = fma2(f[i], fs[i], z);
+                            }
                             if (gain != nullptr) {
                                 y = mul2(y, inv);
                                 z = mul2(z, inv);

@@ -173,6 +173,42 @@ def test_qk_rope_values_of_every_size():
     assert qo[3].view(nq, D).isnan().any(1).all()
 
 
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("rot", [16, 32, 48])
+def test_qk_rope_leaves_what_it_does_not_rotate(rot, layout):
+    """Bit by bit without a norm: infinities, NaN with a payload, zeros of both signs, subnormals.  With one an
+    infinity makes the numbers that are not rotated 0, with their signs, and itself NaN; a zero keeps its sign."""
+    T, nq, nkv = 37, 6, 2
+    x = Rope(T, nq, nkv, rot, layout, "none", True, 9)
+    words = torch.from_numpy(np.random.default_rng(rot).integers(-2 ** 15, 2 ** 15, (T + 1, nq, D)).astype(np.int16))
+    words[0, 0, rot:] = torch.tensor([0x7f80, -0x80, 0x7f81, -0x8000, 0, 1, -0x7fff, 0x7fff] * ((D - rot) // 8), dtype=torch.int16)
+    q = words.cuda().view(torch.bfloat16).reshape(T + 1, nq * D)
+    kc, vc = (torch.zeros(T, nkv, 3, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    qo = torch.empty_like(q)
+    sgp.sgp_qk_rope_append(x.dims, x.rope, None, None, 0.0, x.pos, q, qo, q[:, :nkv * D], None, sgp.make_cache(kc, vc), T,
+                           None, ints([t % 3 for t in range(T)]), T, x.ws)
+    assert status(x.ws) == sgp.SGP_OK
+    assert torch.equal(qo[:T].view(torch.int16).view(T, nq, D)[..., rot:].cpu(), words[:T, :, rot:])
+    t = torch.arange(T, device="cuda")
+    assert torch.equal(kc[t, :, t % 3].view(torch.int16)[..., rot:].cpu(), words[:T, :nkv, rot:])
+    # normed: one infinity to a head, in the part that is not rotated
+    q = bf16(np.random.default_rng(1), T, nq, D)
+    q[..., D - 6] = -0.0
+    at = rot + (torch.arange(T * nq, device="cuda").view(T, nq) * 7) % (D - rot - 8)
+    q.scatter_(2, at[..., None], math.inf)
+    qo = torch.full_like(q, 5.0)
+    sgp.sgp_qk_rope(x.dims, x.rope, x.gq, None, x.eps, x.pos, q.view(T, -1), qo.view(T, -1), None, None, T, x.ws)
+    hit = torch.zeros_like(q, dtype=torch.bool).scatter_(2, at[..., None], True)
+    assert torch.equal(qo.isnan(), hit)
+    assert (qo[~hit] == 0).all()
+    sign = q.signbit() ^ x.gq.signbit()
+    assert torch.equal(qo.signbit()[..., rot:][~hit[..., rot:]], sign[..., rot:][~hit[..., rot:]])
+    q.masked_fill_(hit, 1.0)
+    sgp.sgp_qk_rope(x.dims, x.rope, x.gq, None, x.eps, x.pos, q.view(T, -1), qo.view(T, -1), None, None, T, x.ws)
+    zero = qo[..., D - 6]
+    assert (zero == 0).all() and torch.equal(zero.signbit(), sign[..., D - 6])
+
+
 # ---------------------------------------------------------------------------------------
 # fold
 # ---------------------------------------------------------------------------------------
