@@ -537,15 +537,17 @@ size_t sgp_kvq_attention_workspace_bytes(const sgp_dims* dims, int n_tokens);
  * cache->window = W > 0 it sees the last W of both together.  Nothing is rotated here.
  *   kvq        codes and scales of n_tokens sequences; read only
  *   kvq_len    device int32 [n_tokens], a multiple of block, 0 <= kvq_len[b] <= kvq->cap
- *   cache      bf16 caches [n_tokens][n_kv][kv_cap][d], or NULL: no bf16 positions, no window
+ *   cache      bf16 caches [n_tokens][n_kv][kv_cap][d], kvq->cap + kv_cap < 2^31, or NULL: no bf16
+ *              positions, no window
  *   kv_len     device int32 [n_tokens], 0 <= kv_len[b] <= kv_cap (not read without cache); where either
  *              length is out of range the sequence counts as empty
  *   q, o       device bf16 [n_tokens][n_q d]; o may equal q
  *   lse        device fp32 [n_tokens][n_q] or NULL, as sgp_prefix_attention writes it
  * Sums, maxima and lse are fp32; for their product with v the weights, times v's scale, are rounded to
  * fp16 over coded positions (relative to the largest of them, down to 2^-28 of it) and to bf16 over the
- * others.  Value scales of one sequence and KV head lie within 2^100 of each other (or are 0).  A sequence that sees no position gets o = 0 and lse = -inf.  What caches, codes and scales
- * hold behind their lengths, or before the window, is not looked at (it may be NaN).
+ * others.  Value scales of one sequence and KV head lie within 2^100 of each other (or are 0).  A
+ * sequence that sees no position gets o = 0 and lse = -inf.  What caches, codes and scales hold behind
+ * their lengths, or before the window, is not looked at (it may be NaN).
  * Returns SGP_OK, SGP_ERR_INVALID_ARG or SGP_ERR_CUDA. */
 int sgp_kvq_attention(const sgp_dims* dims, const sgp_kvq* kvq, const int32_t* kvq_len,
                       const sgp_layer* cache, const int32_t* kv_len, const void* q, void* o, float* lse,

@@ -516,6 +516,7 @@ int kvq_attention(const sgp_dims* d, const sgp_kvq* kvq, const int32_t* kvq_len,
     int r;
     if ((r = check_heads(d, true)) || (r = check_tokens(T)) || (r = check_kvq(d, kvq, T))) return r;
     if (cache && (r = check_cache(d, cache, T, true, 16))) return r;
+    if (cache && (int64_t)kvq->cap + cache->kv_cap >= (1ll << 31)) return host_fail_arg("positions of a sequence exceed 2^31");
     if (bad4(kvq_len) || (cache && bad4(kv_len))) return host_fail_arg("kvq_len or kv_len NULL or not aligned");
     if (bad16(q) || bad16(o)) return host_fail_arg("q or o NULL or not 16-byte aligned");
     if (lse && bad4(lse)) return host_fail_arg("lse not aligned");

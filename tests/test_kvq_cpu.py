@@ -237,6 +237,9 @@ def test_kvq_attention_refuses_bad_arguments(lib, mem):
                dict(nbytes=need - 1), dict(nbytes=0), dict(cap=1 << 28)):
         assert call(**kw) == E, kw
         assert lib.sgp_last_error().decode()
+    # a sequence's positions are counted in 32 bits
+    assert call(nq=1, nkv=1, T=1, kvq=dict(cap=1 << 30), cap=1 << 30) == E and b"2^31" in lib.sgp_last_error()
+    assert call(nq=1, nkv=1, T=1, kvq=dict(cap=1 << 30), cap=(1 << 30) - 1, ws=None) == E and b"workspace" in lib.sgp_last_error()
     for kw in (dict(cache=False, n=None), dict(lse=None), dict(o=0), dict(window=5)):
         assert call(nbytes=0, **kw) == E and b"workspace" in lib.sgp_last_error(), kw
     size = sgp.sgp_kvq_attention_workspace_bytes
