@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kRThreads, 1) qk_rope_kernel(const __grid_cons
             if (x.k >= C.q && x.k < C.q + C.k && in_place) {
                 const int j = (x.k - C.q) * kRRows + lane;
                 const long long at = place(x.t, where(x.t), false);
-                const bool live = j < P.nkv && at >= 0;
+                const bool live = lane < kRRows && j < P.nkv && at >= 0;
                 const unsigned rows = __popc(__ballot_sync(0xffffffffu, live));
                 if (lane == 0) mbar_arrive_expect_tx(&full[st], rows * 128);
                 __syncwarp();

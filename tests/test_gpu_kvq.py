@@ -137,6 +137,28 @@ def test_qk_rope_append(T, nq, nkv, rot, layout, scaling, norm, far, n, cap):
     assert torch.equal(kc, before) and torch.equal(vc, values)
 
 
+@pytest.mark.parametrize("nkv", [15, 16, 17, 33, 100])
+def test_qk_rope_append_of_many_kv_heads(nkv):
+    """More rows of a token than a stage holds, from rows and in their slots."""
+    T, n, cap = 300, 20, 16
+    x = Rope(T, nkv, nkv, 64, "half", "none", True, 5)
+    place = np.random.default_rng(nkv).permutation(n * cap)[:T]
+    seq, slot = ints(place // cap), ints(place % cap)
+    at = seq.long(), slot.long()
+    kc, vc = (torch.full((n, nkv, cap, D), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    qo = torch.full((T, nkv * D), NAN, dtype=torch.bfloat16, device="cuda")
+    sgp.sgp_qk_rope_append(x.dims, x.rope, x.gq, x.gk, x.eps, x.pos, x.q, qo, x.k, x.v, sgp.make_cache(kc, vc), n, seq, slot, T, x.ws)
+    x.check("q", qo, x.q, x.gq)
+    x.check("k", kc[at[0], :, at[1]], x.k, x.gk)
+    assert torch.equal(vc[at[0], :, at[1]].reshape(T, -1), x.v[:T])
+    before, values = kc.clone(), vc.clone()
+    kc[at[0], :, at[1]] = x.k[:T].reshape(T, nkv, D)
+    qa = torch.full_like(qo, NAN)
+    sgp.sgp_qk_rope_append(x.dims, x.rope, x.gq, x.gk, x.eps, x.pos, x.q, qa, None, None, sgp.make_cache(kc, vc), n, seq, slot, T, x.ws)
+    assert torch.equal(qa, qo) and torch.equal(kc, before) and torch.equal(vc, values)
+    assert status(x.ws) == sgp.SGP_OK
+
+
 def test_qk_rope_append_without_sequences_and_with_bad_places():
     """Token t goes to sequence t; a place out of range is reported, its caches stay, its q is turned."""
     T, nq, nkv, cap = 6, 8, 2, 9
