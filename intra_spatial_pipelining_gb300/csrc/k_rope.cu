@@ -17,11 +17,11 @@ namespace {
 // own: frequencies 8 c to 8 c + 7 for lane c of the four, in either layout.  Lane i of the warp computes
 // cosine and sine of pair i once for a token.  The angle is a fraction of a turn in 64-bit fixed point,
 // position times (frequency / 2 pi) modulo 1, exact however far the position.
-// Bound by HBM: 16,384 tokens of 64 + 8 heads from a fused projection into q and caches, 336 MB, 54.7 us
-// (0.91 of a copy's rate; 70 with rows in registers and a token to a warp); by latency and the host's 9 to
-// 10 us a call for a batch of single tokens (2.7 us for one, 4.6 for 512).  Fewer rows to a chunk balance
-// small calls, more serve large ones: 32 rows and 12 warps 53.3 us and 5.6 for the batch, 29 against 25 for
-// 12,000 tokens of 32 + 4 normed heads.
+// Bound by HBM: 16,384 tokens of 64 + 8 heads from a fused projection into q and caches, 336 MB, 55.2 us
+// (0.90 of a copy's rate; 70 with rows in registers and a token to a warp), normed 56.2; with few heads by
+// what a chunk costs (32 + 4 heads 32.1, normed 38.6, a copy 24.9); by latency and the host's 9 to 10 us a
+// call for a batch of single tokens (2.6 us for one, 4.6 for 512).  Fewer rows to a chunk balance small
+// calls, more serve large ones: 32 rows and 12 warps 5.6 for the batch.
 constexpr int kRWarps = 16;
 constexpr int kRThreads = 32 * kRWarps;
 constexpr int kRRows = 16;                      // rows of a chunk
@@ -80,12 +80,14 @@ __global__ void __launch_bounds__(kRThreads, 1) qk_rope_kernel(const __grid_cons
     if (left > 0) {
         uint8_t* ring = smem + (size_t)warp * kRStages * kRStage;
         uint64_t* full = S.full[warp];
+        // Going round, a warp begins with another chunk of its tokens than its neighbours (55.8 us without,
+        // for the 55.2 above) and has two chunks under way: with four, reads and writes get in each other's
+        // way (62).
+        const int start = round ? w % per : 0, depth = round ? 2 : kRStages;
         auto next = [&](RopePlace& x) {
             --x.left;
-            if (++x.k == per) {
-                x.k = 0;
-                x.t += round ? warps : 1;
-            }
+            if (++x.k == per) x.k = 0;
+            if (x.k == start) x.t += round ? warps : 1;
         };
         // A token's sequence and slot, and its row in the caches; negative: it has none.
         auto where = [&](int t) { return make_int2(P.seq != nullptr ? P.seq[t] : t, P.slot[t]); };
@@ -129,12 +131,12 @@ __global__ void __launch_bounds__(kRThreads, 1) qk_rope_kernel(const __grid_cons
         cs.left = left;
         const int first = round ? w * per : w * each + min(w, more);
         cs.t = first / per;
-        cs.k = first - cs.t * per;
+        cs.k = round ? start : first - cs.t * per;
         RopePlace ld = cs;
         uint32_t issued = 0, done = 0;
 #pragma unroll
         for (int st = 0; st < kRStages; ++st)
-            if (ld.left > 0) {
+            if (ld.left > 0 && st < depth) {
                 issue(ld, st);
                 ++issued;
             }
@@ -146,13 +148,17 @@ __global__ void __launch_bounds__(kRThreads, 1) qk_rope_kernel(const __grid_cons
             c0 = c < n ? c : 2 * n + 2 * (c - n);
             c1 = c < n ? c + n : c0 + 1;
         }
-        // the next token's position and place, loaded while this one is worked on
-        int pos = 0;
+        // positions and places of the warp's next 32 tokens, one to a lane (8 + 8 heads, 16,384 tokens: 22.5
+        // us; 25.0 with one token's loaded ahead)
+        int pos = 0, nth = 0;
         int2 put = make_int2(-1, 0);
         auto ahead = [&](int t) {
-            if (t >= P.T) return;
-            pos = P.pos[t];
-            if (P.k_cache != nullptr) put = where(t);
+            const long long mine = t + (long long)lane * (round ? warps : 1);
+            if (mine < P.T) {
+                pos = P.pos[mine];
+                if (P.k_cache != nullptr) put = where((int)mine);
+            }
+            nth = 0;
         };
         ahead(cs.t);
         // (first, second) -> (first * ff + second * sf, second * ss + first * fs), gains included
@@ -164,9 +170,11 @@ __global__ void __launch_bounds__(kRThreads, 1) qk_rope_kernel(const __grid_cons
         while (cs.left > 0) {
             if (cs.t != token) {
                 token = cs.t;
-                if (P.k_cache != nullptr) at = place(token, put, lane == 0);
-                const unsigned long long turn = S.turns[lane] * (unsigned long long)(long long)pos;
-                ahead(token + (round ? warps : 1));
+                if (nth == 32) ahead(token);
+                if (P.k_cache != nullptr)
+                    at = place(token, make_int2(__shfl_sync(0xffffffffu, put.x, nth), __shfl_sync(0xffffffffu, put.y, nth)), lane == 0);
+                const unsigned long long turn = S.turns[lane] * (unsigned long long)(long long)__shfl_sync(0xffffffffu, pos, nth);
+                ++nth;
                 float sn, cn;
                 sincospif((float)(int)(turn >> 32) * 0x1p-31f, &sn, &cn);
                 __syncwarp();
@@ -285,7 +293,7 @@ __global__ void __launch_bounds__(kRThreads, 1) qk_rope_kernel(const __grid_cons
                 issue(ld, st);
                 ++issued;
             }
-            if (++st == kRStages) {
+            if (++st == depth) {
                 st = 0;
                 parity ^= 1;
             }
@@ -293,7 +301,7 @@ __global__ void __launch_bounds__(kRThreads, 1) qk_rope_kernel(const __grid_cons
         }
         if (failed)                             // loads still in flight
             for (uint32_t n = done; n < issued; ++n)
-                (void)mbar_wait(&full[n % kRStages], (n / kRStages) & 1u, 10000000ull);
+                (void)mbar_wait(&full[n % depth], (n / depth) & 1u, 10000000ull);
     }
     task_end(ctx);
 }

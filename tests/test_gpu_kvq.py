@@ -159,6 +159,40 @@ def test_qk_rope_append_of_many_kv_heads(nkv):
     assert status(x.ws) == sgp.SGP_OK
 
 
+@pytest.mark.parametrize("T,nq,nkv,rot,layout,scaling,norm,far", [
+    (9800, 36, 18, 64, "half", "none", True, 0),
+    (9801, 2, 1, 48, "interleaved", "turns", False, 77),
+    (100003, 1, 1, 64, "half", "none", True, 0)])
+def test_qk_rope_of_many_tokens(T, nq, nkv, rot, layout, scaling, norm, far):
+    """So many that they go round the warps, in the end more than 32 to a warp: into rows, into caches, and in
+    the caches, the last two with tokens that have no place."""
+    x = Rope(T, nq, nkv, rot, layout, scaling, norm, far)
+    qo, ko = (torch.full((T, n * D), NAN, dtype=torch.bfloat16, device="cuda") for n in (nq, nkv))
+    sgp.sgp_qk_rope(x.dims, x.rope, x.gq, x.gk, x.eps, x.pos, x.q, qo, x.k, ko, T, x.ws)
+    some = np.unique(np.r_[0:T:97, T - 40:T])
+    x.pos_list = [x.pos_list[t] for t in some]
+    for name, got, rows, gain in (("q", qo, x.q, x.gq), ("k", ko, x.k, x.gk)):
+        y, err = Q.rope(f64(rows[some]).reshape(len(some), -1, D), x.pos_list, gain=None if gain is None else f64(gain), **x.kw)
+        within(name, got[some].view(y.shape), y, err)
+    n, cap = 7, T // 7 + 1
+    place = np.random.default_rng(T).permutation(n * cap)[:T]
+    lost = np.arange(T) % 11 == 3
+    seq, slot = ints([-1 if no else int(a) for a, no in zip(place // cap, lost)]), ints(place % cap)
+    live = torch.from_numpy(np.flatnonzero(~lost)).cuda()
+    at = seq[live].long(), slot[live].long()
+    kc, vc = (torch.full((n, nkv, cap, D), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    qa = torch.full_like(qo, NAN)
+    sgp.sgp_qk_rope_append(x.dims, x.rope, x.gq, x.gk, x.eps, x.pos, x.q, qa, x.k, x.v, sgp.make_cache(kc, vc), n, seq, slot, T, x.ws)
+    assert torch.equal(qa, qo)
+    assert torch.equal(kc[at[0], :, at[1]].reshape(len(live), -1), ko[live])
+    assert torch.equal(vc[at[0], :, at[1]].reshape(len(live), -1), x.v[live])
+    assert (kc == 5.0).all(3).sum() == (n * cap - len(live)) * nkv
+    before = kc.clone()
+    kc[at[0], :, at[1]] = x.k[live].reshape(len(live), nkv, D)
+    sgp.sgp_qk_rope_append(x.dims, x.rope, None, x.gk, x.eps, x.pos, None, None, None, None, sgp.make_cache(kc, vc), n, seq, slot, T, x.ws)
+    assert torch.equal(kc, before) and status(x.ws) == sgp.SGP_OK
+
+
 def test_qk_rope_append_without_sequences_and_with_bad_places():
     """Token t goes to sequence t; a place out of range is reported, its caches stay, its q is turned."""
     T, nq, nkv, cap = 6, 8, 2, 9
