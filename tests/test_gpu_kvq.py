@@ -193,6 +193,32 @@ def test_qk_rope_of_many_tokens(T, nq, nkv, rot, layout, scaling, norm, far):
     assert torch.equal(kc, before) and status(x.ws) == sgp.SGP_OK
 
 
+@pytest.mark.parametrize("T", [5, 700, 9900])
+@pytest.mark.parametrize("rows_of_k", [False, True])
+@pytest.mark.parametrize("with_q", [False, True])
+@pytest.mark.parametrize("with_v", [False, True])
+def test_qk_rope_append_of_any_parts(T, rows_of_k, with_q, with_v):
+    """q or not, keys from rows or in their slots, values or not: what is there is as with all of them."""
+    nq, nkv, n = 6, 3, 5
+    cap = T // n + 2
+    x = Rope(T, nq, nkv, 32, "interleaved", "none", True, 5)
+    place = np.random.default_rng(T).permutation(n * cap)[:T]
+    seq, slot = ints(place // cap), ints(place % cap)
+    at = seq.long(), slot.long()
+    caches = [torch.full((n, nkv, cap, D), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    qo, qa = (torch.full((T, nq * D), NAN, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    sgp.sgp_qk_rope_append(x.dims, x.rope, x.gq, x.gk, x.eps, x.pos, x.q, qo, x.k, x.v, sgp.make_cache(*caches[:2]), n, seq, slot, T, x.ws)
+    x.check("q", qo, x.q, x.gq)
+    if not rows_of_k:
+        caches[2][at[0], :, at[1]] = x.k[:T].reshape(T, nkv, D)
+    sgp.sgp_qk_rope_append(x.dims, x.rope, x.gq, x.gk, x.eps, x.pos, x.q if with_q else None, qa if with_q else None,
+                           x.k if rows_of_k else None, x.v if with_v else None, sgp.make_cache(*caches[2:]), n, seq, slot, T, x.ws)
+    assert torch.equal(caches[2], caches[0])
+    assert torch.equal(caches[3], caches[1]) if with_v else (caches[3] == 5.0).all()
+    assert torch.equal(qa, qo) if with_q else qa.isnan().all()
+    assert status(x.ws) == sgp.SGP_OK
+
+
 def test_qk_rope_append_without_sequences_and_with_bad_places():
     """Token t goes to sequence t; a place out of range is reported, its caches stay, its q is turned."""
     T, nq, nkv, cap = 6, 8, 2, 9
